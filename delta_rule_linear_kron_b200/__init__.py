@@ -20,7 +20,10 @@ __all__ = ["fwd", "bwd", "decode", "fwd_gated", "bwd_gated", "fwd_fused", "bwd_f
            "gdn2_fwd", "gdn2_bwd", "gdn2_decode",
            "workspace_size", "device_status", "library_path",
            "KronDeltaError", "KronDeltaFunction", "PrologueFunction", "EpilogueFunction", "Gdn2Function",
-           "KD_WS_FWD", "KD_WS_FWD_SAVE", "KD_WS_BWD"]
+           "KD_WS_FWD", "KD_WS_FWD_SAVE", "KD_WS_BWD",
+           "rotary_fwd", "rotary_bwd", "rotary_freqs", "swa_fwd", "swa_bwd", "swa_decode", "swa_fill",
+           "swa_workspace_size", "glr_fwd", "glr_bwd", "glr_decode", "glr_workspace_size",
+           "RotaryFunction", "SwaFunction", "GlrFunction"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libkron_delta.so")
@@ -99,6 +102,27 @@ def lib():
         L.kron_delta_gdn2_bwd.argtypes = [vp] * 16 + [i] * 6 + [vp, sz, vp, sz, vp]
         L.kron_delta_gdn2_decode.restype = i
         L.kron_delta_gdn2_decode.argtypes = [vp] * 8 + [i] * 5 + [vp]
+        ll, f = ctypes.c_void_p, ctypes.c_float  # positions and lengths are device arrays
+        L.kron_delta_rotary.restype = i
+        L.kron_delta_rotary.argtypes = [vp, vp, vp, ll, vp, vp] + [i] * 8 + [f, i, vp]
+        L.kron_delta_swa_workspace_size.restype = sz
+        L.kron_delta_swa_workspace_size.argtypes = [i] * 9
+        L.kron_delta_swa_fwd.restype = i
+        L.kron_delta_swa_fwd.argtypes = [vp] * 4 + [fp] + [i] * 7 + [f, i, vp, sz, i, vp]
+        L.kron_delta_swa_bwd.restype = i
+        L.kron_delta_swa_bwd.argtypes = [vp] * 9 + [i] * 7 + [f, i, vp, sz, vp, sz, vp]
+        L.kron_delta_swa_decode.restype = i
+        L.kron_delta_swa_decode.argtypes = [vp] * 5 + [ll, vp] + [i] * 6 + [f, i, vp, sz, vp]
+        L.kron_delta_swa_fill.restype = i
+        L.kron_delta_swa_fill.argtypes = [vp, vp, ll, vp, vp] + [i] * 7 + [vp]
+        L.kron_delta_glr_workspace_size.restype = sz
+        L.kron_delta_glr_workspace_size.argtypes = [i] * 5
+        L.kron_delta_glr_fwd.restype = i
+        L.kron_delta_glr_fwd.argtypes = [vp] * 7 + [i] * 4 + [vp, sz, i, vp]
+        L.kron_delta_glr_bwd.restype = i
+        L.kron_delta_glr_bwd.argtypes = [vp] * 11 + [i] * 4 + [vp, sz, vp, sz, vp]
+        L.kron_delta_glr_decode.restype = i
+        L.kron_delta_glr_decode.argtypes = [vp] * 6 + [i] * 3 + [vp]
         L.kron_delta_selftest_timeout.restype = i
         L.kron_delta_selftest_timeout.argtypes = [vp]
         L.kron_delta_profile_enable.restype = None
@@ -648,8 +672,15 @@ def _make_gdn2_function():
     return Gdn2Function
 
 
+from . import hybrid as _hybrid  # noqa: E402  (it takes the helpers above)
+from .hybrid import (rotary_fwd, rotary_bwd, rotary_freqs, swa_fwd, swa_bwd, swa_decode, swa_fill,  # noqa: E402
+                     swa_workspace_size, glr_fwd, glr_bwd, glr_decode, glr_workspace_size, KD_SWA_WS_SAVE,
+                     KD_SWA_WS_BWD, KD_SWA_WS_DECODE, KD_GLR_WS_SAVE, KD_GLR_WS_BWD, KD_SWA_MAX_SINKS)
+
 _LAZY = {"KronDeltaFunction": _make_function, "PrologueFunction": _make_prologue_function,
-         "EpilogueFunction": _make_epilogue_function, "Gdn2Function": _make_gdn2_function}
+         "EpilogueFunction": _make_epilogue_function, "Gdn2Function": _make_gdn2_function,
+         "RotaryFunction": _hybrid.make_rotary_function, "SwaFunction": _hybrid.make_swa_function,
+         "GlrFunction": _hybrid.make_glr_function}
 
 
 def __getattr__(name):

@@ -6,6 +6,7 @@
 // synchronising.  Declarations and argument contracts: include/kron_delta.h.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -16,6 +17,7 @@
 #include <vector>
 
 #include "../../include/kron_delta.h"
+#include "kd_hybrid.h"
 #include "kd_kernels.h"
 
 namespace {
@@ -196,7 +198,14 @@ int check_stream(void* stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(KD_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
 #if CUDART_VERSION >= 12080
+  // a stream that is being captured into a graph does not answer this question
+  // (asking would end the capture)
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (stream) {
+    e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cap);
+    if (e != cudaSuccess) return fail(KD_ERR_INVALID_ARG, "invalid stream: %s", cudaGetErrorString(e));
+  }
+  if (stream && cap == cudaStreamCaptureStatusNone) {
     int sdev = -1;
     e = cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev);
     if (e != cudaSuccess) return fail(KD_ERR_INVALID_ARG, "invalid stream: %s", cudaGetErrorString(e));
@@ -312,7 +321,7 @@ void prof_end(cudaStream_t st) {
 
 extern "C" {
 
-int kron_delta_version(void) { return 200; }
+int kron_delta_version(void) { return 210; }
 
 const char* kron_delta_last_error(void) { return g_err.c_str(); }
 
@@ -935,6 +944,287 @@ int kron_delta_gdn2_decode(const void* q, const void* k, const void* v, const fl
   KD_TRY(check_stream(stream));
   kd::GdnDecodeArgs a{q, k, v, b, w, loga, S, out, B, H, dk, dv, dtype};
   return launched(kd::launch_gdn2_decode(a, static_cast<cudaStream_t>(stream)), "gdn2 decode launch");
+}
+
+// ---- hybrid stacks: rotary positions, sliding-window attention, the gated
+// ---- linear recurrence ------------------------------------------------------
+namespace {
+
+int check_dtype(int dtype) {
+  if (dtype != KD_F32 && dtype != KD_BF16) return fail(KD_ERR_UNSUPPORTED, "dtype must be KD_F32 or KD_BF16 (got %d)", dtype);
+  return KD_OK;
+}
+
+int check_ptr8(const void* p, const char* name, bool required) {
+  if (!p) return required ? fail(KD_ERR_INVALID_ARG, "%s must not be NULL", name) : KD_OK;
+  if (!aligned(p, 8)) return fail(KD_ERR_INVALID_ARG, "%s must be 8-byte aligned", name);
+  return KD_OK;
+}
+
+// An output may be its input (in place) but not overlap it otherwise.
+int check_in_place(const void* in, const void* out, size_t bytes, const char* name) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+  if (a != b && a < b + bytes && b < a + bytes)
+    return fail(KD_ERR_INVALID_ARG, "%s overlaps its input (only exactly in place is allowed)", name);
+  return KD_OK;
+}
+
+int check_swa(int B, int T, int H, int Hk, int d, int window, int sinks, int dtype) {
+  if (B <= 0 || T <= 0 || H <= 0 || Hk <= 0)
+    return fail(KD_ERR_INVALID_ARG, "B, T, H, Hk must be >= 1 (got %d, %d, %d, %d)", B, T, H, Hk);
+  if (B > 65535 || H > 65535) return fail(KD_ERR_INVALID_ARG, "B and H must be <= 65535 (got %d, %d)", B, H);
+  if (H % Hk) return fail(KD_ERR_INVALID_ARG, "H must be a multiple of Hk (got %d, %d)", H, Hk);
+  if (!dim_supported(d)) return fail(KD_ERR_UNSUPPORTED, "d must be 32, 64 or 128 (got %d)", d);
+  if (window <= 0) return fail(KD_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
+  if (sinks < 0) return fail(KD_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", sinks);
+  if (sinks > KD_SWA_MAX_SINKS)
+    return fail(KD_ERR_UNSUPPORTED, "sinks must be <= %d (got %d)", KD_SWA_MAX_SINKS, sinks);
+  // positions behind the last one are formed in 32 bits
+  if (T > (1 << 30) || window > 0x7fffffff - KD_SWA_MAX_SINKS)
+    return fail(KD_ERR_INVALID_ARG, "T must be <= 2^30 and window < 2^31 - %d (got %d, %d)", KD_SWA_MAX_SINKS, T, window);
+  return check_dtype(dtype);
+}
+
+int check_scale(float scale) {
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KD_ERR_INVALID_ARG, "scale must be finite and > 0 (got %g)", (double)scale);
+  return KD_OK;
+}
+
+// A window beyond the sequence is the sequence, and so are more first tokens than it has.
+int clamp_to(int x, int T) { return x < T ? x : T; }
+
+size_t swa_save_bytes(int B, int T, int H, int d, int dtype) { return dtype == KD_BF16 ? (size_t)B * T * H * d * 2 : 0; }
+
+int check_ws(const void* ws, size_t bytes, size_t need, const char* what) {
+  if (need == 0) return KD_OK;
+  if (!ws || bytes < need)
+    return fail(KD_ERR_WORKSPACE, "%s of %zu bytes needed (got %zu)", what, need, ws ? bytes : (size_t)0);
+  if (!aligned(ws, 256)) return fail(KD_ERR_WORKSPACE, "workspaces must be 256-byte aligned");
+  return KD_OK;
+}
+
+int check_glr(int B, int T, int D, int dtype) {
+  if (B <= 0 || T <= 0 || D <= 0) return fail(KD_ERR_INVALID_ARG, "B, T, D must be >= 1 (got %d, %d, %d)", B, T, D);
+  if (B > 65535) return fail(KD_ERR_INVALID_ARG, "B must be <= 65535 (got %d)", B);
+  if (D % 8) return fail(KD_ERR_UNSUPPORTED, "D must be a multiple of 8 (got %d)", D);
+  if (T > (1 << 30) || D > (1 << 27)) return fail(KD_ERR_INVALID_ARG, "T must be <= 2^30 and D <= 2^27 (got %d, %d)", T, D);
+  return check_dtype(dtype);
+}
+size_t glr_chunks(int T) { return ((size_t)T + kd::kChunk - 1) / kd::kChunk; }
+size_t glr_save_bytes(int B, int T, int D) { return (size_t)B * glr_chunks(T) * D * sizeof(float); }
+size_t glr_bwd_bytes(int B, int D) { return (size_t)B * kd::kGlrMaxCluster * D * sizeof(float); }
+
+}  // namespace
+
+int kron_delta_rotary(const void* q, const void* k, const double* freqs, const long long* pos, void* q_out,
+                      void* k_out, int B, int T, int H, int Hk, int d, int rot, int interleaved, int inverse,
+                      float scale, int dtype, void* stream) {
+  if (B <= 0 || T <= 0 || H <= 0) return fail(KD_ERR_INVALID_ARG, "B, T, H must be >= 1 (got %d, %d, %d)", B, T, H);
+  if (Hk < 0 || (Hk > 0) != (k != nullptr))
+    return fail(KD_ERR_INVALID_ARG, "Hk must be >= 1 with k, and 0 without (got %d)", Hk);
+  if (H > 65535 || Hk > 65535) return fail(KD_ERR_INVALID_ARG, "H and Hk must be <= 65535 (got %d, %d)", H, Hk);
+  if (!dim_supported(d)) return fail(KD_ERR_UNSUPPORTED, "d must be 32, 64 or 128 (got %d)", d);
+  if (rot < 2 || rot > d || rot % 2) return fail(KD_ERR_INVALID_ARG, "rot must be even and in 2 .. d (got %d)", rot);
+  if (interleaved < 0 || interleaved > 1 || inverse < 0 || inverse > 1)
+    return fail(KD_ERR_INVALID_ARG, "interleaved and inverse must be 0 or 1 (got %d, %d)", interleaved, inverse);
+  if (!std::isfinite(scale)) return fail(KD_ERR_INVALID_ARG, "scale must be finite");
+  if ((size_t)B * T > 0x7fffffffu) return fail(KD_ERR_INVALID_ARG, "B*T too large (%d, %d)", B, T);
+  KD_TRY(check_dtype(dtype));
+  KD_TRY(check_ptr(q, "q", true));
+  KD_TRY(check_ptr(k, "k", Hk > 0));
+  KD_TRY(check_ptr8(freqs, "freqs", true));
+  KD_TRY(check_ptr8(pos, "pos", false));
+  KD_TRY(check_ptr(q_out, "q_out", true));
+  KD_TRY(check_ptr(k_out, "k_out", Hk > 0));
+  const size_t row = (size_t)B * T * d * (dtype == KD_BF16 ? 2 : 4);
+  KD_TRY(check_in_place(q, q_out, row * H, "q_out"));
+  if (Hk > 0) KD_TRY(check_in_place(k, k_out, row * Hk, "k_out"));
+  KD_TRY(check_stream(stream));
+  kd::RotaryArgs a{};
+  a.x[0] = q; a.x[1] = k; a.y[0] = q_out; a.y[1] = k_out; a.heads[0] = H; a.heads[1] = Hk;
+  a.freqs = freqs; a.pos = pos; a.rows = (long long)B * T; a.T = T; a.d = d; a.rot = rot;
+  a.interleaved = interleaved; a.inverse = inverse; a.dtype = dtype; a.scale = scale;
+  return launched(kd::launch_rotary(a, static_cast<cudaStream_t>(stream)), "rotary launch");
+}
+
+size_t kron_delta_swa_workspace_size(int kind, int B, int T, int H, int Hk, int d, int window, int sinks, int dtype) {
+  if (check_swa(B, kind == KD_SWA_WS_DECODE ? 1 : T, H, Hk, d, window, sinks, dtype) != KD_OK) return 0;
+  switch (kind) {
+    case KD_SWA_WS_SAVE: ok(); return swa_save_bytes(B, T, H, d, dtype);
+    case KD_SWA_WS_BWD: ok(); return kd::swa_bwd_layout(B, T, H, Hk, d, clamp_to(window, T), clamp_to(sinks, T)).bytes;
+    case KD_SWA_WS_DECODE:
+      ok();
+      return kd::swa_decode_bytes(B, H, d, kd::swa_decode_splits(B, H, Hk, d, window, sinks, dtype));
+    default: fail(KD_ERR_INVALID_ARG, "unknown workspace kind %d", kind); return 0;
+  }
+}
+
+int kron_delta_swa_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int B, int T, int H,
+                       int Hk, int d, int window, int sinks, float scale, int dtype, void* workspace,
+                       size_t ws_bytes, int save, void* stream) {
+  KD_TRY(check_swa(B, T, H, Hk, d, window, sinks, dtype));
+  KD_TRY(check_scale(scale));
+  KD_TRY(check_ptr(q, "q", true));
+  KD_TRY(check_ptr(k, "k", true));
+  KD_TRY(check_ptr(v, "v", true));
+  KD_TRY(check_ptr(out, "out", true));
+  KD_TRY(check_ptr(lse, "lse", true));
+  if (save != 0 && save != 1) return fail(KD_ERR_INVALID_ARG, "save must be 0 or 1 (got %d)", save);
+  const size_t need = save ? swa_save_bytes(B, T, H, d, dtype) : 0;
+  KD_TRY(check_ws(workspace, ws_bytes, need, "workspace"));
+  KD_TRY(check_stream(stream));
+  kd::SwaArgs a{};
+  a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.olo = need ? workspace : nullptr;
+  a.B = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.window = clamp_to(window, T); a.sinks = clamp_to(sinks, T);
+  a.dtype = dtype; a.scale = scale;
+  DeviceInfo di;
+  KD_TRY(device_info(&di));
+  a.err = di.err; a.sms = di.sms;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launched(kd::swa_tc_supported(d, dtype) ? kd::launch_swa_fwd_tc(a, st) : kd::launch_swa_fwd_simt(a, st),
+                  "swa forward launch");
+}
+
+int kron_delta_swa_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                       const void* dO, void* dq, void* dk, void* dv, int B, int T, int H, int Hk, int d, int window,
+                       int sinks, float scale, int dtype, const void* fwd_ws, size_t fwd_ws_bytes, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  KD_TRY(check_swa(B, T, H, Hk, d, window, sinks, dtype));
+  KD_TRY(check_scale(scale));
+  KD_TRY(check_ptr(q, "q", true));
+  KD_TRY(check_ptr(k, "k", true));
+  KD_TRY(check_ptr(v, "v", true));
+  KD_TRY(check_ptr(out, "out", true));
+  KD_TRY(check_ptr(lse, "lse", true));
+  KD_TRY(check_ptr(dO, "dO", true));
+  KD_TRY(check_ptr(dq, "dq", true));
+  KD_TRY(check_ptr(dk, "dk", true));
+  KD_TRY(check_ptr(dv, "dv", true));
+  const size_t saved = swa_save_bytes(B, T, H, d, dtype);
+  KD_TRY(check_ws(fwd_ws, fwd_ws_bytes, saved, "the forward's workspace (save=1)"));
+  const kd::SwaBwdLayout L = kd::swa_bwd_layout(B, T, H, Hk, d, clamp_to(window, T), clamp_to(sinks, T));
+  KD_TRY(check_ws(workspace, ws_bytes, L.bytes, "backward workspace"));
+  KD_TRY(check_stream(stream));
+  kd::SwaArgs a{};
+  a.q = q; a.k = k; a.v = v; a.o = out; a.lse_in = lse; a.dO = dO; a.dq = dq; a.dk = dk; a.dv = dv;
+  a.olo_in = saved ? fwd_ws : nullptr; a.ws = static_cast<char*>(workspace);
+  a.B = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.window = clamp_to(window, T); a.sinks = clamp_to(sinks, T);
+  a.dtype = dtype; a.scale = scale;
+  DeviceInfo di;
+  KD_TRY(device_info(&di));
+  a.err = di.err; a.sms = di.sms;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launched(kd::swa_tc_supported(d, dtype) ? kd::launch_swa_bwd_tc(a, st) : kd::launch_swa_bwd_simt(a, st),
+                  "swa backward launch");
+}
+
+int kron_delta_swa_decode(const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                          const long long* pos, void* out, int B, int H, int Hk, int d, int window, int sinks,
+                          float scale, int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  KD_TRY(check_swa(B, 1, H, Hk, d, window, sinks, dtype));
+  KD_TRY(check_scale(scale));
+  KD_TRY(check_ptr(q, "q", true));
+  KD_TRY(check_ptr(k, "k", true));
+  KD_TRY(check_ptr(v, "v", true));
+  KD_TRY(check_ptr(k_cache, "k_cache", true));
+  KD_TRY(check_ptr(v_cache, "v_cache", true));
+  KD_TRY(check_ptr8(pos, "pos", true));
+  KD_TRY(check_ptr(out, "out", true));
+  const int splits = kd::swa_decode_splits(B, H, Hk, d, window, sinks, dtype);
+  KD_TRY(check_ws(workspace, ws_bytes, kd::swa_decode_bytes(B, H, d, splits), "decode workspace"));
+  KD_TRY(check_stream(stream));
+  kd::SwaDecodeArgs a{q, k, v, k_cache, v_cache, pos, out, B, H, Hk, d, window, sinks, dtype, scale,
+                      static_cast<float*>(workspace), splits};
+  return launched(kd::launch_swa_decode(a, static_cast<cudaStream_t>(stream)), "swa decode launch");
+}
+
+int kron_delta_swa_fill(const void* k, const void* v, const long long* lens, void* k_cache, void* v_cache, int B,
+                        int T, int Hk, int d, int window, int sinks, int dtype, void* stream) {
+  KD_TRY(check_swa(B, T, Hk, Hk, d, window, sinks, dtype));
+  KD_TRY(check_ptr(k, "k", true));
+  KD_TRY(check_ptr(v, "v", true));
+  KD_TRY(check_ptr8(lens, "lens", true));
+  KD_TRY(check_ptr(k_cache, "k_cache", true));
+  KD_TRY(check_ptr(v_cache, "v_cache", true));
+  const size_t vectors = ((size_t)window + sinks) * B * Hk * d * (dtype == KD_BF16 ? 2 : 4) / 16;
+  if (vectors / 256 >= 0x7fffffffu) return fail(KD_ERR_INVALID_ARG, "cache too large (%zu vectors)", vectors);
+  KD_TRY(check_stream(stream));
+  kd::SwaFillArgs a{k, v, lens, k_cache, v_cache, B, T, Hk, d, window, sinks, dtype};
+  return launched(kd::launch_swa_fill(a, static_cast<cudaStream_t>(stream)), "swa fill launch");
+}
+
+size_t kron_delta_glr_workspace_size(int kind, int B, int T, int D, int dtype) {
+  if (check_glr(B, T, D, dtype) != KD_OK) return 0;
+  switch (kind) {
+    case KD_GLR_WS_SAVE: ok(); return glr_save_bytes(B, T, D);
+    case KD_GLR_WS_BWD: ok(); return glr_bwd_bytes(B, D);
+    default: fail(KD_ERR_INVALID_ARG, "unknown workspace kind %d", kind); return 0;
+  }
+}
+
+namespace {
+int check_glr_inputs(const void* x, const void* i_pre, const void* f_pre, const float* a_log) {
+  KD_TRY(check_ptr(x, "x", true));
+  KD_TRY(check_ptr(i_pre, "i_pre", true));
+  KD_TRY(check_ptr(f_pre, "f_pre", true));
+  return check_ptr(a_log, "a_log", true);
+}
+}  // namespace
+
+int kron_delta_glr_fwd(const void* x, const void* i_pre, const void* f_pre, const float* a_log, const float* h0,
+                       void* out, float* hT, int B, int T, int D, int dtype, void* workspace, size_t ws_bytes,
+                       int save, void* stream) {
+  KD_TRY(check_glr(B, T, D, dtype));
+  KD_TRY(check_glr_inputs(x, i_pre, f_pre, a_log));
+  KD_TRY(check_ptr(h0, "h0", false));
+  KD_TRY(check_ptr(out, "out", true));
+  KD_TRY(check_ptr(hT, "hT", false));
+  if (save != 0 && save != 1) return fail(KD_ERR_INVALID_ARG, "save must be 0 or 1 (got %d)", save);
+  KD_TRY(check_ws(workspace, ws_bytes, save ? glr_save_bytes(B, T, D) : 0, "workspace"));
+  KD_TRY(check_stream(stream));
+  kd::GlrArgs a{};
+  a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.h0 = h0; a.out = out; a.hT = hT;
+  a.states = save ? static_cast<float*>(workspace) : nullptr;
+  a.B = B; a.T = T; a.D = D; a.dtype = dtype;
+  return launched(kd::launch_glr_fwd(a, static_cast<cudaStream_t>(stream)), "glr forward launch");
+}
+
+int kron_delta_glr_bwd(const void* x, const void* i_pre, const void* f_pre, const float* a_log, const void* dh,
+                       const float* dhT, void* dx, void* di_pre, void* df_pre, float* da_log, float* dh0, int B,
+                       int T, int D, int dtype, const void* fwd_ws, size_t fwd_ws_bytes, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  KD_TRY(check_glr(B, T, D, dtype));
+  KD_TRY(check_glr_inputs(x, i_pre, f_pre, a_log));
+  KD_TRY(check_ptr(dh, "dh", true));
+  KD_TRY(check_ptr(dhT, "dhT", false));
+  KD_TRY(check_ptr(dx, "dx", true));
+  KD_TRY(check_ptr(di_pre, "di_pre", true));
+  KD_TRY(check_ptr(df_pre, "df_pre", true));
+  KD_TRY(check_ptr(da_log, "da_log", true));
+  KD_TRY(check_ptr(dh0, "dh0", false));
+  KD_TRY(check_ws(fwd_ws, fwd_ws_bytes, glr_save_bytes(B, T, D), "the forward's workspace (save=1)"));
+  KD_TRY(check_ws(workspace, ws_bytes, glr_bwd_bytes(B, D), "backward workspace"));
+  KD_TRY(check_stream(stream));
+  kd::GlrArgs a{};
+  a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.dh = dh; a.dhT = dhT;
+  a.dx = dx; a.di_pre = di_pre; a.df_pre = df_pre; a.da_log = da_log; a.dh0 = dh0;
+  a.states_in = static_cast<const float*>(fwd_ws);
+  a.part = static_cast<float*>(workspace);
+  a.B = B; a.T = T; a.D = D; a.dtype = dtype;
+  return launched(kd::launch_glr_bwd(a, static_cast<cudaStream_t>(stream)), "glr backward launch");
+}
+
+int kron_delta_glr_decode(const void* x, const void* i_pre, const void* f_pre, const float* a_log, float* h,
+                          void* out, int B, int D, int dtype, void* stream) {
+  KD_TRY(check_glr(B, 1, D, dtype));
+  KD_TRY(check_glr_inputs(x, i_pre, f_pre, a_log));
+  KD_TRY(check_ptr(h, "h", true));
+  KD_TRY(check_ptr(out, "out", true));
+  KD_TRY(check_stream(stream));
+  kd::GlrArgs a{};
+  a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.hT = h; a.out = out;
+  a.B = B; a.T = 1; a.D = D; a.dtype = dtype;
+  return launched(kd::launch_glr_decode(a, static_cast<cudaStream_t>(stream)), "glr decode launch");
 }
 
 int kron_delta_selftest_timeout(void* stream) {

@@ -1,0 +1,396 @@
+"""Operators that stand beside the delta rules in a hybrid stack (binding over
+the C ABI, like the package's own functions, which re-exports these):
+
+  rotary_fwd, rotary_bwd, rotary_freqs      rotary positions of q and k
+  swa_fwd, swa_bwd, swa_decode, swa_fill    attention over a sliding window
+                                            with first tokens kept
+  glr_fwd, glr_bwd, glr_decode              element-wise gated linear recurrence
+
+Tensors of a call are on one CUDA device, which need not be the current one:
+the call runs on the current stream of the tensors' device, or on `stream`.
+"""
+from __future__ import annotations
+
+import contextlib
+import math
+
+from . import (KD_ERR_INVALID_ARG, KronDeltaError, _alloc_ws, _check, _dtype_code, _need, _ptr, lib)
+
+KD_SWA_WS_SAVE, KD_SWA_WS_BWD, KD_SWA_WS_DECODE = 0, 1, 2
+KD_GLR_WS_SAVE, KD_GLR_WS_BWD = 0, 1
+KD_SWA_MAX_SINKS = 128
+
+__all__ = ["rotary_fwd", "rotary_bwd", "rotary_freqs", "swa_fwd", "swa_bwd", "swa_decode", "swa_fill",
+           "swa_workspace_size", "glr_fwd", "glr_bwd", "glr_decode", "glr_workspace_size",
+           "KD_SWA_WS_SAVE", "KD_SWA_WS_BWD", "KD_SWA_WS_DECODE", "KD_GLR_WS_SAVE", "KD_GLR_WS_BWD",
+           "KD_SWA_MAX_SINKS"]
+
+
+def _invalid(msg):
+    return KronDeltaError(KD_ERR_INVALID_ARG, msg)
+
+
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise _invalid(f"{name} must have {n} dimensions (got shape {tuple(t.shape)})")
+    return t.shape
+
+
+def _call(fn, tensors, stream, *args):
+    """Runs fn(*args, stream) on the device that holds all of `tensors`."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise _invalid(f"tensors on {dev} and {t.device} in one call")
+    other = dev.index != torch.cuda.current_device()
+    with torch.cuda.device(dev) if other else contextlib.nullcontext():
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        _check(fn(*args, s.cuda_stream))
+
+
+def _nbytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _size(n):
+    """A workspace size; 0 is either none needed (no error recorded) or an error."""
+    if n == 0:
+        msg = lib().kron_delta_last_error().decode()
+        if msg:
+            raise _invalid(msg)
+    return n
+
+
+def swa_workspace_size(kind, B, T, H, Hk, d, window, sinks, dtype) -> int:
+    return _size(lib().kron_delta_swa_workspace_size(kind, B, T, H, Hk, d, window, sinks, dtype))
+
+
+def glr_workspace_size(kind, B, T, D, dtype) -> int:
+    return _size(lib().kron_delta_glr_workspace_size(kind, B, T, D, dtype))
+
+
+# ---- rotary positions ---------------------------------------------------------
+
+
+def rotary_freqs(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, trained_len=None, low=1.0, high=32.0,
+                 device="cuda"):
+    """Angular frequencies [rotary_dim/2] (fp64, on `device`) and the factor on
+    the rotated values, for rotary_fwd.  Pair j turns base^(-2j/rotary_dim)
+    radians per position.  scaling, for contexts `factor` times the trained one:
+      "linear"  every frequency divided by factor;
+      "ntk"     base multiplied by factor^(rotary_dim/(rotary_dim-2)): the
+                slowest pair slows by factor, the fastest keeps its pace;
+      "yarn"    pairs that turn more than `high` times over trained_len
+                positions keep their frequency, those below `low` turns are
+                divided by factor, a linear ramp between; the rotated values
+                are scaled by 0.1 ln(factor) + 1."""
+    import torch
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise _invalid(f"rotary_dim must be even and >= 2 (got {rotary_dim})")
+    if not base > 1 or not factor >= 1 or not math.isfinite(base) or not math.isfinite(factor):
+        raise _invalid(f"base must be > 1 and factor >= 1, both finite (got {base}, {factor})")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise _invalid(f"scaling must be None, 'linear', 'ntk' or 'yarn' (got {scaling!r})")
+    if scaling == "ntk":
+        if rotary_dim == 2:
+            raise _invalid("'ntk' scaling needs rotary_dim > 2")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    w = base ** (torch.arange(0, rotary_dim, 2, dtype=torch.float64) / -rotary_dim)
+    scale = 1.0
+    if scaling == "linear":
+        w = w / factor
+    elif scaling == "yarn":
+        if trained_len is None or trained_len < 1 or not low < high:
+            raise _invalid(f"'yarn' scaling needs trained_len >= 1 and low < high (got {trained_len}, {low}, {high})")
+        keep = ((trained_len * w / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        w = w * keep + w / factor * (1 - keep)
+        scale = 0.1 * math.log(factor) + 1.0
+    return w.to(device), scale
+
+
+def _rotary(q, k, freqs, pos, interleaved, scale, inverse, out, stream):
+    import torch
+    step = q.dim() == 3  # one token per sequence: [B,H,d], pos [B]
+    if not step:
+        _dims(q, "q", 4)
+    B, T = q.shape[0], 1 if step else q.shape[1]
+    H, d = q.shape[-2:]
+    lead = tuple(q.shape[:-2])
+    _need(q, "q")
+    Hk = 0
+    if k is not None:
+        _dims(k, "k", q.dim())
+        Hk = k.shape[-2]
+        _need(k, "k", q.dtype, (*lead, Hk, d))
+    _dims(freqs, "freqs", 1)
+    _need(freqs, "freqs", torch.float64)
+    _need(pos, "pos", torch.int64, lead)
+    dt = _dtype_code(q)
+    oq, ok = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
+    _need(oq, "out[0]", q.dtype, q.shape)
+    if (ok is None) != (k is None):
+        raise _invalid("out must be a pair like (q, k)")
+    if k is not None:
+        _need(ok, "out[1]", q.dtype, k.shape)
+    _call(lib().kron_delta_rotary, (q, k, freqs, pos, oq, ok), stream, _ptr(q), _ptr(k), _ptr(freqs), _ptr(pos),
+          _ptr(oq), _ptr(ok), B, T, H, Hk, d, 2 * freqs.shape[0], int(bool(interleaved)), inverse, float(scale), dt)
+    return oq, ok
+
+
+def rotary_fwd(q, k, freqs, pos=None, *, interleaved=False, scale=1.0, out=None, stream=None):
+    """Rotary positions: pair j of the first 2*len(freqs) channels turns by
+    pos*freqs[j] and is scaled by `scale`; the other channels are copied.
+    q [B,T,H,d], k [B,T,Hk,d] or None (bf16 or fp32); freqs fp64; pos [B,T] int64
+    or None for 0..T-1.  One token per sequence: q [B,H,d], k [B,Hk,d], pos [B].
+    Pair j is channels (j, j + len(freqs)), or (2j, 2j+1) with interleaved.
+    out=(q, k) works in place.  Returns (q, k) rotated."""
+    return _rotary(q, k, freqs, pos, interleaved, scale, 0, out, stream)
+
+
+def rotary_bwd(dq, dk, freqs, pos=None, *, interleaved=False, scale=1.0, out=None, stream=None):
+    """Backward of rotary_fwd: the gradients of q and k from those of its
+    outputs (the rotation by -pos*freqs[j])."""
+    return _rotary(dq, dk, freqs, pos, interleaved, scale, 1, out, stream)
+
+
+# ---- attention over a sliding window with first tokens kept -----------------
+
+
+def _swa_inputs(q, k, v):
+    B, T, H, d = _dims(q, "q", 4)
+    Hk = _dims(k, "k", 4)[2]
+    _need(q, "q"); _need(k, "k", q.dtype, (B, T, Hk, d)); _need(v, "v", q.dtype, (B, T, Hk, d))
+    return B, T, H, Hk, d, _dtype_code(q)
+
+
+def _scale(scale, d):
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+
+def swa_fwd(q, k, v, window, sinks=0, *, scale=None, out=None, save=False, workspace=None, stream=None):
+    """Causal attention where query t sees key j when j <= t and (t - j < window
+    or j < sinks).  q [B,T,H,d], k, v [B,T,Hk,d] (bf16 or fp32), H a multiple of
+    Hk; scale defaults to 1/sqrt(d).  Returns (out [B,T,H,d], lse [B,T,H] fp32,
+    workspace or None); pass all three (save=True) to swa_bwd."""
+    import torch
+    B, T, H, Hk, d, dt = _swa_inputs(q, k, v)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", q.dtype, q.shape)
+    lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+    if save and workspace is None:
+        n = swa_workspace_size(KD_SWA_WS_SAVE, B, T, H, Hk, d, window, sinks, dt)
+        workspace = _alloc_ws(n, q.device) if n else None
+    _call(lib().kron_delta_swa_fwd, (q, k, v, out, workspace), stream, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+          B, T, H, Hk, d, window, sinks, _scale(scale, d), dt, _ptr(workspace), _nbytes(workspace), int(bool(save)))
+    return out, lse, workspace
+
+
+def swa_bwd(q, k, v, out, lse, dO, window, sinks=0, *, scale=None, fwd_workspace, workspace=None, stream=None):
+    """Backward of swa_fwd for the loss <dO, out>, from its three results.
+    Returns dict dq, dk, dv (summed in a fixed order: bitwise reproducible)."""
+    import torch
+    B, T, H, Hk, d, dt = _swa_inputs(q, k, v)
+    _need(out, "out", q.dtype, q.shape); _need(dO, "dO", q.dtype, q.shape)
+    _need(lse, "lse", torch.float32, (B, T, H))
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
+    if workspace is None:
+        workspace = _alloc_ws(swa_workspace_size(KD_SWA_WS_BWD, B, T, H, Hk, d, window, sinks, dt), q.device)
+    _call(lib().kron_delta_swa_bwd, (q, k, v, out, lse, dO, fwd_workspace, workspace), stream, _ptr(q), _ptr(k),
+          _ptr(v), _ptr(out), _ptr(lse), _ptr(dO), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), B, T, H, Hk, d,
+          window, sinks, _scale(scale, d), dt, _ptr(fwd_workspace), _nbytes(fwd_workspace), _ptr(workspace),
+          _nbytes(workspace))
+    return g
+
+
+def _swa_cache(cache, name, B, slots, Hk, d, dtype):
+    _need(cache, name, dtype, (B, slots, Hk, d))
+
+
+def swa_decode(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, out=None, workspace=None,
+               stream=None):
+    """One decode step of swa_fwd's attention.  q [B,H,d], k, v [B,Hk,d]: the new
+    tokens, at positions pos [B] int64 (pos < 0: the sequence is idle, its cache
+    stays and its out is zero); k_cache, v_cache [B,sinks+window,Hk,d], updated
+    in place.  Position p lives in slot p (p < sinks) or
+    sinks + (p - sinks) % window; see swa_fill for the start after a prefill.
+    Returns out [B,H,d]."""
+    import torch
+    B, H, d = _dims(q, "q", 3)
+    Hk = _dims(k, "k", 3)[1]
+    _need(q, "q"); _need(k, "k", q.dtype, (B, Hk, d)); _need(v, "v", q.dtype, (B, Hk, d))
+    _swa_cache(k_cache, "k_cache", B, sinks + window, Hk, d, q.dtype)
+    _swa_cache(v_cache, "v_cache", B, sinks + window, Hk, d, q.dtype)
+    _need(pos, "pos", torch.int64, (B,))
+    dt = _dtype_code(q)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", q.dtype, (B, H, d))
+    if workspace is None:
+        n = swa_workspace_size(KD_SWA_WS_DECODE, B, 1, H, Hk, d, window, sinks, dt)
+        workspace = _alloc_ws(n, q.device) if n else None
+    _call(lib().kron_delta_swa_decode, (q, k, v, k_cache, v_cache, pos, out, workspace), stream, _ptr(q), _ptr(k),
+          _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(out), B, H, Hk, d, window, sinks,
+          _scale(scale, d), dt, _ptr(workspace), _nbytes(workspace))
+    return out
+
+
+def swa_fill(k, v, lens, k_cache, v_cache, window, sinks=0, *, stream=None):
+    """Fills swa_decode's caches from a prefill's k, v [B,T,Hk,d]: of sequence
+    b's first lens[b] tokens (int64), the first `sinks` and the last `window` go
+    to their slots; the other slots stay as they were."""
+    import torch
+    B, T, Hk, d = _dims(k, "k", 4)
+    _need(k, "k"); _need(v, "v", k.dtype, k.shape); _need(lens, "lens", torch.int64, (B,))
+    _swa_cache(k_cache, "k_cache", B, sinks + window, Hk, d, k.dtype)
+    _swa_cache(v_cache, "v_cache", B, sinks + window, Hk, d, k.dtype)
+    _call(lib().kron_delta_swa_fill, (k, v, lens, k_cache, v_cache), stream, _ptr(k), _ptr(v), _ptr(lens),
+          _ptr(k_cache), _ptr(v_cache), B, T, Hk, d, window, sinks, _dtype_code(k))
+
+
+# ---- gated linear recurrence --------------------------------------------------
+
+
+def _glr_inputs(x, i_pre, f_pre, a_log, h0, n):
+    import torch
+    shape = _dims(x, "x", n)
+    B, D = shape[0], shape[-1]
+    _need(x, "x"); _need(i_pre, "i_pre", x.dtype, shape); _need(f_pre, "f_pre", x.dtype, shape)
+    _need(a_log, "a_log", torch.float32, (D,)); _need(h0, "h0", torch.float32, (B, D))
+    return B, D, _dtype_code(x)
+
+
+def glr_fwd(x, i_pre, f_pre, a_log, h0=None, *, out=None, want_state=True, save=False, workspace=None, stream=None):
+    """Gated linear recurrence per channel: f = sigmoid(f_pre)^exp(a_log),
+    h_t = f h_{t-1} + sqrt(1 - f^2) sigmoid(i_pre) x.  x, i_pre, f_pre [B,T,D]
+    (bf16 or fp32, D a multiple of 8); a_log [D] fp32; h0 [B,D] fp32 or None.
+    f_pre = -inf starts a new sequence at that token.  Returns (out [B,T,D] = h,
+    hT [B,D] fp32 or None, workspace or None); pass the workspace (save=True) to
+    glr_bwd."""
+    import torch
+    B, D, dt = _glr_inputs(x, i_pre, f_pre, a_log, h0, 3)
+    T = x.shape[1]
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", x.dtype, x.shape)
+    hT = torch.empty((B, D), dtype=torch.float32, device=x.device) if want_state else None
+    if save and workspace is None:
+        workspace = _alloc_ws(glr_workspace_size(KD_GLR_WS_SAVE, B, T, D, dt), x.device)
+    _call(lib().kron_delta_glr_fwd, (x, i_pre, f_pre, a_log, h0, out, workspace), stream, _ptr(x), _ptr(i_pre),
+          _ptr(f_pre), _ptr(a_log), _ptr(h0), _ptr(out), _ptr(hT), B, T, D, dt, _ptr(workspace), _nbytes(workspace),
+          int(bool(save)))
+    return out, hT, workspace
+
+
+def glr_bwd(x, i_pre, f_pre, a_log, h0, dh, dhT=None, *, fwd_workspace, workspace=None, want_dh0=True, stream=None):
+    """Backward of glr_fwd for the loss <dh, out> + <dhT, hT>, reading what
+    glr_fwd(save=True) left in fwd_workspace.  Returns dict dx, di_pre, df_pre
+    (x's dtype), da_log [D] fp32 (fixed-order sum), dh0."""
+    import torch
+    B, D, dt = _glr_inputs(x, i_pre, f_pre, a_log, h0, 3)
+    T = x.shape[1]
+    _need(dh, "dh", x.dtype, x.shape); _need(dhT, "dhT", torch.float32, (B, D))
+    g = dict(dx=torch.empty_like(x), di_pre=torch.empty_like(x), df_pre=torch.empty_like(x),
+             da_log=torch.empty_like(a_log),
+             dh0=torch.empty((B, D), dtype=torch.float32, device=x.device) if want_dh0 else None)
+    if workspace is None:
+        workspace = _alloc_ws(glr_workspace_size(KD_GLR_WS_BWD, B, T, D, dt), x.device)
+    _call(lib().kron_delta_glr_bwd, (x, i_pre, f_pre, a_log, dh, dhT, fwd_workspace, workspace), stream, _ptr(x),
+          _ptr(i_pre), _ptr(f_pre), _ptr(a_log), _ptr(dh), _ptr(dhT), _ptr(g["dx"]), _ptr(g["di_pre"]),
+          _ptr(g["df_pre"]), _ptr(g["da_log"]), _ptr(g["dh0"]), B, T, D, dt, _ptr(fwd_workspace),
+          _nbytes(fwd_workspace), _ptr(workspace), _nbytes(workspace))
+    return g
+
+
+def glr_decode(x, i_pre, f_pre, a_log, h, *, out=None, stream=None):
+    """One decode step of the gated linear recurrence.  x, i_pre, f_pre [B,D];
+    a_log [D] fp32; h [B,D] fp32 (updated in place).  Returns out [B,D]."""
+    import torch
+    B, D, dt = _glr_inputs(x, i_pre, f_pre, a_log, h, 2)
+    if h is None:
+        raise _invalid("h must be given")
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", x.dtype, x.shape)
+    _call(lib().kron_delta_glr_decode, (x, i_pre, f_pre, a_log, h, out), stream, _ptr(x), _ptr(i_pre), _ptr(f_pre),
+          _ptr(a_log), _ptr(h), _ptr(out), B, D, dt)
+    return out
+
+
+# ---- autograd ------------------------------------------------------------------
+
+
+def make_rotary_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class RotaryFunction(torch.autograd.Function):
+        """autograd wrapper of rotary_fwd / rotary_bwd.  apply(q, k, freqs, pos,
+        interleaved, scale) -> (q, k); q and k are not changed."""
+
+        @staticmethod
+        def forward(ctx, q, k, freqs, pos=None, interleaved=False, scale=1.0):
+            ctx.save_for_backward(freqs, pos)
+            ctx.how = dict(interleaved=interleaved, scale=scale)
+            return rotary_fwd(q, k, freqs, pos, **ctx.how)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dq, dk):
+            freqs, pos = ctx.saved_tensors
+            dq, dk = rotary_bwd(dq.contiguous(), dk.contiguous(), freqs, pos, **ctx.how)
+            return dq, dk, None, None, None, None
+
+    return RotaryFunction
+
+
+def make_swa_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class SwaFunction(torch.autograd.Function):
+        """autograd wrapper of swa_fwd / swa_bwd.  apply(q, k, v, window, sinks,
+        scale) -> out."""
+
+        @staticmethod
+        def forward(ctx, q, k, v, window, sinks=0, scale=None):
+            out, lse, ws = swa_fwd(q, k, v, window, sinks, scale=scale, save=True)
+            ctx.save_for_backward(q, k, v, out, lse, ws)
+            ctx.how = (window, sinks, scale)
+            return out
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dO):
+            q, k, v, out, lse, ws = ctx.saved_tensors
+            window, sinks, scale = ctx.how
+            g = swa_bwd(q, k, v, out, lse, dO.contiguous(), window, sinks, scale=scale, fwd_workspace=ws)
+            return g["dq"], g["dk"], g["dv"], None, None, None
+
+    return SwaFunction
+
+
+def make_glr_function():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class GlrFunction(torch.autograd.Function):
+        """autograd wrapper of glr_fwd / glr_bwd.  apply(x, i_pre, f_pre, a_log,
+        h0) -> (out, hT)."""
+
+        @staticmethod
+        def forward(ctx, x, i_pre, f_pre, a_log, h0=None):
+            out, hT, ws = glr_fwd(x, i_pre, f_pre, a_log, h0, save=True)
+            ctx.save_for_backward(x, i_pre, f_pre, a_log, h0, ws)
+            return out, hT
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dh, dhT):
+            x, i_pre, f_pre, a_log, h0, ws = ctx.saved_tensors
+            g = glr_bwd(x, i_pre, f_pre, a_log, h0, dh.contiguous(), dhT.contiguous(), fwd_workspace=ws,
+                        want_dh0=h0 is not None)
+            return g["dx"], g["di_pre"], g["df_pre"], g["da_log"], g["dh0"]
+
+    return GlrFunction

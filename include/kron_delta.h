@@ -35,7 +35,14 @@
  *                         log-decay), kron_delta_epilogue_fwd / _bwd
  *                         (per-head RMSNorm and output gate)
  *   Gated DeltaNet-2      kron_delta_gdn2_fwd / _bwd / _decode
- *   support               kron_delta_workspace_size, kron_delta_device_status,
+ *   hybrid stacks         kron_delta_swa_fwd / _bwd / _decode / _fill (attention
+ *                         over a sliding window with first tokens kept),
+ *                         kron_delta_rotary (rotary positions and their
+ *                         backward), kron_delta_glr_fwd / _bwd / _decode
+ *                         (element-wise gated linear recurrence)
+ *   support               kron_delta_workspace_size,
+ *                         kron_delta_swa_workspace_size,
+ *                         kron_delta_glr_workspace_size, kron_delta_device_status,
  *                         kron_delta_selftest_timeout, kron_delta_last_error,
  *                         kron_delta_version, kron_delta_profile_enable /
  *                         _report
@@ -488,6 +495,169 @@ KD_API int kron_delta_gdn2_bwd(const void *q, const void *k, const void *v, cons
 KD_API int kron_delta_gdn2_decode(const void *q, const void *k, const void *v, const float *b,
                                   const float *w, const float *loga, float *S, void *out, int B,
                                   int H, int dk, int dv, int dtype, void *stream);
+
+/* workspace kinds for kron_delta_swa_workspace_size */
+#define KD_SWA_WS_SAVE 0    /* kept by kron_delta_swa_fwd (save = 1) for kron_delta_swa_bwd */
+#define KD_SWA_WS_BWD 1     /* scratch of kron_delta_swa_bwd */
+#define KD_SWA_WS_DECODE 2  /* scratch of kron_delta_swa_decode */
+
+/* workspace kinds for kron_delta_glr_workspace_size */
+#define KD_GLR_WS_SAVE 0    /* kept by kron_delta_glr_fwd (save = 1) for kron_delta_glr_bwd */
+#define KD_GLR_WS_BWD 1     /* scratch of kron_delta_glr_bwd */
+
+/* largest number of first tokens that stay visible */
+#define KD_SWA_MAX_SINKS 128
+
+/*
+ * Rotary positions: pairs of channels of q and k turn by an angle that grows
+ * with the token's position.  For pair j < rot/2 of a token at position p,
+ * with theta = p * freqs[j]:
+ *     (y1, y2) = scale * (x1 cos theta - x2 sin theta, x1 sin theta + x2 cos theta)
+ * The angle is formed and reduced in 64 bits, so far positions keep their
+ * precision.  Channels rot .. d-1 are copied.
+ *   q, q_out : [B,T,H,d] (dtype).  k, k_out : [B,T,Hk,d] (dtype), or NULL with
+ *         Hk = 0.  q_out = q and k_out = k (in place) are allowed; any other
+ *         overlap is not.
+ *   freqs : [rot/2] fp64 (radians per position; scaled contexts change only
+ *         these and `scale`).
+ *   pos : positions [B,T], 64-bit integers, or NULL for 0 .. T-1.
+ *   rot : number of channels that turn, even, 2 <= rot <= d.
+ *   interleaved : 0 = pair j is (j, j + rot/2), 1 = pair j is (2j, 2j + 1).
+ *   inverse : 1 turns by -theta: the backward of the same call on the
+ *         gradients of its outputs.
+ * d in {32, 64, 128}.  No workspace.  Errors: KD_ERR_INVALID_ARG,
+ * KD_ERR_UNSUPPORTED, KD_ERR_CUDA.  Asynchronous on `stream`.
+ */
+KD_API int kron_delta_rotary(const void *q, const void *k, const double *freqs, const long long *pos,
+                             void *q_out, void *k_out, int B, int T, int H, int Hk, int d, int rot,
+                             int interleaved, int inverse, float scale, int dtype, void *stream);
+
+/* Bytes of device workspace of the sliding-window attention calls (0 for
+ * invalid arguments; the reason is then in kron_delta_last_error, which is
+ * empty where a valid call needs none).  T is ignored for KD_SWA_WS_DECODE. */
+KD_API size_t kron_delta_swa_workspace_size(int kind, int B, int T, int H, int Hk, int d, int window,
+                                            int sinks, int dtype);
+
+/*
+ * Causal attention over a sliding window with first tokens that stay visible.
+ * Query t sees key j when j <= t and (t - j < window or j < sinks):
+ *     o_t = sum_j p_tj v_j,  p_tj = exp(scale q_t.k_j - lse_t),
+ *     lse_t = log sum_j exp(scale q_t.k_j)
+ * Every query sees at least its own key.  window >= T is plain causal
+ * attention.
+ *   q, out : [B,T,H,d] (dtype).  k, v : [B,T,Hk,d] (dtype); H a multiple of
+ *         Hk, query head h reads key head h / (H / Hk).
+ *   lse : [B,T,H] fp32, natural logarithm.
+ *   window >= 1;  0 <= sinks <= KD_SWA_MAX_SINKS;  scale finite, > 0.
+ *   workspace : with save = 1 at least
+ *         kron_delta_swa_workspace_size(KD_SWA_WS_SAVE, ...) bytes, 256-byte
+ *         aligned (the rounding of the bf16 output, which the backward adds
+ *         back; zero bytes for fp32), else NULL.
+ * bf16 with d = 64 or 128 runs on tensor cores, the probabilities rounded to
+ * bf16 for their product with v; other shapes run on CUDA cores in fp32.
+ * Preconditions not checked on the device: q, k, v finite; d in {32, 64, 128}
+ * is checked.  Errors as for kron_delta_fwd.  Asynchronous on `stream`.
+ */
+KD_API int kron_delta_swa_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B,
+                              int T, int H, int Hk, int d, int window, int sinks, float scale, int dtype,
+                              void *workspace, size_t ws_bytes, int save, void *stream);
+
+/*
+ * Backward of kron_delta_swa_fwd for the loss <dO, out>.
+ *   out, lse : as the forward wrote them; fwd_ws : its workspace (save = 1).
+ *   dO, dq : [B,T,H,d];  dk, dv : [B,T,Hk,d] (dtype), each summed over the
+ *         query heads that read the key head.
+ *   workspace : at least kron_delta_swa_workspace_size(KD_SWA_WS_BWD, ...).
+ * Every sum runs in a fixed order (bitwise reproducible).  Errors as for
+ * kron_delta_bwd.  Asynchronous on `stream`.
+ */
+KD_API int kron_delta_swa_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                              const void *dO, void *dq, void *dk, void *dv, int B, int T, int H, int Hk,
+                              int d, int window, int sinks, float scale, int dtype, const void *fwd_ws,
+                              size_t fwd_ws_bytes, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One decode step of the same attention: one new token per sequence, over a
+ * cache of sinks + window slots per sequence that is updated in place.  The
+ * token at position p lives in slot p if p < sinks, else in slot
+ * sinks + (p - sinks) % window.  The call stores k, v in the new token's slot
+ * and attends over the min(p + 1, sinks + window) slots filled so far; the
+ * others are never read.
+ *   q, out : [B,H,d];  k, v : [B,Hk,d];  k_cache, v_cache :
+ *   [B,sinks+window,Hk,d] (dtype).
+ *   pos : the new token's position [B], 64-bit integers.  A sequence with
+ *         pos < 0 is idle: its cache is left as it was and its out is zero.
+ *   workspace : at least kron_delta_swa_workspace_size(KD_SWA_WS_DECODE, ...)
+ *         bytes, 256-byte aligned (NULL where that is 0).
+ * Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_WORKSPACE,
+ * KD_ERR_CUDA.  Asynchronous on `stream`.
+ */
+KD_API int kron_delta_swa_decode(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
+                                 const long long *pos, void *out, int B, int H, int Hk, int d, int window,
+                                 int sinks, float scale, int dtype, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
+/*
+ * Fills the cache of kron_delta_swa_decode after a prefill: of the first
+ * lens[b] tokens of sequence b, the first `sinks` and the last `window` go to
+ * their slots.  Slots that none of them belongs to are left as they were.
+ *   k, v : [B,T,Hk,d] (dtype);  lens : [B] 64-bit integers; a length below 0
+ *   counts as 0 and one above T as T.
+ * No workspace.  Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_CUDA.
+ * Asynchronous on `stream`.
+ */
+KD_API int kron_delta_swa_fill(const void *k, const void *v, const long long *lens, void *k_cache,
+                               void *v_cache, int B, int T, int Hk, int d, int window, int sinks, int dtype,
+                               void *stream);
+
+/* Bytes of device workspace of the gated linear recurrence (0 for invalid
+ * sizes; the reason is then in kron_delta_last_error). */
+KD_API size_t kron_delta_glr_workspace_size(int kind, int B, int T, int D, int dtype);
+
+/*
+ * Gated linear recurrence, element by element: per channel j of D, with the
+ * forget gate in the form of kron_delta_prologue_fwd (sigma(x)^a, a =
+ * e^{a_log}, here one exponent per channel),
+ *     f_t = sigma(f_pre_t)^a,   h_t = f_t h_{t-1} + sqrt(1 - f_t^2) sigma(i_pre_t) x_t
+ * The write is scaled by sqrt(1 - f^2), which keeps the state's variance at
+ * the input's.  f_pre = -infinity (or the type's lowest value) gives f = 0 and
+ * so starts a new sequence at that token.
+ *   x, i_pre, f_pre, out : [B,T,D] (dtype); out is h_t.
+ *   a_log : [D] fp32.  h0 : [B,D] fp32 or NULL (zero).  hT : [B,D] fp32 or NULL.
+ *   D a multiple of 8.  The state, and every sum, is fp32.
+ *   workspace : with save = 1 at least
+ *         kron_delta_glr_workspace_size(KD_GLR_WS_SAVE, ...) bytes, 256-byte
+ *         aligned (the fp32 state at each 64th token), else NULL.
+ * Errors as for kron_delta_fwd.  Asynchronous on `stream`.
+ */
+KD_API int kron_delta_glr_fwd(const void *x, const void *i_pre, const void *f_pre, const float *a_log,
+                              const float *h0, void *out, float *hT, int B, int T, int D, int dtype,
+                              void *workspace, size_t ws_bytes, int save, void *stream);
+
+/*
+ * Backward of kron_delta_glr_fwd for the loss <dh, out> + <dhT, hT>.
+ *   fwd_ws : the workspace of a kron_delta_glr_fwd call with save = 1 on
+ *         exactly these inputs (read only).
+ *   dh : [B,T,D] (dtype).  dhT : [B,D] fp32 or NULL (zero).
+ *   dx, di_pre, df_pre : [B,T,D] (dtype).  da_log : [D] fp32, summed over the
+ *   batch and the tokens in a fixed order.  dh0 : [B,D] fp32 or NULL.
+ *   workspace : at least kron_delta_glr_workspace_size(KD_GLR_WS_BWD, ...).
+ * Errors as for kron_delta_bwd.  Asynchronous on `stream`.
+ */
+KD_API int kron_delta_glr_bwd(const void *x, const void *i_pre, const void *f_pre, const float *a_log,
+                              const void *dh, const float *dhT, void *dx, void *di_pre, void *df_pre,
+                              float *da_log, float *dh0, int B, int T, int D, int dtype, const void *fwd_ws,
+                              size_t fwd_ws_bytes, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One decode step of the gated linear recurrence: one new token per sequence.
+ *   x, i_pre, f_pre, out : [B,D] (dtype);  a_log : [D] fp32.
+ *   h : [B,D] fp32, read and overwritten with the new state.
+ * No workspace.  Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_CUDA.
+ * Asynchronous on `stream`.
+ */
+KD_API int kron_delta_glr_decode(const void *x, const void *i_pre, const void *f_pre, const float *a_log,
+                                 float *h, void *out, int B, int D, int dtype, void *stream);
 
 /*
  * Synchronises `stream` and reports device-side failures of earlier calls:
