@@ -1,5 +1,6 @@
 // kd_swa.cu -- sliding-window attention with first tokens kept, on CUDA cores
-// in fp32.
+// in fp32 (fp32 tensors, and bf16 with d = 32), and the passes around the
+// products that the tensor-core path (kd_swa_tc.cu) shares.
 //
 // Query t sees key j when j <= t and (t - j < W or j < S).
 //   forward   x = scale q k^T over the visible keys, one pass with the running
@@ -462,16 +463,12 @@ SwaBwdLayout swa_bwd_layout(int B, int T, int H, int Hk, int d, int window, int 
 }
 
 cudaError_t launch_swa_fwd_simt(const SwaArgs& a, cudaStream_t st) {
-  if (a.dtype == 1)
-    return a.d == 32 ? fwd_go<__nv_bfloat16, 32>(a, st)
-                     : a.d == 64 ? fwd_go<__nv_bfloat16, 64>(a, st) : fwd_go<__nv_bfloat16, 128>(a, st);
+  if (a.dtype == 1) return fwd_go<__nv_bfloat16, 32>(a, st);  // wider bf16 heads run on tensor cores
   return a.d == 32 ? fwd_go<float, 32>(a, st) : a.d == 64 ? fwd_go<float, 64>(a, st) : fwd_go<float, 128>(a, st);
 }
 
 cudaError_t launch_swa_bwd_simt(const SwaArgs& a, cudaStream_t st) {
-  if (a.dtype == 1)
-    return a.d == 32 ? bwd_go<__nv_bfloat16, 32>(a, st)
-                     : a.d == 64 ? bwd_go<__nv_bfloat16, 64>(a, st) : bwd_go<__nv_bfloat16, 128>(a, st);
+  if (a.dtype == 1) return bwd_go<__nv_bfloat16, 32>(a, st);
   return a.d == 32 ? bwd_go<float, 32>(a, st) : a.d == 64 ? bwd_go<float, 64>(a, st) : bwd_go<float, 128>(a, st);
 }
 
@@ -499,9 +496,5 @@ cudaError_t launch_swa_sink_sum(const SwaArgs& a, const SwaBwdLayout& L, int til
   prof_end(st);
   return cudaGetLastError();
 }
-
-bool swa_tc_supported(int, int) { return false; }
-cudaError_t launch_swa_fwd_tc(const SwaArgs& a, cudaStream_t st) { return launch_swa_fwd_simt(a, st); }
-cudaError_t launch_swa_bwd_tc(const SwaArgs& a, cudaStream_t st) { return launch_swa_bwd_simt(a, st); }
 
 }  // namespace kd

@@ -23,7 +23,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool make_tmap_bthd(CUtensorMap* m, const void* base, int es, int B, int T, int H, int D, int box_d,
-                    bool swizzle128) {
+                    bool swizzle128, int box_t) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t e = static_cast<cuuint64_t>(es);
@@ -31,7 +31,7 @@ bool make_tmap_bthd(CUtensorMap* m, const void* base, int es, int B, int T, int 
                         static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {D * e, static_cast<cuuint64_t>(H) * D * e,
                            static_cast<cuuint64_t>(T) * H * D * e};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), 1u, 64u, 1u};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), 1u, static_cast<cuuint32_t>(box_t), 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   const CUresult r =
       fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
