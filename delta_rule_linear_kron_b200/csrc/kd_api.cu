@@ -1186,6 +1186,9 @@ int kron_delta_glr_fwd(const void* x, const void* i_pre, const void* f_pre, cons
   a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.h0 = h0; a.out = out; a.hT = hT;
   a.states = save ? static_cast<float*>(workspace) : nullptr;
   a.B = B; a.T = T; a.D = D; a.dtype = dtype;
+  DeviceInfo di;
+  KD_TRY(device_info(&di));
+  a.err = di.err;
   return launched(kd::launch_glr_fwd(a, static_cast<cudaStream_t>(stream)), "glr forward launch");
 }
 
@@ -1211,6 +1214,9 @@ int kron_delta_glr_bwd(const void* x, const void* i_pre, const void* f_pre, cons
   a.states_in = static_cast<const float*>(fwd_ws);
   a.part = static_cast<float*>(workspace);
   a.B = B; a.T = T; a.D = D; a.dtype = dtype;
+  DeviceInfo di;
+  KD_TRY(device_info(&di));
+  a.err = di.err;
   return launched(kd::launch_glr_bwd(a, static_cast<cudaStream_t>(stream)), "glr backward launch");
 }
 

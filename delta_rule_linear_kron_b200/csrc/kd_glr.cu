@@ -9,22 +9,26 @@
 //   df~ = dl a sigma(-f~),  da_log = sum dl l
 //
 // HBM-bound in bytes (8 per element forward, 14.25 backward with bf16), but
-// close to the instruction rate too: the gates are about 45 instructions per
-// element, so nothing may be computed twice.  One pass: a cluster of C CTAs
-// takes 64 channels and C consecutive chunks of 64 tokens at a time.  A warp
-// holds 8 tokens, a lane 2 channels; each thread scans its 8 tokens from zero,
-// the warps' (prod f, h) pairs combine through shared memory and the CTAs'
-// through distributed shared memory, and the thread then adds its start
-// state's part, from registers.  The chain along the sequence is then only
-// ceil(T / 64C) cluster exchanges long.
+// close to the rates of instructions and of the special function unit too, so
+// nothing may be computed twice.  One pass: a cluster of C CTAs takes 64
+// channels and C consecutive chunks of 64 tokens at a time.  TMA brings the
+// chunks' tiles a step ahead.  A warp holds 8 tokens, a lane 2 channels (one
+// f32x2 register pair, so that most of the arithmetic is two channels an
+// instruction); each thread scans its 8 tokens from zero, the warps'
+// (prod f, h) pairs combine through shared memory and the CTAs' through
+// distributed shared memory, and the thread then adds its start state's part,
+// from registers.  The chain along the sequence is only ceil(T / 64C) cluster
+// exchanges long.
 //
-// The state's error builds up over 1 / (1 - f) steps, so f and 1 - f^2 are
-// formed through expm1 (f = 1 + y, 1 - f^2 = -y (1 + f)): f is then within
-// half an fp32 step, without a bias, where the hardware exponential alone is
-// off by up to two.
+// Accuracy: the state's error builds up over 1 / (1 - f) steps, so f must not
+// carry a bias.  With L = log2 f = n + r, |r| <= 1/2, f = 2^n (1 + q), q by the
+// series of 2^r - 1; where n = 0 (every gate that keeps more than 0.7), q is
+// f - 1 without cancellation, and 1 - f^2 = -(f - 1)(1 + f) keeps its relative
+// precision however close f is to 1.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 #include "kd_tc.cuh"
+#include "kd_tmap.h"
 
 namespace kd {
 
@@ -50,318 +54,426 @@ __device__ __forceinline__ float rsq(float x) {
   return y;
 }
 constexpr float kLog2e = 1.44269504088896f;
+constexpr float kLn2 = 0.693147180559945f;
 
-// log(1 + e), 0 <= e <= 1: 2 artanh(s) with s = e / (2 + e) <= 1/3, seven
-// terms of its series (the eighth is below 2e-8 of the sum).
-__device__ __forceinline__ float log1p01(float e) {
-  const float s = e * rcp(2.f + e), z = s * s;
-  float p = fmaf(z, 1.f / 13, 1.f / 11);
-  p = fmaf(z, p, 1.f / 9);
-  p = fmaf(z, p, 1.f / 7);
-  p = fmaf(z, p, 1.f / 5);
-  p = fmaf(z, p, 1.f / 3);
-  return 2.f * fmaf(s * z, p, s);
+// Two channels in one register pair.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pk(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 pk(float a) { return pk(a, a); }
+__device__ __forceinline__ float2 un(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
 struct Gates {
-  float l, f, w, i;  // w = 1 - f^2
-  float e;           // e^{-|f~|}
+  F2 L;  // log2 f
+  F2 f;
+  F2 w;  // 1 - f^2
+  F2 i;  // sigma(i~)
+  F2 s, j;  // with kBack: sigma(-f~), and sigma(-i~) = 2^k sigma(i~) (1 - i would cancel)
 };
 
-__device__ __forceinline__ Gates gates(float zf, float zi, float a) {
+// na2: -a log2 e.
+template <bool kBack>
+__device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   Gates g;
-  g.e = ex2(-kLog2e * fabsf(zf));
-  // f~ at the type's lowest value starts a new sequence: l stays finite so
-  // that the backward's dl l is 0 there and not 0 * infinity
-  g.l = fmaxf(-a * (fmaxf(-zf, 0.f) + log1p01(g.e)), -1e30f);
-  // e^l - 1 on [-1/2, 0] by its series up to l^8 / 8! (the next term is below
-  // 1e-8 of the sum); below that nothing cancels
-  const float l = g.l;
-  float p = fmaf(l, 1.f / 40320, 1.f / 5040);
-  p = fmaf(l, p, 1.f / 720);
-  p = fmaf(l, p, 1.f / 120);
-  p = fmaf(l, p, 1.f / 24);
-  p = fmaf(l, p, 1.f / 6);
-  p = fmaf(l, p, 0.5f);
-  p = fmaf(l, p, 1.f) * l;
-  const float far = ex2(kLog2e * l);
-  const bool near = l > -0.5f;
-  g.f = near ? 1.f + p : far;
-  const float y = near ? p : far - 1.f;
-  g.w = -y * (1.f + g.f);
-  g.i = rcp(1.f + ex2(-kLog2e * zi));
+  const float ex = ex2(-kLog2e * fabsf(zf.x)), ey = ex2(-kLog2e * fabsf(zf.y));
+  const F2 e = pk(ex, ey);
+  const F2 d = add2(e, pk(2.f));
+  // sigma(i~) = 1 / (1 + 2^k), 0 beyond 2^60
+  const float kx = -kLog2e * zi.x, ky = -kLog2e * zi.y;
+  const F2 k2 = pk(ex2(fminf(kx, 60.f)), ex2(fminf(ky, 60.f)));
+  const F2 c = add2(k2, pk(1.f));
+  // the reciprocals of 2 + e, 1 + 2^k (and 1 + e) from one of their product
+  F2 dc = mul2(d, c), one = add2(e, pk(1.f));
+  const float2 den = un(kBack ? mul2(dc, one) : dc);
+  const F2 r = pk(rcp(den.x), rcp(den.y));
+  F2 rd;
+  if (kBack) {
+    g.s = mul2(mul2(r, dc), pk(zf.x >= 0.f ? ex : 1.f, zf.y >= 0.f ? ey : 1.f));
+    const F2 ro = mul2(r, one);
+    g.i = mul2(ro, d);
+    g.j = mul2(k2, g.i);
+    rd = mul2(ro, c);
+  } else {
+    g.i = mul2(r, d);
+    rd = mul2(r, c);
+  }
+  const float2 gi = un(g.i);
+  g.i = pk(kx > 60.f ? 0.f : gi.x, ky > 60.f ? 0.f : gi.y);
+  // log(1 + e) = 2 artanh(u), u = e / (2 + e) <= 1/3: seven terms of its
+  // series (the eighth is below 2e-8 of the sum)
+  const F2 u = mul2(e, rd), z = mul2(u, u);
+  F2 p = fma2(z, pk(1.f / 13), pk(1.f / 11));
+  p = fma2(z, p, pk(1.f / 9));
+  p = fma2(z, p, pk(1.f / 7));
+  p = fma2(z, p, pk(1.f / 5));
+  p = fma2(z, p, pk(1.f / 3));
+  p = fma2(mul2(u, z), p, u);
+  const F2 soft = fma2(p, pk(2.f), pk(fmaxf(-zf.x, 0.f), fmaxf(-zf.y, 0.f)));
+  // f~ at the type's lowest value starts a new sequence: L stays finite so
+  // that the backward's dl L is 0 there and not 0 * infinity
+  const float2 Lf = un(mul2(soft, na2));
+  const float Lx = fmaxf(Lf.x, -1e30f), Ly = fmaxf(Lf.y, -1e30f);
+  g.L = pk(Lx, Ly);
+  const F2 Lc = pk(fmaxf(Lx, -126.f), fmaxf(Ly, -126.f));
+  const float kMagic = 12582912.f;  // 1.5 2^23: rounds to an integer, kept in the low bits
+  const F2 t = add2(Lc, pk(kMagic));
+  const F2 n = add2(t, pk(-kMagic)), x = fma2(n, pk(-1.f), Lc);
+  // 2^x - 1 = sum (x ln 2)^k / k! up to k = 7 (the next term is below 2e-8 of it)
+  F2 q = fma2(x, pk(1.52527338e-5f), pk(1.54035304e-4f));
+  q = fma2(x, q, pk(1.33335581e-3f));
+  q = fma2(x, q, pk(9.61812911e-3f));
+  q = fma2(x, q, pk(5.55041087e-2f));
+  q = fma2(x, q, pk(2.40226507e-1f));
+  q = fma2(x, q, pk(6.93147181e-1f));
+  q = mul2(q, x);
+  const float2 t2 = un(t), m2 = un(add2(q, pk(1.f))), q2 = un(q);
+  float fx = __uint_as_float(__float_as_uint(m2.x) + (__float_as_uint(t2.x) << 23));
+  float fy = __uint_as_float(__float_as_uint(m2.y) + (__float_as_uint(t2.y) << 23));
+  fx = Lx < -126.f ? 0.f : fx;
+  fy = Ly < -126.f ? 0.f : fy;
+  g.f = pk(fx, fy);
+  const float2 y2 = un(add2(g.f, pk(-1.f)));
+  const F2 y = pk(t2.x == kMagic ? q2.x : y2.x, t2.y == kMagic ? q2.y : y2.y);
+  g.w = mul2(y, fma2(g.f, pk(-1.f), pk(-1.f)));
   return g;
 }
 
-// 1 / m.  A gate so close to 1 that w leaves the range of the reciprocal root
-// writes nothing (m < 1e-15) and takes no gradient through m.
-__device__ __forceinline__ float inv_m(float w) { return w > 1e-30f ? rsq(w) : 0.f; }
+// 1 / m.  The bound only meets gates so close to 1 that w rounds to 0: w / m
+// is 0 there, and d l vanishes faster than 1 / m is large.
+__device__ __forceinline__ F2 inv_m(F2 w) {
+  const float2 v = un(w);
+  return pk(rsq(fmaxf(v.x, 1e-30f)), rsq(fmaxf(v.y, 1e-30f)));
+}
 
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
   using type = __nv_bfloat162;
   static __device__ __forceinline__ float2 f(type v) { return __bfloat1622float2(v); }
-  static __device__ __forceinline__ type of(float a, float b) { return __floats2bfloat162_rn(a, b); }
+  static __device__ __forceinline__ type of(F2 a) {
+    const float2 v = un(a);
+    return __floats2bfloat162_rn(v.x, v.y);
+  }
 };
 template <> struct Pair<float> {
   using type = float2;
   static __device__ __forceinline__ float2 f(type v) { return v; }
-  static __device__ __forceinline__ type of(float a, float b) { return make_float2(a, b); }
+  static __device__ __forceinline__ type of(F2 a) { return un(a); }
 };
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
+// (f products, states) of a run of tokens, two channels; `then` appends a later run.
+struct Run {
+  F2 f, h;
+};
+__device__ __forceinline__ Run then(Run a, Run b) { return {mul2(a.f, b.f), fma2(b.f, a.h, b.h)}; }
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, Run v) {
+  asm volatile("st.shared::cluster.v2.b64 [%0], {%1,%2};" ::"r"(addr), "l"(v.f.v), "l"(v.h.v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <typename T, int kArrays>
+struct GlrCfg {
+  static constexpr uint32_t TILE = kChunk * kChans * sizeof(T);
+  static constexpr uint32_t STAGE = kArrays * TILE;
+  static constexpr uint32_t RUNS = 2 * STAGE;                                   // Run [2][kWarps][32]
+  static constexpr uint32_t CRUNS = RUNS + 2 * kWarps * 32 * 16;                // Run [2][kGlrMaxCluster][32]
+  static constexpr uint32_t U = CRUNS + 2 * kGlrMaxCluster * 32 * 16;           // backward: F2 [2][kWarps][32]
+  static constexpr uint32_t KEEP = U + 2 * kWarps * 32 * 8;                     // backward: F2 [kTok][threads]
+  static constexpr uint32_t BYTES = (kArrays == 3 ? U : KEEP + kTok * kWarps * 32 * 8) + 128;
+};
+
+// The tiles of one chunk (kArrays tensors) into a stage.
+template <typename T, int kArrays>
+__device__ __forceinline__ void load_stage(unsigned char* sm, int stage, const CUtensorMap* const (&maps)[kArrays], int c,
+                                           int t0, int b, uint64_t* bar) {
+  using Cf = GlrCfg<T, kArrays>;
+  tc::mbar_expect_tx(bar, Cf::STAGE);
+#pragma unroll
+  for (int i = 0; i < kArrays; ++i) tc::tma_load_4d(sm + stage * Cf::STAGE + i * Cf::TILE, maps[i], c, 0, t0, b, bar);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) glr_fwd_kernel(const T* __restrict__ x, const T* __restrict__ ip,
-                                                              const T* __restrict__ fp,
-                                                              const float* __restrict__ a_log,
-                                                              const float* __restrict__ h0, T* __restrict__ out,
-                                                              float* __restrict__ hT, float* __restrict__ states,
-                                                              int T_, int D, int NC, int C) {
+__global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
+    const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mi,
+    const __grid_constant__ CUtensorMap mf, const float* __restrict__ a_log, const float* __restrict__ h0,
+    T* __restrict__ out, float* __restrict__ hT, float* __restrict__ states, int T_, int D, int NC, int C, int* err) {
   using P = Pair<T>;
   using V = typename P::type;
-  __shared__ float4 wagg[2][kWarps][32];  // (f products, states) of a warp's tokens, two channels
-  __shared__ float4 cagg[2][kGlrMaxCluster][32];       // the same of the cluster's CTAs
+  using Cf = GlrCfg<T, 3>;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((128u - (tc::smem_u32(smem_raw) & 127u)) & 127u);
+  __shared__ uint64_t full[2];
+  __shared__ int abort_flag;
+  Run(*runs)[kWarps][32] = reinterpret_cast<Run(*)[kWarps][32]>(sm + Cf::RUNS);
+  Run(*cruns)[kGlrMaxCluster][32] = reinterpret_cast<Run(*)[kGlrMaxCluster][32]>(sm + Cf::CRUNS);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = C > 1 ? (int)tc::cluster_rank() : 0;
-  const int b = blockIdx.y, c = (int)(blockIdx.x / C) * kChans + lane * 2;
+  const int b = blockIdx.y, c0 = (int)(blockIdx.x / C) * kChans, c = c0 + lane * 2;
   const bool live = c < D;
-  const size_t base = (size_t)b * T_ * D + c;
-  float a0 = 1.f, a1 = 1.f;
-  float2 carry = make_float2(0.f, 0.f);
-  if (live) {
-    a0 = expf(a_log[c]);
-    a1 = expf(a_log[c + 1]);
-    if (h0) carry = *reinterpret_cast<const float2*>(h0 + (size_t)b * D + c);
-  }
-  if (C > 1) tc::cluster_sync();  // every CTA of the cluster has started
+  const CUtensorMap* const maps[3] = {&mx, &mi, &mf};
   const int steps = (NC + C - 1) / C;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&full[0], 1);
+    tc::mbar_init(&full[1], 1);
+    tc::mbar_init_fence();
+    abort_flag = 0;
+    for (int s = 0; s < 2; ++s)
+      if (s * C + rank < NC) load_stage<T, 3>(sm, s, maps, c0, (s * C + rank) * kChunk, b, &full[s]);
+  }
+  F2 na2 = pk(0.f), carry = pk(0.f);
+  if (live) {
+    na2 = pk(-kLog2e * expf(a_log[c]), -kLog2e * expf(a_log[c + 1]));
+    if (h0) carry = *reinterpret_cast<const F2*>(h0 + (size_t)b * D + c);
+  }
+  __syncthreads();
+  if (C > 1) tc::cluster_sync();  // every CTA of the cluster has started
+  const size_t base = (size_t)b * T_ * D + c;
   for (int s = 0; s < steps; ++s) {
     const int n = s * C + rank, par = s & 1;
-    const long long t0 = (long long)n * kChunk + warp * kTok;
-    const long long left = T_ - t0;
+    const long long t0 = (long long)n * kChunk + warp * kTok, left = T_ - t0;
     const int k = !live || left <= 0 ? 0 : left < kTok ? (int)left : kTok;  // tokens of this thread
-    const size_t off = base + (size_t)t0 * D;
-    V rx[kTok], ri[kTok], rf[kTok];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j)
-      if (j < k) {
-        rf[j] = __ldcs(reinterpret_cast<const V*>(fp + off + (size_t)j * D));
-        ri[j] = __ldcs(reinterpret_cast<const V*>(ip + off + (size_t)j * D));
-        rx[j] = __ldcs(reinterpret_cast<const V*>(x + off + (size_t)j * D));
-      }
-    float F0[kTok], F1[kTok], H0[kTok], H1[kTok];
-    float p0 = 1.f, p1 = 1.f, q0 = 0.f, q1 = 0.f;
+    const unsigned char* st = sm + par * Cf::STAGE;
+    if (n < NC) tc::mbar_wait<false>(&full[par], (s >> 1) & 1, err, tc::kErrTimeoutLoad, &abort_flag);
+    Run r[kTok], run = {pk(1.f), pk(0.f)};
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
+      const int at = (warp * kTok + j) * 32 + lane;
       if (j < k) {
-        const float2 vx = P::f(rx[j]), vi = P::f(ri[j]), vf = P::f(rf[j]);
-        const Gates g0 = gates(vf.x, vi.x, a0), g1 = gates(vf.y, vi.y, a1);
-        p0 *= g0.f;
-        p1 *= g1.f;
-        q0 = fmaf(g0.f, q0, g0.w * inv_m(g0.w) * g0.i * vx.x);
-        q1 = fmaf(g1.f, q1, g1.w * inv_m(g1.w) * g1.i * vx.y);
+        const float2 x = P::f(reinterpret_cast<const V*>(st)[at]);
+        const Gates g = gates<false>(P::f(reinterpret_cast<const V*>(st + 2 * Cf::TILE)[at]),
+                                     P::f(reinterpret_cast<const V*>(st + Cf::TILE)[at]), na2);
+        const F2 m = mul2(g.w, inv_m(g.w));
+        run = then(run, {g.f, mul2(mul2(m, g.i), pk(x.x, x.y))});
       }
-      F0[j] = p0; F1[j] = p1; H0[j] = q0; H1[j] = q1;
+      r[j] = run;
     }
-    wagg[par][warp][lane] = make_float4(p0, p1, q0, q1);
-    __syncthreads();
-    float4 pre = make_float4(1.f, 1.f, 0.f, 0.f), all = pre;
+    runs[par][warp][lane] = run;
+    __syncthreads();  // and every thread is through with the stage
+    if (threadIdx.x == 0 && n + 2 * C < NC)
+      load_stage<T, 3>(sm, par, maps, c0, (n + 2 * C) * kChunk, b, &full[par]);
+    Run pre = {pk(1.f), pk(0.f)}, all = pre;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w == warp) pre = all;
-      const float4 v = wagg[par][w][lane];
-      all = make_float4(all.x * v.x, all.y * v.y, fmaf(v.x, all.z, v.z), fmaf(v.y, all.w, v.w));
+      all = then(all, runs[par][w][lane]);
     }
-    float2 mine = carry;  // state at the start of this CTA's chunk
+    F2 mine = carry;  // state at the start of this CTA's chunk
     if (C > 1) {
-      // warp w hands the chunk's pair to CTA w; the buffer's last readers have
+      // warp w hands the chunk's run to CTA w; the buffer's last readers have
       // arrived at the barrier of the step before
-      if (warp < C) st_cluster(tc::mapa(tc::smem_u32(&cagg[par][rank][lane]), warp), all);
+      if (warp < C) st_cluster(tc::mapa(tc::smem_u32(&cruns[par][rank][lane]), warp), all);
       tc::cluster_sync();
-      for (int r = 0; r < C; ++r) {
-        if (r == rank) mine = carry;
-        const float4 v = cagg[par][r][lane];
-        carry = make_float2(fmaf(v.x, carry.x, v.z), fmaf(v.y, carry.y, v.w));
+      for (int q = 0; q < C; ++q) {
+        if (q == rank) mine = carry;
+        const Run v = cruns[par][q][lane];
+        carry = fma2(v.f, carry, v.h);
       }
     } else {
-      carry = make_float2(fmaf(all.x, carry.x, all.z), fmaf(all.y, carry.y, all.w));
+      carry = fma2(all.f, carry, all.h);
     }
-    const float s0 = fmaf(pre.x, mine.x, pre.z), s1 = fmaf(pre.y, mine.y, pre.w);
-    if (states && warp == 0 && live && n < NC)
-      *reinterpret_cast<float2*>(states + ((size_t)b * NC + n) * D + c) = mine;
+    const F2 h = fma2(pre.f, mine, pre.h);
+    if (states && warp == 0 && live && n < NC) *reinterpret_cast<F2*>(states + ((size_t)b * NC + n) * D + c) = mine;
+    T* o = out + base + (size_t)t0 * D;
 #pragma unroll
     for (int j = 0; j < kTok; ++j)
-      if (j < k)
-        __stcs(reinterpret_cast<V*>(out + off + (size_t)j * D),
-               P::of(fmaf(F0[j], s0, H0[j]), fmaf(F1[j], s1, H1[j])));
+      if (j < k) __stcs(reinterpret_cast<V*>(o + (size_t)j * D), P::of(fma2(r[j].f, h, r[j].h)));
   }
-  if (hT && rank == 0 && warp == 0 && live) *reinterpret_cast<float2*>(hT + (size_t)b * D + c) = carry;
+  if (hT && rank == 0 && warp == 0 && live) *reinterpret_cast<F2*>(hT + (size_t)b * D + c) = carry;
 }
 
 // The backward walks the chunks from the last.  The states h_{t-1} come from
 // the chunk's saved start state, run forward again over the tokens in
 // registers, so they are fp32 (the bf16 output would put its rounding into
-// df~ and da_log).
+// df~ and da_log).  What the last pass over the tokens needs and registers do
+// not hold waits in shared memory: a sigma(-f~), and log2 f in place of the
+// f~ and i~ that it came from; each thread reads back only what it wrote.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(
-    const T* __restrict__ x, const T* __restrict__ ip, const T* __restrict__ fp, const float* __restrict__ a_log,
-    const float* __restrict__ states, const T* __restrict__ dh, const float* __restrict__ dhT, T* __restrict__ dx,
-    T* __restrict__ di, T* __restrict__ df, float* __restrict__ part, float* __restrict__ dh0, int T_, int D, int NC,
-    int C) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_kernel(
+    const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mi,
+    const __grid_constant__ CUtensorMap mf, const __grid_constant__ CUtensorMap mg, const float* __restrict__ a_log,
+    const float* __restrict__ states, const float* __restrict__ dhT, T* __restrict__ dx, T* __restrict__ di,
+    T* __restrict__ df, float* __restrict__ part, float* __restrict__ dh0, int T_, int D, int NC, int C, int* err) {
   using P = Pair<T>;
   using V = typename P::type;
-  __shared__ float4 wagg[2][kWarps][32];  // (f products, forward states)
-  __shared__ float2 uagg[2][kWarps][32];  // reverse terms u
-  __shared__ float4 cagg[2][kGlrMaxCluster][32];       // (f products, u) of the cluster's CTAs
+  using Cf = GlrCfg<T, 4>;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((128u - (tc::smem_u32(smem_raw) & 127u)) & 127u);
+  __shared__ uint64_t full[2];
+  __shared__ int abort_flag;
+  Run(*runs)[kWarps][32] = reinterpret_cast<Run(*)[kWarps][32]>(sm + Cf::RUNS);
+  Run(*cruns)[kGlrMaxCluster][32] = reinterpret_cast<Run(*)[kGlrMaxCluster][32]>(sm + Cf::CRUNS);
+  F2(*us)[kWarps][32] = reinterpret_cast<F2(*)[kWarps][32]>(sm + Cf::U);
+  F2* keep = reinterpret_cast<F2*>(sm + Cf::KEEP) + threadIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = C > 1 ? (int)tc::cluster_rank() : 0;
-  const int b = blockIdx.y, c = (int)(blockIdx.x / C) * kChans + lane * 2;
+  const int b = blockIdx.y, c0 = (int)(blockIdx.x / C) * kChans, c = c0 + lane * 2;
   const bool live = c < D;
-  const size_t base = (size_t)b * T_ * D + c;
-  float a0 = 1.f, a1 = 1.f;
-  float2 carry = make_float2(0.f, 0.f);
-  if (live) {
-    a0 = expf(a_log[c]);
-    a1 = expf(a_log[c + 1]);
-    if (dhT) carry = *reinterpret_cast<const float2*>(dhT + (size_t)b * D + c);
-  }
-  float da0 = 0.f, da1 = 0.f;
-  if (C > 1) tc::cluster_sync();  // every CTA of the cluster has started
+  const CUtensorMap* const maps[4] = {&mx, &mi, &mf, &mg};
   const int steps = (NC + C - 1) / C;
-  for (int s = steps - 1; s >= 0; --s) {
-    const int n = s * C + rank, par = s & 1;
-    const long long t0 = (long long)n * kChunk + warp * kTok;
-    const long long left = T_ - t0;
+  // step s runs chunk ((steps - 1 - s) C + rank); a stage is loaded one step ahead
+  const auto chunk = [&](int s) { return (steps - 1 - s) * C + rank; };
+  int uses[2] = {0, 0};
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&full[0], 1);
+    tc::mbar_init(&full[1], 1);
+    tc::mbar_init_fence();
+    abort_flag = 0;
+    for (int s = 0; s < 2 && s < steps; ++s)
+      if (chunk(s) < NC) load_stage<T, 4>(sm, s, maps, c0, chunk(s) * kChunk, b, &full[s]);
+  }
+  F2 na2 = pk(0.f), carry = pk(0.f);
+  if (live) {
+    na2 = pk(-kLog2e * expf(a_log[c]), -kLog2e * expf(a_log[c + 1]));
+    if (dhT) carry = *reinterpret_cast<const F2*>(dhT + (size_t)b * D + c);
+  }
+  const F2 a = mul2(na2, pk(-kLn2));
+  F2 da = pk(0.f);
+  __syncthreads();
+  if (C > 1) tc::cluster_sync();  // every CTA of the cluster has started
+  for (int s = 0; s < steps; ++s) {
+    const int n = chunk(s), par = s & 1;
+    const long long t0 = (long long)n * kChunk + warp * kTok, left = T_ - t0;
     const int k = !live || left <= 0 ? 0 : left < kTok ? (int)left : kTok;
-    const size_t off = base + (size_t)t0 * D;
-    V rx[kTok], ri[kTok], rf[kTok], rg[kTok];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j)
-      if (j < k) {
-        rf[j] = __ldcs(reinterpret_cast<const V*>(fp + off + (size_t)j * D));
-        ri[j] = __ldcs(reinterpret_cast<const V*>(ip + off + (size_t)j * D));
-        rx[j] = __ldcs(reinterpret_cast<const V*>(x + off + (size_t)j * D));
-        rg[j] = __ldcs(reinterpret_cast<const V*>(dh + off + (size_t)j * D));
-      }
-    float2 start = make_float2(0.f, 0.f);
-    if (live && n < NC) start = *reinterpret_cast<const float2*>(states + ((size_t)b * NC + n) * D + c);
-    float F[2][kTok], Bx[2][kTok], Wr[2][kTok], I[2][kTok];  // f, m i x, 1 / m, i
-    float p0 = 1.f, p1 = 1.f, q0 = 0.f, q1 = 0.f;
+    unsigned char* st = sm + par * Cf::STAGE;
+    const V* xs = reinterpret_cast<const V*>(st) + warp * kTok * 32 + lane;
+    const V* gs = reinterpret_cast<const V*>(st + 3 * Cf::TILE) + warp * kTok * 32 + lane;
+    F2 start = pk(0.f);
+    if (live && n < NC) start = *reinterpret_cast<const F2*>(states + ((size_t)b * NC + n) * D + c);
+    if (n < NC) {
+      tc::mbar_wait<false>(&full[par], uses[par] & 1, err, tc::kErrTimeoutLoad, &abort_flag);
+      ++uses[par];
+    }
+    F2 F[kTok], M[kTok], Q[kTok], J[kTok];  // f, m i, f i x / m, sigma(-i~)
+    Run run = {pk(1.f), pk(0.f)};
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      F[0][j] = F[1][j] = 1.f;
-      Bx[0][j] = Bx[1][j] = Wr[0][j] = Wr[1][j] = I[0][j] = I[1][j] = 0.f;
+      F[j] = pk(1.f);
+      M[j] = Q[j] = J[j] = pk(0.f);
       if (j < k) {
-        const float2 vx = P::f(rx[j]), vi = P::f(ri[j]), vf = P::f(rf[j]);
-        const Gates g0 = gates(vf.x, vi.x, a0), g1 = gates(vf.y, vi.y, a1);
-        F[0][j] = g0.f;
-        F[1][j] = g1.f;
-        I[0][j] = g0.i;
-        I[1][j] = g1.i;
-        Wr[0][j] = inv_m(g0.w);
-        Wr[1][j] = inv_m(g1.w);
-        Bx[0][j] = g0.w * Wr[0][j] * g0.i * vx.x;
-        Bx[1][j] = g1.w * Wr[1][j] * g1.i * vx.y;
-        p0 *= g0.f;
-        p1 *= g1.f;
-        q0 = fmaf(g0.f, q0, Bx[0][j]);
-        q1 = fmaf(g1.f, q1, Bx[1][j]);
+        const int at = (warp * kTok + j) * 32 + lane;
+        const float2 x = P::f(xs[j * 32]);
+        const Gates g = gates<true>(P::f(reinterpret_cast<const V*>(st + 2 * Cf::TILE)[at]),
+                                    P::f(reinterpret_cast<const V*>(st + Cf::TILE)[at]), na2);
+        const float2 L = un(g.L);
+        // the same thread's own two words: 4 bytes of the i~ tile and of the f~ tile
+        *reinterpret_cast<float*>(st + Cf::TILE + at * sizeof(V)) = L.x;
+        *reinterpret_cast<float*>(st + 2 * Cf::TILE + at * sizeof(V)) = L.y;
+        keep[j * kWarps * 32] = mul2(a, g.s);
+        const F2 r = inv_m(g.w), x2 = pk(x.x, x.y);
+        F[j] = g.f;
+        J[j] = g.j;
+        M[j] = mul2(mul2(g.w, r), g.i);
+        Q[j] = mul2(mul2(g.f, x2), mul2(g.i, r));
+        run = then(run, {g.f, mul2(M[j], x2)});
       }
     }
-    float u0 = 0.f, u1 = 0.f;
+    F2 u = pk(0.f);
 #pragma unroll
     for (int j = kTok - 1; j >= 0; --j)
       if (j < k) {
-        const float2 g = P::f(rg[j]);
-        u0 = F[0][j] * (g.x + u0);
-        u1 = F[1][j] * (g.y + u1);
+        const float2 g = P::f(gs[j * 32]);
+        u = mul2(F[j], add2(pk(g.x, g.y), u));
       }
-    wagg[par][warp][lane] = make_float4(p0, p1, q0, q1);
-    uagg[par][warp][lane] = make_float2(u0, u1);
+    runs[par][warp][lane] = run;
+    us[par][warp][lane] = u;
     __syncthreads();
-    // forward: state before this warp's first token
-    float2 hs = start;
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < warp) {
-        const float4 v = wagg[par][w][lane];
-        hs = make_float2(fmaf(v.x, hs.x, v.z), fmaf(v.y, hs.y, v.w));
-      }
-    // backward: what this warp's last token gets from the later ones
-    float4 post = make_float4(1.f, 1.f, 0.f, 0.f), all = post;
+    // every thread is through with the other stage (the step before)
+    if (threadIdx.x == 0 && s > 0 && s + 1 < steps && chunk(s + 1) < NC)
+      load_stage<T, 4>(sm, par ^ 1, maps, c0, chunk(s + 1) * kChunk, b, &full[par ^ 1]);
+    // what this warp's last token gets from the later ones: runs of (f products, u)
+    Run post = {pk(1.f), pk(0.f)}, all = post;
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
       if (w == warp) post = all;
-      const float4 v = wagg[par][w][lane];
-      const float2 u = uagg[par][w][lane];
-      all = make_float4(all.x * v.x, all.y * v.y, fmaf(v.x, all.z, u.x), fmaf(v.y, all.w, u.y));
+      const F2 f = runs[par][w][lane].f;
+      all = {mul2(all.f, f), fma2(f, all.h, us[par][w][lane])};
     }
-    float2 mine = carry;
     if (C > 1) {
-      if (warp < C) st_cluster(tc::mapa(tc::smem_u32(&cagg[par][rank][lane]), warp), all);
-      tc::cluster_sync();
-      for (int r = C - 1; r >= 0; --r) {
-        if (r == rank) mine = carry;
-        const float4 v = cagg[par][r][lane];
-        carry = make_float2(fmaf(v.x, carry.x, v.z), fmaf(v.y, carry.y, v.w));
-      }
-    } else {
-      carry = make_float2(fmaf(all.x, carry.x, all.z), fmaf(all.y, carry.y, all.w));
+      if (warp < C) st_cluster(tc::mapa(tc::smem_u32(&cruns[par][rank][lane]), warp), all);
+      cluster_arrive();
     }
-    float Hp[2][kTok];  // h_{t-1}
+    // state before this warp's first token, then before each of its tokens
+    F2 h = start;
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) {
+        const Run v = runs[par][w][lane];
+        h = fma2(v.f, h, v.h);
+      }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      Hp[0][j] = hs.x;
-      Hp[1][j] = hs.y;
-      hs = make_float2(fmaf(F[0][j], hs.x, Bx[0][j]), fmaf(F[1][j], hs.y, Bx[1][j]));
+      Q[j] = fma2(Q[j], pk(-1.f), h);  // h_{t-1} - f i x / m, whose product with u_t is dl
+      if (j < k) {
+        const float2 x = P::f(xs[j * 32]);
+        h = fma2(F[j], h, mul2(M[j], pk(x.x, x.y)));
+      }
     }
-    float v0 = fmaf(post.x, mine.x, post.z), v1 = fmaf(post.y, mine.y, post.w);
+    F2 mine = carry;
+    if (C > 1) {
+      cluster_wait();
+      for (int q = C - 1; q >= 0; --q) {
+        if (q == rank) mine = carry;
+        const Run v = cruns[par][q][lane];
+        carry = fma2(v.f, carry, v.h);
+      }
+    } else {
+      carry = fma2(all.f, carry, all.h);
+    }
+    F2 v = fma2(post.f, mine, post.h);
+    const size_t off = ((size_t)b * T_ + t0) * D + c;
 #pragma unroll
     for (int j = kTok - 1; j >= 0; --j)
       if (j < k) {
-        const float2 vx = P::f(rx[j]), vf = P::f(rf[j]), vg = P::f(rg[j]);
-        float o[3][2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float a = q ? a1 : a0, xx = q ? vx.y : vx.x, zf = q ? vf.y : vf.x;
-          const float g = (q ? vg.y : vg.x) + (q ? v1 : v0);
-          const float f = F[q][j], i = I[q][j], r = Wr[q][j];
-          const float u = f * g;
-          (q ? v1 : v0) = u;
-          // 1 - f^2 again from its reciprocal root, so that it stays out of the registers
-          const float m = r > 0.f ? rcp(r) : 0.f;
-          o[0][q] = g * m * i;
-          o[1][q] = g * Bx[q][j] * (1.f - i);
-          const float dl = u * (Hp[q][j] - i * xx * f * r);
-          const float e = ex2(-kLog2e * fabsf(zf)), den = rcp(1.f + e);
-          const float l = fmaxf(-a * (fmaxf(-zf, 0.f) + log1p01(e)), -1e30f);
-          o[2][q] = dl * a * (zf >= 0.f ? e * den : den);
-          (q ? da1 : da0) += dl * l;
-        }
-        const size_t at = off + (size_t)j * D;
-        __stcs(reinterpret_cast<V*>(dx + at), P::of(o[0][0], o[0][1]));
-        __stcs(reinterpret_cast<V*>(di + at), P::of(o[1][0], o[1][1]));
-        __stcs(reinterpret_cast<V*>(df + at), P::of(o[2][0], o[2][1]));
+        const int at = (warp * kTok + j) * 32 + lane;
+        const float2 vg = P::f(gs[j * 32]), x = P::f(xs[j * 32]);
+        const F2 g = add2(pk(vg.x, vg.y), v), gm = mul2(g, M[j]);
+        v = mul2(F[j], g);
+        const F2 dl = mul2(v, Q[j]);
+        const float Lx = *reinterpret_cast<const float*>(st + Cf::TILE + at * sizeof(V));
+        const float Ly = *reinterpret_cast<const float*>(st + 2 * Cf::TILE + at * sizeof(V));
+        da = fma2(dl, pk(Lx, Ly), da);
+        const size_t to = off + (size_t)j * D;
+        __stcs(reinterpret_cast<V*>(dx + to), P::of(gm));
+        __stcs(reinterpret_cast<V*>(di + to), P::of(mul2(mul2(gm, pk(x.x, x.y)), J[j])));
+        __stcs(reinterpret_cast<V*>(df + to), P::of(mul2(dl, keep[j * kWarps * 32])));
       }
+    tc::fence_proxy_async();  // the words written over f~ and i~, before the stage is loaded again
   }
-  if (dh0 && rank == 0 && warp == 0 && live) *reinterpret_cast<float2*>(dh0 + (size_t)b * D + c) = carry;
+  if (dh0 && rank == 0 && warp == 0 && live) *reinterpret_cast<F2*>(dh0 + (size_t)b * D + c) = carry;
   // da_log: the warps' sums in a fixed order, one row per CTA of the cluster
   __syncthreads();
-  uagg[0][warp][lane] = make_float2(da0, da1);
+  us[0][warp][lane] = da;
   __syncthreads();
   if (warp == 0 && live) {
-    float2 t = make_float2(0.f, 0.f);
+    F2 t = pk(0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 v = uagg[0][w][lane];
-      t.x += v.x;
-      t.y += v.y;
-    }
-    *reinterpret_cast<float2*>(part + ((size_t)b * C + rank) * D + c) = t;
+    for (int w = 0; w < kWarps; ++w) t = add2(t, us[0][w][lane]);
+    *reinterpret_cast<F2*>(part + ((size_t)b * C + rank) * D + c) = mul2(t, pk(kLn2));
   }
 }
 
@@ -386,12 +498,11 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const T* __restrict__ x
   const int c = (int)(at % D);
   const float2 vx = P::f(*reinterpret_cast<const V*>(x + at)), vi = P::f(*reinterpret_cast<const V*>(ip + at));
   const float2 vf = P::f(*reinterpret_cast<const V*>(fp + at));
-  float2 s = *reinterpret_cast<const float2*>(h + at);
-  const Gates g0 = gates(vf.x, vi.x, expf(a_log[c])), g1 = gates(vf.y, vi.y, expf(a_log[c + 1]));
-  s.x = fmaf(g0.f, s.x, g0.w * inv_m(g0.w) * g0.i * vx.x);
-  s.y = fmaf(g1.f, s.y, g1.w * inv_m(g1.w) * g1.i * vx.y);
-  *reinterpret_cast<float2*>(h + at) = s;
-  *reinterpret_cast<V*>(out + at) = P::of(s.x, s.y);
+  const F2 s = *reinterpret_cast<const F2*>(h + at);
+  const Gates g = gates<false>(vf, vi, pk(-kLog2e * expf(a_log[c]), -kLog2e * expf(a_log[c + 1])));
+  const F2 y = fma2(g.f, s, mul2(mul2(mul2(g.w, inv_m(g.w)), g.i), pk(vx.x, vx.y)));
+  *reinterpret_cast<F2*>(h + at) = y;
+  *reinterpret_cast<V*>(out + at) = P::of(y);
 }
 
 // CTAs of a cluster (chunks taken at a time): enough CTAs for two on each of
@@ -404,10 +515,13 @@ int cluster_size(const GlrArgs& a, int NC) {
 }
 
 template <typename K, typename... A>
-cudaError_t launch_cluster(K kernel, dim3 grid, int C, cudaStream_t st, A... args) {
+cudaError_t launch_cluster(K kernel, dim3 grid, int C, size_t smem, cudaStream_t st, A... args) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -418,15 +532,22 @@ cudaError_t launch_cluster(K kernel, dim3 grid, int C, cudaStream_t st, A... arg
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// a chunk's tile of a [B,T,D] tensor: 64 channels of 64 tokens
+template <typename T>
+bool tile_map(CUtensorMap* m, const GlrArgs& a, const void* p) {
+  return make_tmap_bthd(m, p, sizeof(T), a.B, a.T, 1, a.D, kChans, false, kChunk);
+}
+
 template <typename T>
 cudaError_t glr_fwd_t(const GlrArgs& a, cudaStream_t st) {
   const int NC = (a.T + kChunk - 1) / kChunk, C = cluster_size(a, NC);
   const dim3 grid((unsigned)((a.D + kChans - 1) / kChans) * C, a.B);
+  CUtensorMap mx, mi, mf;
+  if (!tile_map<T>(&mx, a, a.x) || !tile_map<T>(&mi, a, a.i_pre) || !tile_map<T>(&mf, a, a.f_pre))
+    return cudaErrorInvalidValue;
   prof_begin(st, "glr_fwd");
-  const cudaError_t e =
-      launch_cluster(glr_fwd_kernel<T>, grid, C, st, static_cast<const T*>(a.x), static_cast<const T*>(a.i_pre),
-                     static_cast<const T*>(a.f_pre), a.a_log, a.h0, static_cast<T*>(a.out), a.hT, a.states, a.T, a.D,
-                     NC, C);
+  const cudaError_t e = launch_cluster(glr_fwd_kernel<T>, grid, C, GlrCfg<T, 3>::BYTES, st, mx, mi, mf, a.a_log, a.h0,
+                                       static_cast<T*>(a.out), a.hT, a.states, a.T, a.D, NC, C, a.err);
   prof_end(st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -435,12 +556,14 @@ template <typename T>
 cudaError_t glr_bwd_t(const GlrArgs& a, cudaStream_t st) {
   const int NC = (a.T + kChunk - 1) / kChunk, C = cluster_size(a, NC);
   const dim3 grid((unsigned)((a.D + kChans - 1) / kChans) * C, a.B);
+  CUtensorMap mx, mi, mf, mg;
+  if (!tile_map<T>(&mx, a, a.x) || !tile_map<T>(&mi, a, a.i_pre) || !tile_map<T>(&mf, a, a.f_pre) ||
+      !tile_map<T>(&mg, a, a.dh))
+    return cudaErrorInvalidValue;
   prof_begin(st, "glr_bwd");
-  cudaError_t e =
-      launch_cluster(glr_bwd_kernel<T>, grid, C, st, static_cast<const T*>(a.x), static_cast<const T*>(a.i_pre),
-                     static_cast<const T*>(a.f_pre), a.a_log, a.states_in, static_cast<const T*>(a.dh), a.dhT,
-                     static_cast<T*>(a.dx), static_cast<T*>(a.di_pre), static_cast<T*>(a.df_pre), a.part, a.dh0, a.T,
-                     a.D, NC, C);
+  cudaError_t e = launch_cluster(glr_bwd_kernel<T>, grid, C, GlrCfg<T, 4>::BYTES, st, mx, mi, mf, mg, a.a_log,
+                                 a.states_in, a.dhT, static_cast<T*>(a.dx), static_cast<T*>(a.di_pre),
+                                 static_cast<T*>(a.df_pre), a.part, a.dh0, a.T, a.D, NC, C, a.err);
   prof_end(st);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -101,6 +101,7 @@ struct GlrArgs {
   const float* states_in;  // backward
   float* part;             // backward: parts of da_log [B][cluster][D]
   int B, T, D, dtype;
+  int* err = nullptr;      // the library's device error word
 };
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t st);
 cudaError_t launch_glr_bwd(const GlrArgs& a, cudaStream_t st);

@@ -7,12 +7,21 @@
 // in an order that a softmax does not depend on.
 //
 // HBM-bound: every key and value in use is read once, for all query heads of
-// its group.  A row of d channels is one 16-byte vector per lane, so a warp
-// takes 32 / (d / vector) keys at a time: dot products per lane, a butterfly
-// over the row's lanes, one running maximum and sum per warp and head, and
-// the values weighted in the same layout.  A warp's lanes hold partial sums
-// over its keys; they are joined at the end, over the warps through shared
-// memory, and over the parts of a long cache by a second kernel.
+// its group.  The parts of a long cache are joined by a second kernel.
+//
+// bf16: m16n8k16 products, the (up to 16) query heads of a key head as the 16
+// rows.  tcgen05 would want 128 rows, of which a group fills 1 to 16, and the
+// products are an eighth of what the tensor cores can do while the cache
+// streams in; what matters is that the cache's bytes are in flight.  So each
+// warp works alone: its own ring of 16-key tiles, filled by 16-byte async
+// copies two tiles ahead, its own running maximum and sum, and no barrier
+// until the warps' results are joined.  The weights go into the value product
+// as bf16 high and low parts (2^-16 of themselves): the second product costs
+// nothing here, and the output is as exact as with fp32 weights.
+//
+// fp32: CUDA cores.  A row of d channels is one 16-byte vector per lane, so a
+// warp takes 32 / (d / 4) keys at a time: dot products per lane, a butterfly
+// over the row's lanes, the values weighted in the same layout.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 
@@ -56,7 +65,7 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
   const int n = pos < 0 ? 0 : pos + 1 < slots ? (int)pos + 1 : slots;
   const int mine = pos < 0 ? -1 : (int)slot_of(pos, a.window, a.sinks);
   const int per = (n + a.splits - 1) / a.splits;
-  const int lo = blockIdx.x * per < n ? blockIdx.x * per : n, hi = lo + per < n ? lo + per : n;
+  const int lo = (int)min((long long)blockIdx.x * per, (long long)n), hi = min((long long)lo + per, (long long)n);
 
   const size_t pitch = (size_t)a.Hk * D;
   T* kc = static_cast<T*>(a.k_cache) + (b * slots * a.Hk + hk) * D;
@@ -170,6 +179,229 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
   }
 }
 
+// ---- bf16 -------------------------------------------------------------------
+
+template <int D>
+struct MmaCfg {
+  static constexpr int CH = D / 8;              // 16-byte chunks of a row
+  static constexpr int TILE = 16 * D * 2;       // bytes of 16 keys (or values)
+  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int WARP = STAGES * 2 * TILE;
+  static constexpr int BYTES = kWarps * WARP;
+  // byte offset of chunk c of row r: the eight rows that one ldmatrix reads at
+  // a chunk lie in eight different 16-byte bank groups
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return (uint32_t)(r * CH + (D == 32 ? c ^ ((r >> 1) & 3) : c ^ (r & 7))) * 16u;
+  }
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {  // zeros where !in
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <bool kTrans>
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  if (kTrans)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// the part of (lo, hi) that pack2 leaves
+__device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t packed) {
+  return pack2(lo - __uint_as_float(packed << 16), hi - __uint_as_float(packed & 0xffff0000u));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecodeArgs a) {
+  using Cf = MmaCfg<D>;
+  using T = __nv_bfloat16;
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ float sh_m[kWarps][16], sh_l[kWarps][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+  const int group = a.H / a.Hk, chunks = (group + 15) / 16;
+  const int hk = blockIdx.y / chunks, g0 = blockIdx.y % chunks * 16, heads = min(16, group - g0);
+  const size_t b = blockIdx.z;
+  const int slots = a.window + a.sinks;
+  const long long pos = a.pos[b];
+  const int n = pos < 0 ? 0 : pos + 1 < slots ? (int)pos + 1 : slots;
+  const int mine = pos < 0 ? -1 : (int)slot_of(pos, a.window, a.sinks);
+  const int per = (n + a.splits - 1) / a.splits;
+  const int lo = (int)min((long long)blockIdx.x * per, (long long)n), hi = (int)min((long long)lo + per, (long long)n);
+
+  const size_t pitch = (size_t)a.Hk * D;
+  T* kc = static_cast<T*>(a.k_cache) + (b * slots * a.Hk + hk) * D;
+  T* vc = static_cast<T*>(a.v_cache) + (b * slots * a.Hk + hk) * D;
+  const T* kn = static_cast<const T*>(a.k) + (b * a.Hk + hk) * D;
+  const T* vn = static_cast<const T*>(a.v) + (b * a.Hk + hk) * D;
+  const uint32_t ring = smem_addr(sm) + warp * Cf::WARP;
+  const int tiles = hi - lo > warp * 16 ? (hi - lo - warp * 16 + kWarps * 16 - 1) / (kWarps * 16) : 0;
+
+  const auto load = [&](int it) {
+    if (it < tiles) {
+      const int j0 = lo + (it * kWarps + warp) * 16;
+      const uint32_t dst = ring + it % Cf::STAGES * 2 * Cf::TILE;
+#pragma unroll
+      for (int i = 0; i < Cf::CH / 2; ++i) {
+        const int r = (lane + 32 * i) / Cf::CH, c = (lane + 32 * i) % Cf::CH, j = j0 + r;
+        const bool in = j < hi, fresh = j == mine;  // the new token comes from the arguments
+        const size_t off = (size_t)(in ? j : lo) * pitch;
+        copy16(dst + Cf::at(r, c), (fresh ? kn : kc + off) + c * 8, in);
+        copy16(dst + Cf::TILE + Cf::at(r, c), (fresh ? vn : vc + off) + c * 8, in);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < Cf::STAGES - 1; ++i) load(i);
+  // The new token is stored by one CTA; all read it from the arguments.
+  if (mine >= lo && mine < hi && g0 == 0 && warp == 0 && lane < Cf::CH) {
+    *reinterpret_cast<uint4*>(kc + mine * pitch + lane * 8) = *reinterpret_cast<const uint4*>(kn + lane * 8);
+    *reinterpret_cast<uint4*>(vc + mine * pitch + lane * 8) = *reinterpret_cast<const uint4*>(vn + lane * 8);
+  }
+
+  uint32_t q[D / 16][4];
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = g + (i & 1) * 8, c = s * 16 + (i >> 1) * 8 + tq * 2;
+      q[s][i] = r < heads ? *reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) +
+                                                               (b * a.H + hk * group + g0 + r) * D + c)
+                          : 0u;
+    }
+  float o[D / 8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  const float s2 = a.scale * kLog2e;
+  const int mat = lane >> 3, mr = lane & 7;
+  for (int it = 0; it < tiles; ++it) {
+    copy_wait<Cf::STAGES - 2>();
+    __syncwarp();
+    load(it + Cf::STAGES - 1);
+    const uint32_t kt = ring + it % Cf::STAGES * 2 * Cf::TILE, vt = kt + Cf::TILE;
+    float x[2][4] = {};
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      uint32_t f[4];  // keys 0-7 and 8-15, channels 16s .. 16s + 15
+      ldm4<false>(kt + Cf::at((mat >> 1) * 8 + mr, 2 * s + (mat & 1)), f);
+      mma16816(x[0], q[s], f[0], f[1]);
+      mma16816(x[1], q[s], f[2], f[3]);
+    }
+    const int j0 = lo + (it * kWarps + warp) * 16;
+    float t0 = m0, t1 = m1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[h][e] = j0 + h * 8 + tq * 2 + (e & 1) < hi ? x[h][e] * s2 : -INFINITY;
+        if (e < 2) t0 = fmaxf(t0, x[h][e]);
+        else t1 = fmaxf(t1, x[h][e]);
+      }
+#pragma unroll
+    for (int w = 1; w <= 2; w <<= 1) {
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+    }
+    if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {  // both finite: a tile has a key in range
+      const float f0 = ex2(m0 - t0), f1 = ex2(m1 - t1);
+      m0 = t0;
+      m1 = t1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= f0;
+        o[i][1] *= f0;
+        o[i][2] *= f1;
+        o[i][3] *= f1;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[h][e] = ex2(x[h][e] - (e < 2 ? m0 : m1));
+        if (e < 2) l0 += x[h][e];
+        else l1 += x[h][e];
+      }
+    const uint32_t ph[4] = {pack2(x[0][0], x[0][1]), pack2(x[0][2], x[0][3]), pack2(x[1][0], x[1][1]),
+                            pack2(x[1][2], x[1][3])};
+    const uint32_t pl[4] = {rest2(x[0][0], x[0][1], ph[0]), rest2(x[0][2], x[0][3], ph[1]),
+                            rest2(x[1][0], x[1][1], ph[2]), rest2(x[1][2], x[1][3], ph[3])};
+#pragma unroll
+    for (int c = 0; c < Cf::CH; c += 2) {
+      uint32_t f[4];  // values: channels 8c .. 8c + 7 of keys 0-7, 8-15, then the next eight channels
+      ldm4<true>(vt + Cf::at((mat & 1) * 8 + mr, c + (mat >> 1)), f);
+      mma16816(o[c], ph, f[0], f[1]);
+      mma16816(o[c + 1], ph, f[2], f[3]);
+      mma16816(o[c], pl, f[0], f[1]);
+      mma16816(o[c + 1], pl, f[2], f[3]);
+    }
+    __syncwarp();  // the slot is filled again by all lanes in the next round
+  }
+  copy_wait<0>();
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(sm);  // [warp][16][D] over the rings
+#pragma unroll
+  for (int w = 1; w <= 2; w <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+  }
+  if (tq == 0) {
+    sh_m[warp][g] = m0;
+    sh_m[warp][g + 8] = m1;
+    sh_l[warp][g] = l0;
+    sh_l[warp][g + 8] = l1;
+  }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    *reinterpret_cast<float2*>(so + (warp * 16 + g) * D + i * 8 + tq * 2) = make_float2(o[i][0], o[i][1]);
+    if (heads > 8)
+      *reinterpret_cast<float2*>(so + (warp * 16 + g + 8) * D + i * 8 + tq * 2) = make_float2(o[i][2], o[i][3]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * D; i += kWarps * 32) {
+    const int r = i / D, ch = i % D, h = hk * group + g0 + r;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][r]);
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sh_m[w][r] == -INFINITY ? 0.f : ex2(sh_m[w][r] - top);
+      sum = fmaf(f, sh_l[w][r], sum);
+      acc = fmaf(f, so[(w * 16 + r) * D + ch], acc);
+    }
+    if (a.splits == 1) {
+      static_cast<T*>(a.out)[(b * a.H + h) * D + ch] = from_f<T>(n ? acc / sum : 0.f);
+    } else {
+      float* part = a.part + ((b * a.H + h) * a.splits + blockIdx.x) * (size_t)(D + 2);
+      part[2 + ch] = acc;
+      if (ch == 0) {
+        part[0] = top;
+        part[1] = sum;
+      }
+    }
+  }
+}
+
 // Joins the parts of one head: weights of the parts first, then the channels.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restrict__ part, int splits,
@@ -188,13 +420,12 @@ __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restr
   out[(size_t)blockIdx.x * D + threadIdx.x] = from_f<T>(sum > 0.f ? acc / sum : 0.f);
 }
 
-template <typename T, int D, int GC>
-cudaError_t decode_gc(const SwaDecodeArgs& a, cudaStream_t st) {
-  const int chunks = (a.H / a.Hk + GC - 1) / GC;
-  prof_begin(st, "swa_decode");
-  swa_decode_kernel<T, D, GC><<<dim3(a.splits, a.Hk * chunks, a.B), kWarps * 32, 0, st>>>(a);
-  prof_end(st);
-  cudaError_t e = cudaGetLastError();
+// query heads of a key head that one CTA takes
+int heads_per_cta(int group, int dtype) { return dtype == 1 ? 16 : group >= 3 ? 4 : group; }
+
+template <typename T, int D>
+cudaError_t join(const SwaDecodeArgs& a, cudaStream_t st) {
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.splits == 1) return e;
   prof_begin(st, "swa_decode_join");
   swa_decode_join_kernel<T, D><<<a.B * a.H, D, 0, st>>>(a.part, a.splits, static_cast<T*>(a.out));
@@ -202,20 +433,33 @@ cudaError_t decode_gc(const SwaDecodeArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-int heads_per_cta(int group) { return group >= 3 ? 4 : group; }
-
-template <typename T, int D>
-cudaError_t decode_d(const SwaDecodeArgs& a, cudaStream_t st) {
-  switch (heads_per_cta(a.H / a.Hk)) {
-    case 1: return decode_gc<T, D, 1>(a, st);
-    case 2: return decode_gc<T, D, 2>(a, st);
-    default: return decode_gc<T, D, 4>(a, st);
-  }
+dim3 decode_grid(const SwaDecodeArgs& a) {
+  const int gc = heads_per_cta(a.H / a.Hk, a.dtype);
+  return dim3(a.splits, a.Hk * ((a.H / a.Hk + gc - 1) / gc), a.B);
 }
 
-template <typename T>
-cudaError_t decode_t(const SwaDecodeArgs& a, cudaStream_t st) {
-  return a.d == 32 ? decode_d<T, 32>(a, st) : a.d == 64 ? decode_d<T, 64>(a, st) : decode_d<T, 128>(a, st);
+template <int D>
+cudaError_t decode_f32(const SwaDecodeArgs& a, cudaStream_t st) {
+  prof_begin(st, "swa_decode");
+  switch (heads_per_cta(a.H / a.Hk, 0)) {
+    case 1: swa_decode_kernel<float, D, 1><<<decode_grid(a), kWarps * 32, 0, st>>>(a); break;
+    case 2: swa_decode_kernel<float, D, 2><<<decode_grid(a), kWarps * 32, 0, st>>>(a); break;
+    default: swa_decode_kernel<float, D, 4><<<decode_grid(a), kWarps * 32, 0, st>>>(a);
+  }
+  prof_end(st);
+  return join<float, D>(a, st);
+}
+
+template <int D>
+cudaError_t decode_bf16(const SwaDecodeArgs& a, cudaStream_t st) {
+  using Cf = MmaCfg<D>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(swa_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::BYTES);
+  if (e != cudaSuccess) return e;
+  prof_begin(st, "swa_decode");
+  swa_decode_mma_kernel<D><<<decode_grid(a), kWarps * 32, Cf::BYTES, st>>>(a);
+  prof_end(st);
+  return join<__nv_bfloat16, D>(a, st);
 }
 
 // Per slot: the newest of the first n tokens that belongs there.
@@ -243,7 +487,7 @@ __global__ void __launch_bounds__(256) swa_fill_kernel(const uint4* __restrict__
 // Parts of a cache: enough CTAs for four on each of 148 SMs, but at least 64
 // slots to a part.
 int swa_decode_splits(int B, int H, int Hk, int d, int window, int sinks, int dtype) {
-  const int gc = heads_per_cta(H / Hk);
+  const int gc = heads_per_cta(H / Hk, dtype);
   const long long units = (long long)B * Hk * ((H / Hk + gc - 1) / gc);
   const long long most = ((long long)window + sinks + 63) / 64;
   long long s = (592 + units - 1) / units;
@@ -256,7 +500,9 @@ size_t swa_decode_bytes(int B, int H, int d, int splits) {
 }
 
 cudaError_t launch_swa_decode(const SwaDecodeArgs& a, cudaStream_t st) {
-  return a.dtype == 1 ? decode_t<__nv_bfloat16>(a, st) : decode_t<float>(a, st);
+  if (a.dtype == 1)
+    return a.d == 32 ? decode_bf16<32>(a, st) : a.d == 64 ? decode_bf16<64>(a, st) : decode_bf16<128>(a, st);
+  return a.d == 32 ? decode_f32<32>(a, st) : a.d == 64 ? decode_f32<64>(a, st) : decode_f32<128>(a, st);
 }
 
 cudaError_t launch_swa_fill(const SwaFillArgs& a, cudaStream_t st) {

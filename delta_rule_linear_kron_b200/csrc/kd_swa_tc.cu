@@ -16,7 +16,10 @@
 // exponentials take as long as the two products of that tile at d = 128).  The
 // output stays in TMEM; it is rescaled only when a row's maximum has grown by
 // more than 2^8 over the one its sums refer to (then p <= 2^8, still exact
-// enough in bf16, whose precision does not depend on the size).
+// enough in bf16, whose precision does not depend on the size).  Short rows
+// (kFine) take the weights as bf16 high and low parts: over a few keys the
+// roundings of p do not average out, and the backward's delta = dO.o would
+// pass them on to every gradient.
 //
 // Backward: p is recomputed from the saved lse.  dk, dv: 128 keys per CTA
 // (rows are keys: S^T = k q^T, dP^T = v dO^T), 64 queries at a time, the two
@@ -112,7 +115,7 @@ struct FwdCfg {
   static constexpr int S_COL = 0, O_COL = 256;    // 128 columns per group each
 };
 
-template <int D>
+template <int D, bool kFine>
 __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
     const __grid_constant__ CUtensorMap tv, SwaArgs a) {
@@ -206,9 +209,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
             tc::mbar_wait<false>(&p_full[i], p_use[i]++ & 1, a.err, tc::kErrTimeoutMma, ab);
             tc::tc_after_sync();
 #pragma unroll
-            for (int s = 0; s < 8; ++s)  // O_i += P_i v
+            for (int s = 0; s < (kFine ? 16 : 8); ++s)  // O_i += P_i v
               tc::mma_bf16_ts(tmem + Cf::O_COL + i * 128, tmem + Cf::S_COL + i * 128 + s * 8,
-                              tc::desc_sw128_mn(v + s * 2048, 16384u), ID_O, started[i] || s > 0);
+                              tc::desc_sw128_mn(v + s % 8 * 2048, 16384u), ID_O, started[i] || s > 0);
             started[i] = true;
             if (kt == mine[i].end) tc::mma_commit(&o_full[i]);
           }
@@ -274,6 +277,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
           w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
         }
         tc::tmem_st16(s_lane + c / 2, w);
+        if (kFine) {  // what the rounding left, behind the 64 columns of the high parts
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint32_t hi = __float_as_uint(w[e / 2]);
+            w[e / 2] = bf16_pair(x[c + e] - __uint_as_float(hi << 16), x[c + e + 1] - __uint_as_float(hi & 0xffff0000u));
+          }
+          tc::tmem_st16(s_lane + 64 + c / 2, w);
+        }
       }
       tc::tmem_st_wait();
       tc::tc_before_sync();
@@ -626,7 +637,12 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <int D>
+// Rows of at most this many keys take the finer weights.  Measured with bf16
+// gradients, relative to their own rounding (1.41 is what rounding dS alone
+// costs): dq 1.72 at 1 to 2 keys, 1.52 at 9, 1.45 at 129 with one bf16 weight.
+constexpr int kFineKeys = 256;
+
+template <int D, bool kFine>
 cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
   using Cf = FwdCfg<D>;
   CUtensorMap tq, tk, tv;
@@ -634,10 +650,10 @@ cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
       !make_tmap_bthd(&tk, a.k, 2, a.B, a.T, a.Hk, D, 64, true, 128) ||
       !make_tmap_bthd(&tv, a.v, 2, a.B, a.T, a.Hk, D, 64, true, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(swa_fwd_tc_kernel<D>, Cf::BYTES);
+  cudaError_t e = allow_smem(swa_fwd_tc_kernel<D, kFine>, Cf::BYTES);
   if (e != cudaSuccess) return e;
   prof_begin(st, "swa_fwd_tc");
-  swa_fwd_tc_kernel<D><<<dim3((a.T + 255) / 256, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(tq, tk, tv, a);
+  swa_fwd_tc_kernel<D, kFine><<<dim3((a.T + 255) / 256, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(tq, tk, tv, a);
   prof_end(st);
   return cudaGetLastError();
 }
@@ -673,7 +689,11 @@ cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
 }  // namespace
 
 bool swa_tc_supported(int d, int dtype) { return dtype == 1 && (d == 64 || d == 128); }
-cudaError_t launch_swa_fwd_tc(const SwaArgs& a, cudaStream_t st) { return a.d == 64 ? fwd_go<64>(a, st) : fwd_go<128>(a, st); }
+cudaError_t launch_swa_fwd_tc(const SwaArgs& a, cudaStream_t st) {
+  const int keys = a.window + a.sinks < a.T ? a.window + a.sinks : a.T;  // window, sinks <= T
+  if (keys <= kFineKeys) return a.d == 64 ? fwd_go<64, true>(a, st) : fwd_go<128, true>(a, st);
+  return a.d == 64 ? fwd_go<64, false>(a, st) : fwd_go<128, false>(a, st);
+}
 cudaError_t launch_swa_bwd_tc(const SwaArgs& a, cudaStream_t st) { return a.d == 64 ? bwd_go<64>(a, st) : bwd_go<128>(a, st); }
 
 }  // namespace kd

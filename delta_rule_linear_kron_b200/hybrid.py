@@ -11,10 +11,10 @@ the call runs on the current stream of the tensors' device, or on `stream`.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 import math
 
-from . import (KD_ERR_INVALID_ARG, KronDeltaError, _alloc_ws, _check, _dtype_code, _need, _ptr, lib)
+from . import (KD_ERR_INVALID_ARG, KronDeltaError, _alloc_ws, _check, _dtype_code, _need, lib)
 
 KD_SWA_WS_SAVE, KD_SWA_WS_BWD, KD_SWA_WS_DECODE = 0, 1, 2
 KD_GLR_WS_SAVE, KD_GLR_WS_BWD = 0, 1
@@ -36,21 +36,61 @@ def _dims(t, name, n):
     return t.shape
 
 
-def _call(fn, tensors, stream, *args):
-    """Runs fn(*args, stream) on the device that holds all of `tensors`."""
+def _device(t, name):
+    """Ordinal of the CUDA device that the call's tensors share."""
+    dev = t.get_device()
+    if dev < 0:
+        _need(t, name)
+    return dev
+
+
+def _arg(t, name, dev, dtype, shape):
+    """The checked tensor's address (None for None).  One short test on the way
+    of a good argument: these run on every decode step."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise _invalid(f"{name} is on {t.device}, the call's first tensor on device {dev}")
+
+
+def _bytes_arg(t, name, dev):
+    """Address and size of a workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _need(t, name)
+        raise _invalid(f"{name} is on {t.device}, the call's first tensor on device {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _streamed(fn):
+    """The public form of a function: with `stream`, all of it runs under that
+    stream, what it allocates too, so that the allocator hands none of that
+    memory to another stream while the call's kernels use it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        first = args[0] if args else next(iter(kw.values()))
+        if first.device != stream.device:
+            raise _invalid(f"stream belongs to {stream.device} but the call's tensors are on {first.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) on device `dev` and its current stream."""
     import torch
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise _invalid(f"tensors on {dev} and {t.device} in one call")
-    other = dev.index != torch.cuda.current_device()
-    with torch.cuda.device(dev) if other else contextlib.nullcontext():
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        _check(fn(*args, s.cuda_stream))
-
-
-def _nbytes(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    s = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        _check(fn(*args, s))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s))
 
 
 def _size(n):
@@ -109,35 +149,33 @@ def rotary_freqs(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, trained_
     return w.to(device), scale
 
 
-def _rotary(q, k, freqs, pos, interleaved, scale, inverse, out, stream):
+def _rotary(q, k, freqs, pos, interleaved, scale, inverse, out):
     import torch
-    step = q.dim() == 3  # one token per sequence: [B,H,d], pos [B]
-    if not step:
-        _dims(q, "q", 4)
-    B, T = q.shape[0], 1 if step else q.shape[1]
-    H, d = q.shape[-2:]
-    lead = tuple(q.shape[:-2])
-    _need(q, "q")
-    Hk = 0
-    if k is not None:
-        _dims(k, "k", q.dim())
-        Hk = k.shape[-2]
-        _need(k, "k", q.dtype, (*lead, Hk, d))
-    _dims(freqs, "freqs", 1)
-    _need(freqs, "freqs", torch.float64)
-    _need(pos, "pos", torch.int64, lead)
+    shape = q.shape
+    if len(shape) == 4:
+        B, T, H, d = shape
+    else:  # one token per sequence: [B,H,d], pos [B]
+        B, H, d = _dims(q, "q", 3)
+        T = 1
+    lead, dev, dtype = shape[:-2], _device(q, "q"), q.dtype
     dt = _dtype_code(q)
+    Hk, k_shape = 0, None
+    if k is not None:
+        k_shape = _dims(k, "k", len(shape))
+        Hk = k_shape[-2]
+    half = _dims(freqs, "freqs", 1)[0]
     oq, ok = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
-    _need(oq, "out[0]", q.dtype, q.shape)
     if (ok is None) != (k is None):
         raise _invalid("out must be a pair like (q, k)")
-    if k is not None:
-        _need(ok, "out[1]", q.dtype, k.shape)
-    _call(lib().kron_delta_rotary, (q, k, freqs, pos, oq, ok), stream, _ptr(q), _ptr(k), _ptr(freqs), _ptr(pos),
-          _ptr(oq), _ptr(ok), B, T, H, Hk, d, 2 * freqs.shape[0], int(bool(interleaved)), inverse, float(scale), dt)
+    kk = (*lead, Hk, d)
+    _call(lib().kron_delta_rotary, dev, _arg(q, "q", dev, dtype, shape), _arg(k, "k", dev, dtype, kk),
+          _arg(freqs, "freqs", dev, torch.float64, (half,)), _arg(pos, "pos", dev, torch.int64, lead),
+          _arg(oq, "out[0]", dev, dtype, shape), _arg(ok, "out[1]", dev, dtype, kk), B, T, H, Hk, d, 2 * half,
+          1 if interleaved else 0, inverse, scale, dt)
     return oq, ok
 
 
+@_streamed
 def rotary_fwd(q, k, freqs, pos=None, *, interleaved=False, scale=1.0, out=None, stream=None):
     """Rotary positions: pair j of the first 2*len(freqs) channels turns by
     pos*freqs[j] and is scaled by `scale`; the other channels are copied.
@@ -145,69 +183,69 @@ def rotary_fwd(q, k, freqs, pos=None, *, interleaved=False, scale=1.0, out=None,
     or None for 0..T-1.  One token per sequence: q [B,H,d], k [B,Hk,d], pos [B].
     Pair j is channels (j, j + len(freqs)), or (2j, 2j+1) with interleaved.
     out=(q, k) works in place.  Returns (q, k) rotated."""
-    return _rotary(q, k, freqs, pos, interleaved, scale, 0, out, stream)
+    return _rotary(q, k, freqs, pos, interleaved, scale, 0, out)
 
 
+@_streamed
 def rotary_bwd(dq, dk, freqs, pos=None, *, interleaved=False, scale=1.0, out=None, stream=None):
     """Backward of rotary_fwd: the gradients of q and k from those of its
     outputs (the rotation by -pos*freqs[j])."""
-    return _rotary(dq, dk, freqs, pos, interleaved, scale, 1, out, stream)
+    return _rotary(dq, dk, freqs, pos, interleaved, scale, 1, out)
 
 
 # ---- attention over a sliding window with first tokens kept -----------------
 
 
 def _swa_inputs(q, k, v):
-    B, T, H, d = _dims(q, "q", 4)
+    """Sizes, dtype code, device and the three addresses."""
+    shape = _dims(q, "q", 4)
+    B, T, H, d = shape
     Hk = _dims(k, "k", 4)[2]
-    _need(q, "q"); _need(k, "k", q.dtype, (B, T, Hk, d)); _need(v, "v", q.dtype, (B, T, Hk, d))
-    return B, T, H, Hk, d, _dtype_code(q)
+    dev, dtype, kv = _device(q, "q"), q.dtype, (B, T, Hk, d)
+    return B, T, H, Hk, d, _dtype_code(q), dev, (_arg(q, "q", dev, dtype, shape), _arg(k, "k", dev, dtype, kv),
+                                                 _arg(v, "v", dev, dtype, kv))
 
 
 def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
 
+@_streamed
 def swa_fwd(q, k, v, window, sinks=0, *, scale=None, out=None, save=False, workspace=None, stream=None):
     """Causal attention where query t sees key j when j <= t and (t - j < window
     or j < sinks).  q [B,T,H,d], k, v [B,T,Hk,d] (bf16 or fp32), H a multiple of
     Hk; scale defaults to 1/sqrt(d).  Returns (out [B,T,H,d], lse [B,T,H] fp32,
     workspace or None); pass all three (save=True) to swa_bwd."""
     import torch
-    B, T, H, Hk, d, dt = _swa_inputs(q, k, v)
+    B, T, H, Hk, d, dt, dev, ptrs = _swa_inputs(q, k, v)
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", q.dtype, q.shape)
     lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
     if save and workspace is None:
         n = swa_workspace_size(KD_SWA_WS_SAVE, B, T, H, Hk, d, window, sinks, dt)
         workspace = _alloc_ws(n, q.device) if n else None
-    _call(lib().kron_delta_swa_fwd, (q, k, v, out, workspace), stream, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-          B, T, H, Hk, d, window, sinks, _scale(scale, d), dt, _ptr(workspace), _nbytes(workspace), int(bool(save)))
+    _call(lib().kron_delta_swa_fwd, dev, *ptrs, _arg(out, "out", dev, q.dtype, q.shape), lse.data_ptr(), B, T,
+          H, Hk, d, window, sinks, _scale(scale, d), dt, *_bytes_arg(workspace, "workspace", dev), 1 if save else 0)
     return out, lse, workspace
 
 
+@_streamed
 def swa_bwd(q, k, v, out, lse, dO, window, sinks=0, *, scale=None, fwd_workspace, workspace=None, stream=None):
     """Backward of swa_fwd for the loss <dO, out>, from its three results.
     Returns dict dq, dk, dv (summed in a fixed order: bitwise reproducible)."""
     import torch
-    B, T, H, Hk, d, dt = _swa_inputs(q, k, v)
-    _need(out, "out", q.dtype, q.shape); _need(dO, "dO", q.dtype, q.shape)
-    _need(lse, "lse", torch.float32, (B, T, H))
+    B, T, H, Hk, d, dt, dev, ptrs = _swa_inputs(q, k, v)
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
     if workspace is None:
         workspace = _alloc_ws(swa_workspace_size(KD_SWA_WS_BWD, B, T, H, Hk, d, window, sinks, dt), q.device)
-    _call(lib().kron_delta_swa_bwd, (q, k, v, out, lse, dO, fwd_workspace, workspace), stream, _ptr(q), _ptr(k),
-          _ptr(v), _ptr(out), _ptr(lse), _ptr(dO), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), B, T, H, Hk, d,
-          window, sinks, _scale(scale, d), dt, _ptr(fwd_workspace), _nbytes(fwd_workspace), _ptr(workspace),
-          _nbytes(workspace))
+    _call(lib().kron_delta_swa_bwd, dev, *ptrs, _arg(out, "out", dev, q.dtype, q.shape),
+          _arg(lse, "lse", dev, torch.float32, (B, T, H)), _arg(dO, "dO", dev, q.dtype, q.shape), g["dq"].data_ptr(),
+          g["dk"].data_ptr(), g["dv"].data_ptr(), B, T, H, Hk, d, window, sinks, _scale(scale, d), dt,
+          *_bytes_arg(fwd_workspace, "fwd_workspace", dev), *_bytes_arg(workspace, "workspace", dev))
     return g
 
 
-def _swa_cache(cache, name, B, slots, Hk, d, dtype):
-    _need(cache, name, dtype, (B, slots, Hk, d))
-
-
+@_streamed
 def swa_decode(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, out=None, workspace=None,
                stream=None):
     """One decode step of swa_fwd's attention.  q [B,H,d], k, v [B,Hk,d]: the new
@@ -217,50 +255,53 @@ def swa_decode(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, o
     sinks + (p - sinks) % window; see swa_fill for the start after a prefill.
     Returns out [B,H,d]."""
     import torch
-    B, H, d = _dims(q, "q", 3)
+    shape = _dims(q, "q", 3)
+    B, H, d = shape
     Hk = _dims(k, "k", 3)[1]
-    _need(q, "q"); _need(k, "k", q.dtype, (B, Hk, d)); _need(v, "v", q.dtype, (B, Hk, d))
-    _swa_cache(k_cache, "k_cache", B, sinks + window, Hk, d, q.dtype)
-    _swa_cache(v_cache, "v_cache", B, sinks + window, Hk, d, q.dtype)
-    _need(pos, "pos", torch.int64, (B,))
-    dt = _dtype_code(q)
+    dev, dtype, dt = _device(q, "q"), q.dtype, _dtype_code(q)
+    kv, cache = (B, Hk, d), (B, sinks + window, Hk, d)
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", q.dtype, (B, H, d))
     if workspace is None:
         n = swa_workspace_size(KD_SWA_WS_DECODE, B, 1, H, Hk, d, window, sinks, dt)
         workspace = _alloc_ws(n, q.device) if n else None
-    _call(lib().kron_delta_swa_decode, (q, k, v, k_cache, v_cache, pos, out, workspace), stream, _ptr(q), _ptr(k),
-          _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(out), B, H, Hk, d, window, sinks,
-          _scale(scale, d), dt, _ptr(workspace), _nbytes(workspace))
+    _call(lib().kron_delta_swa_decode, dev, _arg(q, "q", dev, dtype, shape), _arg(k, "k", dev, dtype, kv),
+          _arg(v, "v", dev, dtype, kv), _arg(k_cache, "k_cache", dev, dtype, cache),
+          _arg(v_cache, "v_cache", dev, dtype, cache), _arg(pos, "pos", dev, torch.int64, (B,)),
+          _arg(out, "out", dev, dtype, shape), B, H, Hk, d, window, sinks, _scale(scale, d), dt,
+          *_bytes_arg(workspace, "workspace", dev))
     return out
 
 
+@_streamed
 def swa_fill(k, v, lens, k_cache, v_cache, window, sinks=0, *, stream=None):
     """Fills swa_decode's caches from a prefill's k, v [B,T,Hk,d]: of sequence
     b's first lens[b] tokens (int64), the first `sinks` and the last `window` go
     to their slots; the other slots stay as they were."""
     import torch
-    B, T, Hk, d = _dims(k, "k", 4)
-    _need(k, "k"); _need(v, "v", k.dtype, k.shape); _need(lens, "lens", torch.int64, (B,))
-    _swa_cache(k_cache, "k_cache", B, sinks + window, Hk, d, k.dtype)
-    _swa_cache(v_cache, "v_cache", B, sinks + window, Hk, d, k.dtype)
-    _call(lib().kron_delta_swa_fill, (k, v, lens, k_cache, v_cache), stream, _ptr(k), _ptr(v), _ptr(lens),
-          _ptr(k_cache), _ptr(v_cache), B, T, Hk, d, window, sinks, _dtype_code(k))
+    shape = _dims(k, "k", 4)
+    B, T, Hk, d = shape
+    dev, dtype, cache = _device(k, "k"), k.dtype, (B, sinks + window, Hk, d)
+    dt = _dtype_code(k)
+    _call(lib().kron_delta_swa_fill, dev, _arg(k, "k", dev, dtype, shape), _arg(v, "v", dev, dtype, shape),
+          _arg(lens, "lens", dev, torch.int64, (B,)), _arg(k_cache, "k_cache", dev, dtype, cache),
+          _arg(v_cache, "v_cache", dev, dtype, cache), B, T, Hk, d, window, sinks, dt)
 
 
 # ---- gated linear recurrence --------------------------------------------------
 
 
-def _glr_inputs(x, i_pre, f_pre, a_log, h0, n):
+def _glr_inputs(x, i_pre, f_pre, a_log, n):
+    """Shape, dtype code, device and the four addresses."""
     import torch
     shape = _dims(x, "x", n)
-    B, D = shape[0], shape[-1]
-    _need(x, "x"); _need(i_pre, "i_pre", x.dtype, shape); _need(f_pre, "f_pre", x.dtype, shape)
-    _need(a_log, "a_log", torch.float32, (D,)); _need(h0, "h0", torch.float32, (B, D))
-    return B, D, _dtype_code(x)
+    dev, dtype = _device(x, "x"), x.dtype
+    return shape, _dtype_code(x), dev, (_arg(x, "x", dev, dtype, shape), _arg(i_pre, "i_pre", dev, dtype, shape),
+                                        _arg(f_pre, "f_pre", dev, dtype, shape),
+                                        _arg(a_log, "a_log", dev, torch.float32, shape[-1:]))
 
 
+@_streamed
 def glr_fwd(x, i_pre, f_pre, a_log, h0=None, *, out=None, want_state=True, save=False, workspace=None, stream=None):
     """Gated linear recurrence per channel: f = sigmoid(f_pre)^exp(a_log),
     h_t = f h_{t-1} + sqrt(1 - f^2) sigmoid(i_pre) x.  x, i_pre, f_pre [B,T,D]
@@ -269,52 +310,51 @@ def glr_fwd(x, i_pre, f_pre, a_log, h0=None, *, out=None, want_state=True, save=
     hT [B,D] fp32 or None, workspace or None); pass the workspace (save=True) to
     glr_bwd."""
     import torch
-    B, D, dt = _glr_inputs(x, i_pre, f_pre, a_log, h0, 3)
-    T = x.shape[1]
+    shape, dt, dev, ptrs = _glr_inputs(x, i_pre, f_pre, a_log, 3)
+    B, T, D = shape
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", x.dtype, x.shape)
     hT = torch.empty((B, D), dtype=torch.float32, device=x.device) if want_state else None
     if save and workspace is None:
         workspace = _alloc_ws(glr_workspace_size(KD_GLR_WS_SAVE, B, T, D, dt), x.device)
-    _call(lib().kron_delta_glr_fwd, (x, i_pre, f_pre, a_log, h0, out, workspace), stream, _ptr(x), _ptr(i_pre),
-          _ptr(f_pre), _ptr(a_log), _ptr(h0), _ptr(out), _ptr(hT), B, T, D, dt, _ptr(workspace), _nbytes(workspace),
-          int(bool(save)))
+    _call(lib().kron_delta_glr_fwd, dev, *ptrs, _arg(h0, "h0", dev, torch.float32, (B, D)),
+          _arg(out, "out", dev, x.dtype, shape), hT.data_ptr() if want_state else None, B, T, D, dt,
+          *_bytes_arg(workspace, "workspace", dev), 1 if save else 0)
     return out, hT, workspace
 
 
+@_streamed
 def glr_bwd(x, i_pre, f_pre, a_log, h0, dh, dhT=None, *, fwd_workspace, workspace=None, want_dh0=True, stream=None):
     """Backward of glr_fwd for the loss <dh, out> + <dhT, hT>, reading what
-    glr_fwd(save=True) left in fwd_workspace.  Returns dict dx, di_pre, df_pre
-    (x's dtype), da_log [D] fp32 (fixed-order sum), dh0."""
+    glr_fwd(save=True) left in fwd_workspace (h0 included).  Returns dict dx,
+    di_pre, df_pre (x's dtype), da_log [D] fp32 (fixed-order sum), dh0."""
     import torch
-    B, D, dt = _glr_inputs(x, i_pre, f_pre, a_log, h0, 3)
-    T = x.shape[1]
-    _need(dh, "dh", x.dtype, x.shape); _need(dhT, "dhT", torch.float32, (B, D))
+    shape, dt, dev, ptrs = _glr_inputs(x, i_pre, f_pre, a_log, 3)
+    B, T, D = shape
+    _arg(h0, "h0", dev, torch.float32, (B, D))
     g = dict(dx=torch.empty_like(x), di_pre=torch.empty_like(x), df_pre=torch.empty_like(x),
              da_log=torch.empty_like(a_log),
              dh0=torch.empty((B, D), dtype=torch.float32, device=x.device) if want_dh0 else None)
     if workspace is None:
         workspace = _alloc_ws(glr_workspace_size(KD_GLR_WS_BWD, B, T, D, dt), x.device)
-    _call(lib().kron_delta_glr_bwd, (x, i_pre, f_pre, a_log, dh, dhT, fwd_workspace, workspace), stream, _ptr(x),
-          _ptr(i_pre), _ptr(f_pre), _ptr(a_log), _ptr(dh), _ptr(dhT), _ptr(g["dx"]), _ptr(g["di_pre"]),
-          _ptr(g["df_pre"]), _ptr(g["da_log"]), _ptr(g["dh0"]), B, T, D, dt, _ptr(fwd_workspace),
-          _nbytes(fwd_workspace), _ptr(workspace), _nbytes(workspace))
+    _call(lib().kron_delta_glr_bwd, dev, *ptrs, _arg(dh, "dh", dev, x.dtype, shape),
+          _arg(dhT, "dhT", dev, torch.float32, (B, D)), g["dx"].data_ptr(), g["di_pre"].data_ptr(),
+          g["df_pre"].data_ptr(), g["da_log"].data_ptr(), g["dh0"].data_ptr() if want_dh0 else None, B, T, D, dt,
+          *_bytes_arg(fwd_workspace, "fwd_workspace", dev), *_bytes_arg(workspace, "workspace", dev))
     return g
 
 
+@_streamed
 def glr_decode(x, i_pre, f_pre, a_log, h, *, out=None, stream=None):
     """One decode step of the gated linear recurrence.  x, i_pre, f_pre [B,D];
     a_log [D] fp32; h [B,D] fp32 (updated in place).  Returns out [B,D]."""
     import torch
-    B, D, dt = _glr_inputs(x, i_pre, f_pre, a_log, h, 2)
-    if h is None:
-        raise _invalid("h must be given")
+    shape, dt, dev, ptrs = _glr_inputs(x, i_pre, f_pre, a_log, 2)
+    B, D = shape
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", x.dtype, x.shape)
-    _call(lib().kron_delta_glr_decode, (x, i_pre, f_pre, a_log, h, out), stream, _ptr(x), _ptr(i_pre), _ptr(f_pre),
-          _ptr(a_log), _ptr(h), _ptr(out), B, D, dt)
+    _call(lib().kron_delta_glr_decode, dev, *ptrs, _arg(h, "h", dev, torch.float32, shape),
+          _arg(out, "out", dev, x.dtype, shape), B, D, dt)
     return out
 
 
