@@ -123,14 +123,12 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   }
   const float2 gi = un(g.i);
   g.i = pk(kx > 60.f ? 0.f : gi.x, ky > 60.f ? 0.f : gi.y);
-  // log(1 + e) = 2 artanh(u), u = e / (2 + e) <= 1/3: seven terms of its
-  // series (the eighth is below 2e-8 of the sum)
+  // log(1 + e) = 2 artanh(u), u = e / (2 + e) <= 1/3: artanh(u) = u + u z p(z),
+  // z = u^2, p of least error on [0, 1/9] (1.6e-8 of the sum)
   const F2 u = mul2(e, rd), z = mul2(u, u);
-  F2 p = fma2(z, pk(1.f / 13), pk(1.f / 11));
-  p = fma2(z, p, pk(1.f / 9));
-  p = fma2(z, p, pk(1.f / 7));
-  p = fma2(z, p, pk(1.f / 5));
-  p = fma2(z, p, pk(1.f / 3));
+  F2 p = fma2(z, pk(1.34418249e-1f), pk(1.41156361e-1f));
+  p = fma2(z, p, pk(2.00038910e-1f));
+  p = fma2(z, p, pk(3.33333194e-1f));
   p = fma2(mul2(u, z), p, u);
   const F2 soft = fma2(p, pk(2.f), pk(fmaxf(-zf.x, 0.f), fmaxf(-zf.y, 0.f)));
   // f~ at the type's lowest value starts a new sequence: L stays finite so
@@ -142,13 +140,12 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   const float kMagic = 12582912.f;  // 1.5 2^23: rounds to an integer, kept in the low bits
   const F2 t = add2(Lc, pk(kMagic));
   const F2 n = add2(t, pk(-kMagic)), x = fma2(n, pk(-1.f), Lc);
-  // 2^x - 1 = sum (x ln 2)^k / k! up to k = 7 (the next term is below 2e-8 of it)
-  F2 q = fma2(x, pk(1.52527338e-5f), pk(1.54035304e-4f));
-  q = fma2(x, q, pk(1.33335581e-3f));
-  q = fma2(x, q, pk(9.61812911e-3f));
-  q = fma2(x, q, pk(5.55041087e-2f));
+  // (2^x - 1) / x of least error on [-1/2, 1/2] (1.3e-8 of it)
+  F2 q = fma2(x, pk(1.54697351e-4f), pk(1.33908668e-3f));
+  q = fma2(x, q, pk(9.61803086e-3f));
+  q = fma2(x, q, pk(5.55035695e-2f));
   q = fma2(x, q, pk(2.40226507e-1f));
-  q = fma2(x, q, pk(6.93147181e-1f));
+  q = fma2(x, q, pk(6.93147182e-1f));
   q = mul2(q, x);
   const float2 t2 = un(t), m2 = un(add2(q, pk(1.f))), q2 = un(q);
   float fx = __uint_as_float(__float_as_uint(m2.x) + (__float_as_uint(t2.x) << 23));
@@ -190,11 +187,13 @@ struct Run {
 };
 __device__ __forceinline__ Run then(Run a, Run b) { return {mul2(a.f, b.f), fma2(b.f, a.h, b.h)}; }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, Run v) {
-  asm volatile("st.shared::cluster.v2.b64 [%0], {%1,%2};" ::"r"(addr), "l"(v.f.v), "l"(v.h.v) : "memory");
+// This lane's run of CTA `rank` into CTA `to`, whose barrier counts the bytes.
+// (A cluster barrier would do too, but its release waits for the outputs that
+// the CTA has stored to global memory, on every step: 1.6 us of a 5 us step.)
+__device__ __forceinline__ void send(Run* slot, uint64_t* bar, int to, Run v) {
+  const float2 f = un(v.f), h = un(v.h);
+  tc::st_async_v4(tc::mapa(tc::smem_u32(slot), to), make_float4(f.x, f.y, h.x, h.y), tc::mapa(tc::smem_u32(bar), to));
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <typename T, int kArrays>
 struct GlrCfg {
@@ -217,6 +216,20 @@ __device__ __forceinline__ void load_stage(unsigned char* sm, int stage, const C
   for (int i = 0; i < kArrays; ++i) tc::tma_load_4d(sm + stage * Cf::STAGE + i * Cf::TILE, maps[i], c, 0, t0, b, bar);
 }
 
+// Tokens behind the sequence's end and channels behind D: this thread's words
+// of a stage from token k on are set so that the gate keeps everything and
+// writes nothing (f = 1 and m = 0 exactly), and the loops over the tokens need
+// no branch.
+template <typename T, int kArrays>
+__device__ __forceinline__ void neutral_from(int k, unsigned char* st, int at) {
+  using V = typename Pair<T>::type;
+  for (int j = k; j < kTok; ++j)
+#pragma unroll
+    for (int i = 0; i < kArrays; ++i)
+      reinterpret_cast<V*>(st + i * GlrCfg<T, kArrays>::TILE)[at + j * 32] = Pair<T>::of(pk(i == 2 ? 1e4f : 0.f));
+  tc::fence_proxy_async();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
     const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mi,
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
   using Cf = GlrCfg<T, 3>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((128u - (tc::smem_u32(smem_raw) & 127u)) & 127u);
-  __shared__ uint64_t full[2];
+  __shared__ uint64_t full[2], runs_in[2];
   __shared__ int abort_flag;
   Run(*runs)[kWarps][32] = reinterpret_cast<Run(*)[kWarps][32]>(sm + Cf::RUNS);
   Run(*cruns)[kGlrMaxCluster][32] = reinterpret_cast<Run(*)[kGlrMaxCluster][32]>(sm + Cf::CRUNS);
@@ -240,6 +253,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
   if (threadIdx.x == 0) {
     tc::mbar_init(&full[0], 1);
     tc::mbar_init(&full[1], 1);
+    tc::mbar_init(&runs_in[0], 1);
+    tc::mbar_init(&runs_in[1], 1);
     tc::mbar_init_fence();
     abort_flag = 0;
     for (int s = 0; s < 2; ++s)
@@ -257,42 +272,38 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
     const int n = s * C + rank, par = s & 1;
     const long long t0 = (long long)n * kChunk + warp * kTok, left = T_ - t0;
     const int k = !live || left <= 0 ? 0 : left < kTok ? (int)left : kTok;  // tokens of this thread
-    const unsigned char* st = sm + par * Cf::STAGE;
+    unsigned char* st = sm + par * Cf::STAGE;
+    const int own = warp * kTok * 32 + lane;  // this thread's first word of a tile
     if (n < NC) tc::mbar_wait<false>(&full[par], (s >> 1) & 1, err, tc::kErrTimeoutLoad, &abort_flag);
+    if (k < kTok) neutral_from<T, 3>(k, st, own);
+    const V *xs = reinterpret_cast<const V*>(st) + own, *is = reinterpret_cast<const V*>(st + Cf::TILE) + own;
+    const V* fs = reinterpret_cast<const V*>(st + 2 * Cf::TILE) + own;
     Run r[kTok], run = {pk(1.f), pk(0.f)};
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const int at = (warp * kTok + j) * 32 + lane;
-      if (j < k) {
-        const float2 x = P::f(reinterpret_cast<const V*>(st)[at]);
-        const Gates g = gates<false>(P::f(reinterpret_cast<const V*>(st + 2 * Cf::TILE)[at]),
-                                     P::f(reinterpret_cast<const V*>(st + Cf::TILE)[at]), na2);
-        const F2 m = mul2(g.w, inv_m(g.w));
-        run = then(run, {g.f, mul2(mul2(m, g.i), pk(x.x, x.y))});
-      }
+      const float2 x = P::f(xs[j * 32]);
+      const Gates g = gates<false>(P::f(fs[j * 32]), P::f(is[j * 32]), na2);
+      run = then(run, {g.f, mul2(mul2(mul2(g.w, inv_m(g.w)), g.i), pk(x.x, x.y))});
       r[j] = run;
     }
+    if (C > 1 && threadIdx.x == 0) tc::mbar_expect_tx(&runs_in[par], (uint32_t)C * 32 * sizeof(Run));
     runs[par][warp][lane] = run;
     __syncthreads();  // and every thread is through with the stage
     if (threadIdx.x == 0 && n + 2 * C < NC)
       load_stage<T, 3>(sm, par, maps, c0, (n + 2 * C) * kChunk, b, &full[par]);
-    Run pre = {pk(1.f), pk(0.f)}, all = pre;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) pre = all;
-      all = then(all, runs[par][w][lane]);
-    }
+    Run pre = {pk(1.f), pk(0.f)};
+    for (int w = 0; w < warp; ++w) pre = then(pre, runs[par][w][lane]);
+    Run all = pre;
+    for (int w = warp; w < kWarps; ++w) all = then(all, runs[par][w][lane]);
     F2 mine = carry;  // state at the start of this CTA's chunk
     if (C > 1) {
-      // warp w hands the chunk's run to CTA w; the buffer's last readers have
-      // arrived at the barrier of the step before
-      if (warp < C) st_cluster(tc::mapa(tc::smem_u32(&cruns[par][rank][lane]), warp), all);
-      tc::cluster_sync();
-      for (int q = 0; q < C; ++q) {
-        if (q == rank) mine = carry;
-        const Run v = cruns[par][q][lane];
-        carry = fma2(v.f, carry, v.h);
-      }
+      // warp w hands the chunk's run to CTA w; the buffer's readers of two steps
+      // ago are through: their CTA's runs of the step before have arrived here
+      if (warp < C) send(&cruns[par][rank][lane], &runs_in[par], warp, all);
+      tc::mbar_wait<true>(&runs_in[par], (s >> 1) & 1, err, tc::kErrTimeoutCluster, &abort_flag);
+      for (int q = 0; q < rank; ++q) mine = fma2(cruns[par][q][lane].f, mine, cruns[par][q][lane].h);
+      carry = mine;
+      for (int q = rank; q < C; ++q) carry = fma2(cruns[par][q][lane].f, carry, cruns[par][q][lane].h);
     } else {
       carry = fma2(all.f, carry, all.h);
     }
@@ -303,6 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
     for (int j = 0; j < kTok; ++j)
       if (j < k) __stcs(reinterpret_cast<V*>(o + (size_t)j * D), P::of(fma2(r[j].f, h, r[j].h)));
   }
+  if (C > 1) tc::cluster_sync();  // no CTA leaves while another may still write to it
   if (hT && rank == 0 && warp == 0 && live) *reinterpret_cast<F2*>(hT + (size_t)b * D + c) = carry;
 }
 
@@ -323,7 +335,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
   using Cf = GlrCfg<T, 4>;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((128u - (tc::smem_u32(smem_raw) & 127u)) & 127u);
-  __shared__ uint64_t full[2];
+  __shared__ uint64_t full[2], runs_in[2];
   __shared__ int abort_flag;
   Run(*runs)[kWarps][32] = reinterpret_cast<Run(*)[kWarps][32]>(sm + Cf::RUNS);
   Run(*cruns)[kGlrMaxCluster][32] = reinterpret_cast<Run(*)[kGlrMaxCluster][32]>(sm + Cf::CRUNS);
@@ -341,6 +353,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
   if (threadIdx.x == 0) {
     tc::mbar_init(&full[0], 1);
     tc::mbar_init(&full[1], 1);
+    tc::mbar_init(&runs_in[0], 1);
+    tc::mbar_init(&runs_in[1], 1);
     tc::mbar_init_fence();
     abort_flag = 0;
     for (int s = 0; s < 2 && s < steps; ++s)
@@ -360,45 +374,40 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
     const long long t0 = (long long)n * kChunk + warp * kTok, left = T_ - t0;
     const int k = !live || left <= 0 ? 0 : left < kTok ? (int)left : kTok;
     unsigned char* st = sm + par * Cf::STAGE;
-    const V* xs = reinterpret_cast<const V*>(st) + warp * kTok * 32 + lane;
-    const V* gs = reinterpret_cast<const V*>(st + 3 * Cf::TILE) + warp * kTok * 32 + lane;
+    const int own = warp * kTok * 32 + lane;  // this thread's first word of a tile
+    const V *xs = reinterpret_cast<const V*>(st) + own, *gs = reinterpret_cast<const V*>(st + 3 * Cf::TILE) + own;
+    V *is = reinterpret_cast<V*>(st + Cf::TILE) + own, *fs = reinterpret_cast<V*>(st + 2 * Cf::TILE) + own;
     F2 start = pk(0.f);
     if (live && n < NC) start = *reinterpret_cast<const F2*>(states + ((size_t)b * NC + n) * D + c);
     if (n < NC) {
       tc::mbar_wait<false>(&full[par], uses[par] & 1, err, tc::kErrTimeoutLoad, &abort_flag);
       ++uses[par];
     }
+    if (k < kTok) neutral_from<T, 4>(k, st, own);
     F2 F[kTok], M[kTok], Q[kTok], J[kTok];  // f, m i, f i x / m, sigma(-i~)
     Run run = {pk(1.f), pk(0.f)};
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      F[j] = pk(1.f);
-      M[j] = Q[j] = J[j] = pk(0.f);
-      if (j < k) {
-        const int at = (warp * kTok + j) * 32 + lane;
-        const float2 x = P::f(xs[j * 32]);
-        const Gates g = gates<true>(P::f(reinterpret_cast<const V*>(st + 2 * Cf::TILE)[at]),
-                                    P::f(reinterpret_cast<const V*>(st + Cf::TILE)[at]), na2);
-        const float2 L = un(g.L);
-        // the same thread's own two words: 4 bytes of the i~ tile and of the f~ tile
-        *reinterpret_cast<float*>(st + Cf::TILE + at * sizeof(V)) = L.x;
-        *reinterpret_cast<float*>(st + 2 * Cf::TILE + at * sizeof(V)) = L.y;
-        keep[j * kWarps * 32] = mul2(a, g.s);
-        const F2 r = inv_m(g.w), x2 = pk(x.x, x.y);
-        F[j] = g.f;
-        J[j] = g.j;
-        M[j] = mul2(mul2(g.w, r), g.i);
-        Q[j] = mul2(mul2(g.f, x2), mul2(g.i, r));
-        run = then(run, {g.f, mul2(M[j], x2)});
-      }
+      const float2 x = P::f(xs[j * 32]);
+      const Gates g = gates<true>(P::f(fs[j * 32]), P::f(is[j * 32]), na2);
+      const float2 L = un(g.L);
+      *reinterpret_cast<float*>(&is[j * 32]) = L.x;
+      *reinterpret_cast<float*>(&fs[j * 32]) = L.y;
+      keep[j * kWarps * 32] = mul2(a, g.s);
+      const F2 r = inv_m(g.w), x2 = pk(x.x, x.y);
+      F[j] = g.f;
+      J[j] = g.j;
+      M[j] = mul2(mul2(g.w, r), g.i);
+      Q[j] = mul2(mul2(g.f, x2), mul2(g.i, r));
+      run = then(run, {g.f, mul2(M[j], x2)});
     }
     F2 u = pk(0.f);
 #pragma unroll
-    for (int j = kTok - 1; j >= 0; --j)
-      if (j < k) {
-        const float2 g = P::f(gs[j * 32]);
-        u = mul2(F[j], add2(pk(g.x, g.y), u));
-      }
+    for (int j = kTok - 1; j >= 0; --j) {
+      const float2 g = P::f(gs[j * 32]);
+      u = mul2(F[j], add2(pk(g.x, g.y), u));
+    }
+    if (C > 1 && threadIdx.x == 0) tc::mbar_expect_tx(&runs_in[par], (uint32_t)C * 32 * sizeof(Run));
     runs[par][warp][lane] = run;
     us[par][warp][lane] = u;
     __syncthreads();
@@ -406,64 +415,50 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
     if (threadIdx.x == 0 && s > 0 && s + 1 < steps && chunk(s + 1) < NC)
       load_stage<T, 4>(sm, par ^ 1, maps, c0, chunk(s + 1) * kChunk, b, &full[par ^ 1]);
     // what this warp's last token gets from the later ones: runs of (f products, u)
-    Run post = {pk(1.f), pk(0.f)}, all = post;
-#pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w) {
-      if (w == warp) post = all;
-      const F2 f = runs[par][w][lane].f;
-      all = {mul2(all.f, f), fma2(f, all.h, us[par][w][lane])};
-    }
+    Run post = {pk(1.f), pk(0.f)};
+    for (int w = kWarps - 1; w > warp; --w) post = then(post, {runs[par][w][lane].f, us[par][w][lane]});
+    Run all = post;
+    for (int w = warp; w >= 0; --w) all = then(all, {runs[par][w][lane].f, us[par][w][lane]});
     if (C > 1) {
-      if (warp < C) st_cluster(tc::mapa(tc::smem_u32(&cruns[par][rank][lane]), warp), all);
-      cluster_arrive();
+      if (warp < C) send(&cruns[par][rank][lane], &runs_in[par], warp, all);
     }
     // state before this warp's first token, then before each of its tokens
     F2 h = start;
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < warp) {
-        const Run v = runs[par][w][lane];
-        h = fma2(v.f, h, v.h);
-      }
+    for (int w = 0; w < warp; ++w) h = fma2(runs[par][w][lane].f, h, runs[par][w][lane].h);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
+      const float2 x = P::f(xs[j * 32]);
       Q[j] = fma2(Q[j], pk(-1.f), h);  // h_{t-1} - f i x / m, whose product with u_t is dl
-      if (j < k) {
-        const float2 x = P::f(xs[j * 32]);
-        h = fma2(F[j], h, mul2(M[j], pk(x.x, x.y)));
-      }
+      h = fma2(F[j], h, mul2(M[j], pk(x.x, x.y)));
     }
     F2 mine = carry;
     if (C > 1) {
-      cluster_wait();
-      for (int q = C - 1; q >= 0; --q) {
-        if (q == rank) mine = carry;
-        const Run v = cruns[par][q][lane];
-        carry = fma2(v.f, carry, v.h);
-      }
+      tc::mbar_wait<true>(&runs_in[par], (s >> 1) & 1, err, tc::kErrTimeoutCluster, &abort_flag);
+      for (int q = C - 1; q > rank; --q) mine = fma2(cruns[par][q][lane].f, mine, cruns[par][q][lane].h);
+      carry = mine;
+      for (int q = rank; q >= 0; --q) carry = fma2(cruns[par][q][lane].f, carry, cruns[par][q][lane].h);
     } else {
       carry = fma2(all.f, carry, all.h);
     }
     F2 v = fma2(post.f, mine, post.h);
     const size_t off = ((size_t)b * T_ + t0) * D + c;
 #pragma unroll
-    for (int j = kTok - 1; j >= 0; --j)
+    for (int j = kTok - 1; j >= 0; --j) {
+      const float2 vg = P::f(gs[j * 32]), x = P::f(xs[j * 32]);
+      const F2 g = add2(pk(vg.x, vg.y), v), gm = mul2(g, M[j]);
+      v = mul2(F[j], g);
+      const F2 dl = mul2(v, Q[j]);
+      da = fma2(dl, pk(*reinterpret_cast<const float*>(&is[j * 32]), *reinterpret_cast<const float*>(&fs[j * 32])), da);
       if (j < k) {
-        const int at = (warp * kTok + j) * 32 + lane;
-        const float2 vg = P::f(gs[j * 32]), x = P::f(xs[j * 32]);
-        const F2 g = add2(pk(vg.x, vg.y), v), gm = mul2(g, M[j]);
-        v = mul2(F[j], g);
-        const F2 dl = mul2(v, Q[j]);
-        const float Lx = *reinterpret_cast<const float*>(st + Cf::TILE + at * sizeof(V));
-        const float Ly = *reinterpret_cast<const float*>(st + 2 * Cf::TILE + at * sizeof(V));
-        da = fma2(dl, pk(Lx, Ly), da);
         const size_t to = off + (size_t)j * D;
         __stcs(reinterpret_cast<V*>(dx + to), P::of(gm));
         __stcs(reinterpret_cast<V*>(di + to), P::of(mul2(mul2(gm, pk(x.x, x.y)), J[j])));
         __stcs(reinterpret_cast<V*>(df + to), P::of(mul2(dl, keep[j * kWarps * 32])));
       }
+    }
     tc::fence_proxy_async();  // the words written over f~ and i~, before the stage is loaded again
   }
+  if (C > 1) tc::cluster_sync();  // no CTA leaves while another may still write to it
   if (dh0 && rank == 0 && warp == 0 && live) *reinterpret_cast<F2*>(dh0 + (size_t)b * D + c) = carry;
   // da_log: the warps' sums in a fixed order, one row per CTA of the cluster
   __syncthreads();

@@ -527,3 +527,31 @@ def test_training_step_through_the_layer_by_differences():
         want, got = float((up - down) / (2 * step)), float((g.double() * u.double()).sum())
         # fp32 noise of the two losses over the step; the third-order term of a 1e-2 step is below 1e-3
         assert abs(want - got) <= 1e-3 * float((g.double() ** 2).sum() ** 0.5 * u.norm()) + 64 * 2 ** -24 * size / step
+
+
+def test_a_thread_without_a_context_can_call():
+    """The first CUDA work of a fresh thread is one of these calls."""
+    import threading
+    t, _ = glr_inputs(1, 70, 64, "bf16", 1)
+    a = (t["x"], t["i_pre"], t["f_pre"], t["a_log"], t["h0"])
+    q = torch.randn(1, 70, 2, 64, device="cuda").bfloat16()
+    want = kd.glr_fwd(*a)[0], kd.swa_fwd(q, q, q, 9)[0]
+    torch.cuda.synchronize()
+    outs = torch.empty_like(a[0]), torch.empty_like(q)
+    lib, stream, p = kd.lib(), torch.cuda.current_stream().cuda_stream, lambda x: x.data_ptr()  # noqa: E731
+    lse = torch.empty(1, 70, 2, device="cuda")
+    rc = []
+
+    def work():
+        rc.append(lib.kron_delta_glr_fwd(*(p(x) for x in a), p(outs[0]), None, 1, 70, 64, 1, None, 0, 0, stream))
+
+    def more():
+        rc.append(lib.kron_delta_swa_fwd(p(q), p(q), p(q), p(outs[1]), p(lse), 1, 70, 2, 2, 64, 9, 0, 0.125, 1, None, 0,
+                                         0, stream))
+    for f in (work, more):
+        th = threading.Thread(target=f)
+        th.start()
+        th.join()
+    torch.cuda.synchronize()
+    assert rc == [kd.KD_OK, kd.KD_OK]
+    assert all(torch.equal(x, y) for x, y in zip(outs, want))
