@@ -1,30 +1,36 @@
 // kd_swa_tc.cu -- sliding-window attention with first tokens kept, on tcgen05
 // (bf16, d = 64 and 128).  The formulas are in kd_swa.cu.
 //
-// Every kernel has ten warps: two groups of four (thread = TMEM lane = tile
+// Every kernel has eleven warps: two groups of four (thread = TMEM lane = tile
 // row) for the elementwise work, one thread that loads tiles by TMA into a
-// ring, one that issues the MMAs.  The groups work on separate tiles, so that
-// the tensor core multiplies one group's operands while the other group turns
-// its scores into weights.  The weights (p, dS) are rounded to bf16 and go
-// back to TMEM over the scores they came from, as the next product's A
-// operand; the B operand of those products (v, k, dO, q) is read MN-major from
-// the same shared-memory tile that the score product reads K-major, so no tile
-// is stored twice or transposed.
+// ring, and two that issue MMAs, each the products of one chain (scores, then
+// what is made of them), so that one chain's waits (250 cycles each, even for
+// a phase that is complete) lie beside the other's products.  Tiles are 128 x
+// 128: an MMA of 128 x 64 x 16 takes 50 cycles where one of 128 x 128 x 16
+// takes 68.  B operands of the second products (v, k, dO, q) are read MN-major
+// from the same shared-memory tile that the score product reads K-major, so no
+// tile is stored twice or transposed.
 //
-// Forward: 256 queries of one head per CTA, a group to each 128; keys in tiles
-// of 128.  Bound by the hardware exponential as much as by the MMAs (128 x 128
-// exponentials take as long as the two products of that tile at d = 128).  The
-// output stays in TMEM; it is rescaled only when a row's maximum has grown by
-// more than 2^8 over the one its sums refer to (then p <= 2^8, still exact
-// enough in bf16, whose precision does not depend on the size).  Short rows
-// (kFine) take the weights as bf16 high and low parts: over a few keys the
-// roundings of p do not average out, and the backward's delta = dO.o would
-// pass them on to every gradient.
+// Forward: 256 queries of one head per CTA, a group to each 128.  Scores are
+// read into registers at once and their TMEM columns given back for the next
+// tile's, p goes to shared memory as the next product's A operand; per tile
+// pair 32 MMAs (2,200 cycles) stand against 2,050 cycles of the hardware
+// exponential.  With p over the scores in TMEM, where a group waits for both
+// products between two tiles, the forward took 0.41 ms in place of FWD_MS (H16
+// Hk4 T16384 d128 window 2048).  The output stays in TMEM and is rescaled only
+// when a row's maximum has grown by more than 2^8 over the one its sums refer
+// to (then p <= 2^8, still exact enough in bf16, whose precision does not
+// depend on the size).  Short rows (kFine) take the weights as bf16 high and
+// low parts: over a few keys the roundings of p do not average out, and the
+// backward's delta = dO.o would pass them on to every gradient.
 //
 // Backward: p is recomputed from the saved lse.  dk, dv: 128 keys per CTA
-// (rows are keys: S^T = k q^T, dP^T = v dO^T), 64 queries at a time, the two
-// groups alternating; dv += P^T dO, dk += dS^T q.  dq: 128 queries per CTA, 64
-// keys at a time; dq += dS k.  Seven products in place of the five of one
+// (rows are keys: S^T = k q^T, dP^T = v dO^T), 128 queries at a time; dv +=
+// P^T dO, dk += dS^T q.  dq: 128 queries per CTA; dq += dS k.  The weights go
+// over the scores in TMEM, and the two groups take half of the columns of each
+// tile; p is formed while dP is still being multiplied.  (64-column tiles, two
+// at a time, a group to each: 0.88 and 0.75 ms in place of DKV_MS and DQ_MS at
+// H16 T16384 d128 window 2048.)  Seven products in place of the five of one
 // joint pass, but no atomics and no fp32 copy of dq: every sum has one order.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
@@ -35,8 +41,8 @@ namespace kd {
 
 namespace {
 
-constexpr int kTcThreads = 320;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kTcThreads = 352;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;  // and 10
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -104,16 +110,50 @@ __device__ __forceinline__ void store_lane(uint32_t lanes, float scale, __nv_bfl
   }
 }
 
+// Tile of rows x 64-channel blocks by TMA (D / 64 boxes).
+template <int D>
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* m, int h, int t0, int b, uint64_t* bar) {
+#pragma unroll
+  for (int c = 0; c < D; c += 64) tc::tma_load_4d(dst + c * 256, m, c, h, t0, b, bar);
+}
+
+// D = A B^T of 128 x 128, K = d: both tiles of 128 rows, K-major.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = tc::idesc(128, 128, 1);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    const uint32_t o = s / 4 * 16384 + s % 4 * 32;
+    tc::mma_bf16_ss(d, tc::desc_sw128(a + o), tc::desc_sw128(b + o), id, s > 0);
+  }
+}
+
+// D (+)= W X of 128 x d, K = 128: W in TMEM, the columns of group 0's half at
+// `w` and of group 1's at w + 64 (32 columns each), X a tile of 128 rows read
+// MN-major.
+template <int D>
+__device__ __forceinline__ void mma_mix(uint32_t d, uint32_t w, uint32_t x, bool acc) {
+  constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    tc::mma_bf16_ts(d, w + s / 4 * 64 + s % 4 * 8, tc::desc_sw128_mn(x + s * 2048, 16384u), id, acc || s > 0);
+}
+
 // ---- forward -----------------------------------------------------------------
 
 template <int D>
 struct FwdCfg {
   static constexpr uint32_t TILE = 128 * D * 2;
-  static constexpr int SLOTS = D == 128 ? 5 : 8;  // ring of key and value tiles
-  static constexpr uint32_t RING = 2 * TILE;      // behind the two query tiles
-  static constexpr uint32_t BYTES = (2 + SLOTS) * TILE + 1024;
-  static constexpr int S_COL = 0, O_COL = 256;    // 128 columns per group each
+  static constexpr int SLOTS = D == 128 ? 3 : 6;  // ring of key and value tiles
+  static constexpr uint32_t P = 2 * TILE;         // behind the two query tiles: weights, 32 KB per group
+  static constexpr uint32_t RING = P + 65536;
+  static constexpr uint32_t BYTES = RING + SLOTS * TILE + 1024;
+  static constexpr int S_COL = 0, O_COL = 256;    // 128 columns per group: scores; the output
 };
+
+// Order of the ring's loads: k0 k1 v0 k2 v1 k3 .. (count tiles of each).
+__device__ __forceinline__ int load_of_k(int n) { return n < 2 ? n : 2 * n - 1; }
+__device__ __forceinline__ int load_of_v(int n, int count) { return (n + 2 < count ? n + 2 : count) + n; }
 
 template <int D, bool kFine>
 __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
@@ -122,7 +162,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
   using Cf = FwdCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t q_full, full[Cf::SLOTS], empty[Cf::SLOTS], s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t q_full, full[Cf::SLOTS], empty[Cf::SLOTS], s_full[2], s_free[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -136,10 +176,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     tc::mbar_init(&q_full, 1);
     for (int i = 0; i < Cf::SLOTS; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&s_free[i], 128);
       tc::mbar_init(&p_full[i], 128);
       tc::mbar_init(&o_full[i], 1);
     }
@@ -152,80 +193,95 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
   tc::tc_after_sync();
   const uint32_t tmem = tmem_slot;
   volatile int* ab = &abort_flag;
+  const int loads = 2 * all.count;
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
       const bool two = q0 + 128 < a.T;
       tc::mbar_expect_tx(&q_full, (two ? 2 : 1) * Cf::TILE);
-      for (int i = 0; i < (two ? 2 : 1); ++i)
-        for (int c = 0; c < D; c += 64) tc::tma_load_4d(sm + i * Cf::TILE + c * 256, &tq, c, h, q0 + 128 * i, b, &q_full);
-      for (int n = 0; n < 2 * all.count; ++n) {  // keys, values of one tile after the other
-        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS;
+      for (int i = 0; i < (two ? 2 : 1); ++i) load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &q_full);
+      int kn = 0, vn = 0;
+      for (int n = 0; n < loads; ++n) {
+        const bool is_k = kn < all.count && load_of_k(kn) == n;
+        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS, tile = is_k ? kn++ : vn++;
         if (use && !tc::mbar_wait<false>(&empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
         tc::mbar_expect_tx(&full[slot], Cf::TILE);
-        for (int c = 0; c < D; c += 64)
-          tc::tma_load_4d(sm + Cf::RING + slot * Cf::TILE + c * 256, n & 1 ? &tv : &tk, c, hk, all.tile(n / 2) * 128, b,
-                          &full[slot]);
+        load_tile<D>(sm + Cf::RING + slot * Cf::TILE, is_k ? &tk : &tv, hk, all.tile(tile) * 128, b, &full[slot]);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     if (lane == 0) {
-      const uint32_t ID_S = tc::idesc(128, 128, 1), ID_O = tc::idesc(128, D, 1) | tc::kMajorB;
-      const KeyRange mine[2] = {KeyRange(q0, upto(q0 + 128), W, S, 128),
-                                KeyRange(upto(q0 + 128), upto(q0 + 256), W, S, 128)};
+      const int i = warp - kMmaWarp;
+      const KeyRange mine(upto(q0 + 128 * i), upto(q0 + 128 * i + 128), W, S, 128);
       const uint32_t base = tc::smem_u32(sm);
-      bool started[2] = {false, false};
-      int p_use[2] = {0, 0};
-      const auto landed = [&](int n) {
-        return tc::mbar_wait<false>(&full[n % Cf::SLOTS], (n / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab);
+      const uint32_t q = base + i * Cf::TILE, p = base + Cf::P + i * 32768;
+      const uint32_t sc = tmem + Cf::S_COL + i * 128, o = tmem + Cf::O_COL + i * 128;
+      int s_done = 0, p_done = 0;  // tiles whose scores, whose products are issued
+      const auto landed = [&](int load) {
+        tc::mbar_wait<false>(&full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab);
+        return base + Cf::RING + load % Cf::SLOTS * Cf::TILE;
       };
-      const auto scores = [&](int i, int n) {  // S_i = q_i k_n^T
-        const uint32_t k = base + Cf::RING + (2 * n) % Cf::SLOTS * Cf::TILE, q = base + i * Cf::TILE;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = s / 4 * 16384 + s % 4 * 32;
-          tc::mma_bf16_ss(tmem + Cf::S_COL + i * 128, tc::desc_sw128(q + o), tc::desc_sw128(k + o), ID_S, s > 0);
+      const auto release = [&](int load, bool used) {  // only where the slot is loaded again: every commit is waited for
+        if (load + Cf::SLOTS >= loads) return;
+        if (used)
+          tc::mma_commit(&empty[load % Cf::SLOTS]);
+        else
+          tc::mbar_arrive(&empty[load % Cf::SLOTS]);
+      };
+      // S = q k^T of tile n, when the group has read the scores before
+      const auto scores = [&](int n) {
+        const bool has = mine.has(all.tile(n));
+        // a tile that this group skips is waited for as well, so that its slot's
+        // barrier counts one arrival of each chain per load
+        const uint32_t k = landed(load_of_k(n));
+        if (has) {
+          const int m = s_done++;
+          if (m > 0) tc::mbar_wait<false>(&s_free[i], (m - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
+          tc::tc_after_sync();
+          mma_scores<D>(sc, q, k);
+          tc::mma_commit(&s_full[i]);
         }
-        tc::mma_commit(&s_full[i]);
+        release(load_of_k(n), has);
       };
-      const auto release = [&](int n) {  // only where the slot is loaded again: every commit is waited for
-        if (n + Cf::SLOTS < 2 * all.count) tc::mma_commit(&empty[n % Cf::SLOTS]);
-      };
-      tc::mbar_wait<false>(&q_full, 0, a.err, tc::kErrTimeoutLoad, ab);
-      landed(0);
-      tc::tc_after_sync();
-      for (int i = 0; i < 2; ++i)
-        if (mine[i].has(all.tile(0))) scores(i, 0);
-      release(0);
-      for (int n = 0; n < all.count && !*ab; ++n) {
-        const int kt = all.tile(n);
-        const bool more = n + 1 < all.count;
-        landed(2 * n + 1);
-        if (more) landed(2 * n + 2);
-        const uint32_t v = base + Cf::RING + (2 * n + 1) % Cf::SLOTS * Cf::TILE;
+      // O += P v of tile n
+      const auto mix = [&](int n) {
+        const bool has = mine.has(all.tile(n));
+        const int load = load_of_v(n, all.count);
+        const uint32_t v = landed(load);
+        if (has) {
+          constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+          const int m = p_done++;
+          tc::mbar_wait<false>(&p_full[i], m & 1, a.err, tc::kErrTimeoutMma, ab);
+          tc::tc_after_sync();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (mine[i].has(kt)) {
-            tc::mbar_wait<false>(&p_full[i], p_use[i]++ & 1, a.err, tc::kErrTimeoutMma, ab);
-            tc::tc_after_sync();
+          for (int s = 0; s < 8; ++s)
+            tc::mma_bf16_ss(o, tc::desc_sw128(p + s / 4 * 16384 + s % 4 * 32), tc::desc_sw128_mn(v + s * 2048, 16384u),
+                            id, m > 0 || s > 0);
+          if (kFine) {  // the low parts, over the scores
 #pragma unroll
-            for (int s = 0; s < (kFine ? 16 : 8); ++s)  // O_i += P_i v
-              tc::mma_bf16_ts(tmem + Cf::O_COL + i * 128, tmem + Cf::S_COL + i * 128 + s * 8,
-                              tc::desc_sw128_mn(v + s % 8 * 2048, 16384u), ID_O, started[i] || s > 0);
-            started[i] = true;
-            if (kt == mine[i].end) tc::mma_commit(&o_full[i]);
+            for (int s = 0; s < 8; ++s)
+              tc::mma_bf16_ts(o, sc + s * 8, tc::desc_sw128_mn(v + s * 2048, 16384u), id, 1);
           }
-          if (more && mine[i].has(all.tile(n + 1))) scores(i, n + 1);
+          tc::mma_commit(&o_full[i]);
         }
-        release(2 * n + 1);
-        if (more) release(2 * n + 2);
+        release(load, has);
+      };
+      if (mine.count) tc::mbar_wait<false>(&q_full, 0, a.err, tc::kErrTimeoutLoad, ab);
+      scores(0);
+      for (int n = 0; n < all.count && !*ab; ++n) {
+        const bool more = n + 1 < all.count;
+        if (more && !kFine) scores(n + 1);
+        mix(n);
+        if (more && kFine) scores(n + 1);
       }
     }
   } else {
-    const int i = warp >> 2, r0 = upto(q0 + 128 * i), t = q0 + tid;
+    const int i = warp >> 2, r0 = upto(q0 + 128 * i), t = q0 + tid, r = tid & 127;
     const KeyRange mine(r0, upto(q0 + 128 * i + 128), W, S, 128);
     const uint32_t s_lane = tc::tmem_lane_addr(tmem, warp, Cf::S_COL + i * 128);
     const uint32_t o_lane = tc::tmem_lane_addr(tmem, warp, Cf::O_COL + i * 128);
+    // this row of the group's weights: 16-byte chunk c of a block at (c ^ (row & 7)) * 16
+    unsigned char* prow = sm + Cf::P + i * 32768 + r * 128;
     const float s2 = a.scale * kLog2e;
     float top = -INFINITY, sum = 0.f;  // sums refer to 2^(s2 top)
     for (int n = 0; n < mine.count; ++n) {
@@ -236,6 +292,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
 #pragma unroll
       for (int c = 0; c < 128; c += 32) tc::tmem_ld32(s_lane + c, x + c);
       tc::tmem_ld_wait();
+      if (!kFine) {
+        tc::tc_before_sync();
+        tc::mbar_arrive(&s_free[i]);
+      }
       if (!(k0 + 127 <= r0 && (r0 + 127 - k0 < W || k0 + 127 < S))) {
         const int hi = t - k0, lo = hi - W, sk = S - k0;
 #pragma unroll
@@ -251,56 +311,66 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       }
       const float m = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
       const bool grow = n == 0 ? m > top : (m - top) * s2 > 8.f;  // false while a row has seen no key
-      if (n > 0 && __any_sync(0xffffffffu, grow)) {
-        // the commit of these scores covered the product before: O is complete
-        const float f = grow ? ex2((top - m) * s2) : 1.f;
-        sum *= f;
+      if (n > 0) {  // the product before has read the weights, and the output is complete
+        warp_wait(&o_full[i], (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
+        if (__any_sync(0xffffffffu, grow)) {
+          tc::tc_after_sync();
+          const float f = grow ? ex2((top - m) * s2) : 1.f;
+          sum *= f;
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tc::tmem_ld16(o_lane + c, o);
-          tc::tmem_ld_wait();
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tc::tmem_ld16(o_lane + c, o);
+            tc::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= f;
-          tc::tmem_st16(o_lane + c, o);
+            for (int e = 0; e < 16; ++e) o[e] *= f;
+            tc::tmem_st16(o_lane + c, o);
+          }
+          tc::tmem_st_wait();
         }
       }
       if (grow) top = m;
       const float ref = top == -INFINITY ? 0.f : top * s2;
+      float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        float w[16];
+      for (int c = 0; c < 128; c += 8) {
+        uint4 w;
+        uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < 8; e += 2) {
           x[c + e] = ex2(fmaf(x[c + e], s2, -ref));
           x[c + e + 1] = ex2(fmaf(x[c + e + 1], s2, -ref));
-          w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
+          wp[e / 2] = __float_as_uint(bf16_pair(x[c + e], x[c + e + 1]));
+          a0 += x[c + e];
+          a1 += x[c + e + 1];
         }
-        tc::tmem_st16(s_lane + c / 2, w);
-        if (kFine) {  // what the rounding left, behind the 64 columns of the high parts
+        *reinterpret_cast<uint4*>(prow + c / 64 * 16384 + ((c / 8 % 8) ^ (r & 7)) * 16) = w;
+        if (kFine) {  // what the rounding left
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint32_t hi = __float_as_uint(w[e / 2]);
-            w[e / 2] = bf16_pair(x[c + e] - __uint_as_float(hi << 16), x[c + e + 1] - __uint_as_float(hi & 0xffff0000u));
+          for (int e = 0; e < 8; e += 2) {
+            x[c + e] -= __uint_as_float(wp[e / 2] << 16);
+            x[c + e + 1] -= __uint_as_float(wp[e / 2] & 0xffff0000u);
           }
-          tc::tmem_st16(s_lane + 64 + c / 2, w);
         }
       }
-      tc::tmem_st_wait();
+      sum += a0 + a1;
+      if (kFine) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          float w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
+          tc::tmem_st16(s_lane + c / 2, w);
+        }
+        tc::tmem_st_wait();
+      }
+      tc::fence_proxy_async();
       tc::tc_before_sync();
       tc::mbar_arrive(&p_full[i]);
-      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll
-      for (int c = 0; c < 128; c += 4) {
-        a0 += x[c];
-        a1 += x[c + 1];
-        a2 += x[c + 2];
-        a3 += x[c + 3];
-      }
-      sum += (a0 + a1) + (a2 + a3);
+      if (kFine) tc::mbar_arrive(&s_free[i]);  // the next scores follow this tile's product
     }
     if (mine.count) {
-      warp_wait(&o_full[i], 0, a.err, tc::kErrTimeoutMma, ab);
+      warp_wait(&o_full[i], (mine.count - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
       tc::tc_after_sync();
       const bool live = t < a.T;
       const size_t row = ((size_t)b * a.T + t) * a.H + h;
@@ -319,34 +389,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
 
 template <int D>
 struct BwdCfg {
-  static constexpr uint32_t BIG = 128 * D * 2;    // the CTA's own two tiles of 128 rows
-  static constexpr uint32_t SMALL = 64 * D * 2;   // a ring stage holds two tiles of 64 rows
-  static constexpr int STAGES = 4;
-  static constexpr uint32_t RING = 2 * BIG, STAGE = 2 * SMALL;
-  static constexpr uint32_t ROWS = RING + STAGES * STAGE;  // lse2, delta of a stage's 64 queries
-  static constexpr uint32_t BYTES = ROWS + STAGES * 512 + 1024;
-  static constexpr int S_COL = 0, P_COL = 128;    // scores and dP, 64 columns per group each
-  static constexpr int A_COL = 256, B_COL = 384;  // accumulators
+  static constexpr uint32_t TILE = 128 * D * 2;
+  static constexpr int SLOTS = 5;
+  static constexpr uint32_t RING = 2 * TILE;               // behind the CTA's own two tiles
+  static constexpr uint32_t ROWS = RING + SLOTS * TILE;    // dkv: lse2, delta of two query tiles
+  static constexpr uint32_t BARS = ROWS + 2 * 1024;
+  static constexpr uint32_t BYTES = BARS + 256;            // no static shared memory: all 227 KB at d = 128
 };
 
 struct BwdBars {
-  uint64_t own, full[4], empty[4], s_full[2], w_full[2], done;
+  uint64_t own, full[5], empty[5], s_full[2], dp_full, p_ready, ds_ready[2], done;
   uint32_t tmem;
   int abort_flag;
 };
+static_assert(sizeof(BwdBars) <= 256, "barriers fit behind the tiles");
 
-__device__ __forceinline__ uint32_t bwd_setup(BwdBars& s) {
+// The kernels' tiles need the dynamic shared memory to start on 1024 bytes,
+// which it does where there is no static one; checked, since the swizzle
+// depends on it.
+// `chains`: MMA chains that a slot's tile and an accumulator's end wait for.
+__device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int chains, int* err) {
+  if (tc::smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(err, tc::kErrTimeoutLoad);
+    return false;
+  }
   if (threadIdx.x == 0) {
     tc::mbar_init(&s.own, 1);
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 5; ++i) {
       tc::mbar_init(&s.full[i], 1);
-      tc::mbar_init(&s.empty[i], 1);
+      tc::mbar_init(&s.empty[i], chains);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&s.s_full[i], 1);
-      tc::mbar_init(&s.w_full[i], 128);
-    }
-    tc::mbar_init(&s.done, 1);
+    tc::mbar_init(&s.s_full[0], 1);
+    tc::mbar_init(&s.s_full[1], 1);
+    tc::mbar_init(&s.dp_full, 1);
+    tc::mbar_init(&s.p_ready, 256);
+    tc::mbar_init(&s.ds_ready[0], 256);
+    tc::mbar_init(&s.ds_ready[1], 256);
+    tc::mbar_init(&s.done, chains);
     tc::mbar_init_fence();
     s.abort_flag = 0;
   }
@@ -354,7 +433,7 @@ __device__ __forceinline__ uint32_t bwd_setup(BwdBars& s) {
   tc::tc_before_sync();
   __syncthreads();
   tc::tc_after_sync();
-  return s.tmem;
+  return true;
 }
 
 __device__ __forceinline__ void bwd_finish(uint32_t tmem) {
@@ -364,56 +443,40 @@ __device__ __forceinline__ void bwd_finish(uint32_t tmem) {
   if (threadIdx.x < 32) tc::tmem_dealloc(tmem, 512);
 }
 
-// The products of both backward kernels over `count` stages: into group n & 1,
-// S = own0 stage0^T and dP = own1 stage1^T (128 x 64, K = d); then, from the
-// weights that the group put over them, acc_b += W_dP stage0 (dS with k or q)
-// and, with kTwo, acc_a += W_S stage1 (P^T with dO).  Without kTwo dS lies over S.
-template <int D, bool kTwo>
-__device__ __forceinline__ void bwd_products(BwdBars& s, unsigned char* sm, uint32_t tmem, int count, int* err) {
+// The ring of a backward kernel as its MMA threads see it.
+template <int D>
+struct BwdRing {
   using Cf = BwdCfg<D>;
-  volatile int* ab = &s.abort_flag;
-  const uint32_t ID_S = tc::idesc(128, 64, 1), ID_A = tc::idesc(128, D, 1) | tc::kMajorB;
-  const uint32_t base = tc::smem_u32(sm);
-  const auto scores = [&](int n) {
-    const uint32_t stage = base + Cf::RING + n % Cf::STAGES * Cf::STAGE;
-    const int g = n & 1;
-    tc::mbar_wait<false>(&s.full[n % Cf::STAGES], (n / Cf::STAGES) & 1, err, tc::kErrTimeoutLoad, ab);
+  BwdBars& s;
+  uint32_t base;
+  int loads;
+  int* err;
+  __device__ uint32_t landed(int load) const {
+    tc::mbar_wait<false>(&s.full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, err, tc::kErrTimeoutLoad, &s.abort_flag);
     tc::tc_after_sync();
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t o = k / 4 * 16384 + k % 4 * 32, p = k / 4 * 8192 + k % 4 * 32;
-      tc::mma_bf16_ss(tmem + Cf::S_COL + g * 64, tc::desc_sw128(base + o), tc::desc_sw128(stage + p), ID_S, k > 0);
-    }
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t o = k / 4 * 16384 + k % 4 * 32, p = k / 4 * 8192 + k % 4 * 32;
-      tc::mma_bf16_ss(tmem + Cf::P_COL + g * 64, tc::desc_sw128(base + Cf::BIG + o),
-                      tc::desc_sw128(stage + Cf::SMALL + p), ID_S, k > 0);
-    }
-    tc::mma_commit(&s.s_full[g]);
-  };
-  tc::mbar_wait<false>(&s.own, 0, err, tc::kErrTimeoutLoad, ab);
-  scores(0);
-  if (count > 1) scores(1);
-  for (int n = 0; n < count && !*ab; ++n) {
-    const uint32_t stage = base + Cf::RING + n % Cf::STAGES * Cf::STAGE;
-    const int g = n & 1;
-    tc::mbar_wait<false>(&s.w_full[g], (n >> 1) & 1, err, tc::kErrTimeoutMma, ab);
-    tc::tc_after_sync();
-    if (kTwo) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc::mma_bf16_ts(tmem + Cf::A_COL, tmem + Cf::S_COL + g * 64 + k * 8,
-                        tc::desc_sw128_mn(stage + Cf::SMALL + k * 2048, 8192u), ID_A, n > 0 || k > 0);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      tc::mma_bf16_ts(tmem + Cf::B_COL, tmem + (kTwo ? Cf::P_COL : Cf::S_COL) + g * 64 + k * 8,
-                      tc::desc_sw128_mn(stage + k * 2048, 8192u), ID_A, n > 0 || k > 0);
-    if (n + Cf::STAGES < count) tc::mma_commit(&s.empty[n % Cf::STAGES]);
-    if (n + 1 == count) tc::mma_commit(&s.done);
-    if (n + 2 < count) scores(n + 2);
+    return base + Cf::RING + load % Cf::SLOTS * Cf::TILE;
   }
+  __device__ uint32_t at(int load) const { return base + Cf::RING + load % Cf::SLOTS * Cf::TILE; }  // landed before
+  __device__ void release(int load) const {  // only where the slot is loaded again
+    if (load + Cf::SLOTS < loads) tc::mma_commit(&s.empty[load % Cf::SLOTS]);
+  }
+  __device__ void ready(uint64_t* bar, int use) const {
+    tc::mbar_wait<false>(bar, use & 1, err, tc::kErrTimeoutMma, &s.abort_flag);
+    tc::tc_after_sync();
+  }
+};
+
+// 64 weights of this thread's row, rounded, as the A operand at `dst`.
+__device__ __forceinline__ void store_weights(uint32_t dst, const float (&x)[64]) {
+#pragma unroll
+  for (int c = 0; c < 64; c += 32) {
+    float w[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
+    tc::tmem_st16(dst + c / 2, w);
+  }
+  tc::tmem_st_wait();
+  tc::tc_before_sync();
 }
 
 template <int D>
@@ -421,74 +484,99 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, SwaArgs a, SwaBwdLayout L) {
   using Cf = BwdCfg<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ BwdBars s;
+  constexpr int DP = 256, DQ = 384;  // TMEM: two buffers of scores, dP, dq
+  extern __shared__ __align__(1024) unsigned char sm[];
+  BwdBars& s = *reinterpret_cast<BwdBars*>(sm + Cf::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * 128, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (a.H / a.Hk), W = a.window, S = a.sinks;
-  const KeyRange keys(q0, q0 + 128 < a.T ? q0 + 128 : a.T, W, S, 64);
-  const uint32_t tmem = bwd_setup(s);
+  const KeyRange keys(q0, q0 + 128 < a.T ? q0 + 128 : a.T, W, S, 128);
+  if (!bwd_setup(sm, s, 1, a.err)) return;
+  const uint32_t tmem = s.tmem;
   volatile int* ab = &s.abort_flag;
+  const int count = keys.count;
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      tc::mbar_expect_tx(&s.own, 2 * Cf::BIG);
-      for (int c = 0; c < D; c += 64) {
-        tc::tma_load_4d(sm + c * 256, &tq, c, h, q0, b, &s.own);
-        tc::tma_load_4d(sm + Cf::BIG + c * 256, &tg, c, h, q0, b, &s.own);
-      }
-      for (int n = 0; n < keys.count; ++n) {
-        const int slot = n % Cf::STAGES, use = n / Cf::STAGES, k0 = keys.tile(n) * 64;
+      tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
+      load_tile<D>(sm, &tq, h, q0, b, &s.own);
+      load_tile<D>(sm + Cf::TILE, &tg, h, q0, b, &s.own);
+      for (int n = 0; n < 2 * count; ++n) {  // k0 v0 k1 v1 ..
+        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS;
         if (use && !tc::mbar_wait<false>(&s.empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-        unsigned char* st = sm + Cf::RING + slot * Cf::STAGE;
-        tc::mbar_expect_tx(&s.full[slot], Cf::STAGE);
-        for (int c = 0; c < D; c += 64) {
-          tc::tma_load_4d(st + c * 128, &tk, c, hk, k0, b, &s.full[slot]);
-          tc::tma_load_4d(st + Cf::SMALL + c * 128, &tv, c, hk, k0, b, &s.full[slot]);
-        }
+        tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
+        load_tile<D>(sm + Cf::RING + slot * Cf::TILE, n & 1 ? &tv : &tk, hk, keys.tile(n / 2) * 128, b, &s.full[slot]);
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) bwd_products<D, false>(s, sm, tmem, keys.count, a.err);
+  } else if (warp == kMmaWarp) {  // scores and dq
+    if (lane == 0) {
+      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      ring.ready(&s.own, 0);
+      mma_scores<D>(tmem, ring.base, ring.landed(0));
+      tc::mma_commit(&s.s_full[0]);
+      for (int n = 0; n < count && !*ab; ++n) {
+        if (n + 1 < count) {  // the next scores, while the groups work on dS
+          mma_scores<D>(tmem + (n + 1) % 2 * 128, ring.base, ring.landed(2 * n + 2));
+          tc::mma_commit(&s.s_full[(n + 1) % 2]);
+        }
+        ring.ready(&s.ds_ready[n % 2], n >> 1);
+        mma_mix<D>(tmem + DQ, tmem + n % 2 * 128, ring.at(2 * n), n > 0);
+        ring.release(2 * n);
+      }
+      tc::mma_commit(&s.done);
+    }
+  } else if (warp == kMmaWarp + 1) {  // dP, when the groups have read the one before
+    if (lane == 0) {
+      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      ring.ready(&s.own, 0);
+      for (int n = 0; n < count && !*ab; ++n) {
+        const uint32_t v = ring.landed(2 * n + 1);
+        if (n > 0) ring.ready(&s.ds_ready[(n - 1) % 2], (n - 1) >> 1);
+        mma_scores<D>(tmem + DP, ring.base + Cf::TILE, v);
+        tc::mma_commit(&s.dp_full);
+        ring.release(2 * n + 1);
+      }
+    }
   } else {
     const int g = warp >> 2, t = q0 + (tid & 127);
-    const uint32_t s_lane = tc::tmem_lane_addr(tmem, warp, Cf::S_COL + g * 64);
-    const uint32_t p_lane = tc::tmem_lane_addr(tmem, warp, Cf::P_COL + g * 64);
+    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, g * 64);
     const size_t at = ((size_t)b * a.H + h) * L.Tp + t;
     const float lse2 = reinterpret_cast<const float*>(a.ws + L.lse2)[at];
     const float delta = reinterpret_cast<const float*>(a.ws + L.delta)[at];
     const float s2 = a.scale * kLog2e;
-    for (int n = g; n < keys.count; n += 2) {
-      const int k0 = keys.tile(n) * 64;
-      if (!warp_wait(&s.s_full[g], (n >> 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+    for (int n = 0; n < count; ++n) {
+      const int k0 = keys.tile(n) * 128;
+      const uint32_t buf = lanes + n % 2 * 128;
+      if (!warp_wait(&s.s_full[n % 2], (n >> 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
-      const bool all = k0 + 63 <= q0 && (q0 + 127 - k0 < W || k0 + 63 < S);
+      float x[64];
+      tc::tmem_ld32(buf, x);
+      tc::tmem_ld32(buf + 32, x + 32);
+      tc::tmem_ld_wait();
+      if (!(k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S))) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          x[e] = visible(t, k0 + g * 64 + e, W, S) && !single_key(t, W, S) ? x[e] : -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < 64; ++e) x[e] = ex2(fmaf(x[e], s2, -lse2));
+      if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+      tc::tc_after_sync();
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
-        float x[32], dp[32], w[16];
-        tc::tmem_ld32(s_lane + c, x);
-        tc::tmem_ld32(p_lane + c, dp);
+        float dp[32];
+        tc::tmem_ld32(lanes + DP + c, dp);
         tc::tmem_ld_wait();
-        if (!all) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = visible(t, k0 + c + e, W, S) && !single_key(t, W, S) ? x[e] : -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = ex2(fmaf(x[e], s2, -lse2)) * (dp[e] - delta);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[e], x[e + 1]);
-        tc::tmem_st16(s_lane + c / 2, w);
+        for (int e = 0; e < 32; ++e) x[c + e] *= dp[e] - delta;
       }
-      tc::tmem_st_wait();
-      tc::tc_before_sync();
-      tc::mbar_arrive(&s.w_full[g]);
+      store_weights(buf, x);
+      tc::mbar_arrive(&s.ds_ready[n % 2]);
     }
     warp_wait(&s.done, 0, a.err, tc::kErrTimeoutMma, ab);
     tc::tc_after_sync();
     if (g == 0) {
       const size_t row = ((size_t)b * a.T + t) * a.H + h;
-      store_lane<D>(tc::tmem_lane_addr(tmem, warp, Cf::B_COL), a.scale,
+      store_lane<D>(tc::tmem_lane_addr(tmem, warp, DQ), a.scale,
                     t < a.T ? static_cast<__nv_bfloat16*>(a.dq) + row * D : nullptr, nullptr);
     }
   }
@@ -503,9 +591,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg, SwaArgs a, SwaBwdLayout L,
     int tiles, int has_far) {
   using Cf = BwdCfg<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ BwdBars s;
+  constexpr int DP = 128, DV = 256, DK = 384;  // TMEM: scores, dP, dv, dk
+  extern __shared__ __align__(1024) unsigned char sm[];
+  BwdBars& s = *reinterpret_cast<BwdBars*>(sm + Cf::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.z, group = a.H / a.Hk, W = a.window, S = a.sinks;
   const bool far = (int)blockIdx.x >= tiles;
@@ -523,86 +611,131 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     q_lo = k0;
     q_hi = band_end;
   }
-  const int hk = h0 / group, qt0 = q_lo / 64, per = (q_hi - 1) / 64 - qt0 + 1, count = per * heads;
-  const uint32_t tmem = bwd_setup(s);
+  const int hk = h0 / group, qt0 = q_lo / 128, per = (q_hi - 1) / 128 - qt0 + 1, count = per * heads;
+  if (!bwd_setup(sm, s, 2, a.err)) return;
+  const uint32_t tmem = s.tmem;
   volatile int* ab = &s.abort_flag;
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      tc::mbar_expect_tx(&s.own, 2 * Cf::BIG);
-      for (int c = 0; c < D; c += 64) {
-        tc::tma_load_4d(sm + c * 256, &tk, c, hk, k0, b, &s.own);
-        tc::tma_load_4d(sm + Cf::BIG + c * 256, &tv, c, hk, k0, b, &s.own);
-      }
-      for (int n = 0; n < count; ++n) {
-        const int slot = n % Cf::STAGES, use = n / Cf::STAGES, h = h0 + n / per, t0 = (qt0 + n % per) * 64;
+      tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
+      load_tile<D>(sm, &tk, hk, k0, b, &s.own);
+      load_tile<D>(sm + Cf::TILE, &tv, hk, k0, b, &s.own);
+      for (int n = 0; n < 2 * count; ++n) {  // q0 dO0 q1 dO1 ..; lse2 and delta with q
+        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS, i = n / 2, h = h0 + i / per, t0 = (qt0 + i % per) * 128;
         if (use && !tc::mbar_wait<false>(&s.empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-        unsigned char* st = sm + Cf::RING + slot * Cf::STAGE;
-        float* rows = reinterpret_cast<float*>(sm + Cf::ROWS + slot * 512);
-        const size_t at = ((size_t)b * a.H + h) * L.Tp + t0;
-        tc::mbar_expect_tx(&s.full[slot], Cf::STAGE + 512);
-        for (int c = 0; c < D; c += 64) {
-          tc::tma_load_4d(st + c * 128, &tq, c, h, t0, b, &s.full[slot]);
-          tc::tma_load_4d(st + Cf::SMALL + c * 128, &tg, c, h, t0, b, &s.full[slot]);
+        unsigned char* st = sm + Cf::RING + slot * Cf::TILE;
+        if (n & 1) {
+          tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
+          load_tile<D>(st, &tg, h, t0, b, &s.full[slot]);
+        } else {
+          // the rows of two tiles ago share this tile's place: the groups are
+          // through with them when that tile's q is released
+          if (i >= 2 && !tc::mbar_wait<false>(&s.empty[(n - 4) % Cf::SLOTS], ((n - 4) / Cf::SLOTS) & 1, a.err,
+                                              tc::kErrTimeoutLoad, ab))
+            break;
+          float* rows = reinterpret_cast<float*>(sm + Cf::ROWS + i % 2 * 1024);
+          const size_t at = ((size_t)b * a.H + h) * L.Tp + t0;
+          tc::mbar_expect_tx(&s.full[slot], Cf::TILE + 1024);
+          load_tile<D>(st, &tq, h, t0, b, &s.full[slot]);
+          tc::bulk_g2s(rows, reinterpret_cast<const float*>(a.ws + L.lse2) + at, 512, &s.full[slot]);
+          tc::bulk_g2s(rows + 128, reinterpret_cast<const float*>(a.ws + L.delta) + at, 512, &s.full[slot]);
         }
-        tc::bulk_g2s(rows, reinterpret_cast<const float*>(a.ws + L.lse2) + at, 256, &s.full[slot]);
-        tc::bulk_g2s(rows + 64, reinterpret_cast<const float*>(a.ws + L.delta) + at, 256, &s.full[slot]);
       }
     }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) bwd_products<D, true>(s, sm, tmem, count, a.err);
+  } else if (warp == kMmaWarp) {  // scores and dv
+    if (lane == 0) {
+      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      ring.ready(&s.own, 0);
+      for (int n = 0; n < count && !*ab; ++n) {
+        // over P of the tile before, which the product before reads: one
+        // thread's MMAs run in order
+        mma_scores<D>(tmem, ring.base, ring.landed(2 * n));
+        tc::mma_commit(&s.s_full[0]);
+        ring.release(2 * n);
+        const uint32_t g = ring.landed(2 * n + 1);
+        ring.ready(&s.p_ready, n);
+        mma_mix<D>(tmem + DV, tmem, g, n > 0);
+        ring.release(2 * n + 1);
+      }
+      tc::mma_commit(&s.done);
+    }
+  } else if (warp == kMmaWarp + 1) {  // dP and dk
+    if (lane == 0) {
+      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      ring.ready(&s.own, 0);
+      for (int n = 0; n < count && !*ab; ++n) {
+        mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(2 * n + 1));
+        tc::mma_commit(&s.dp_full);
+        ring.release(2 * n + 1);
+        const uint32_t q = ring.landed(2 * n);
+        ring.ready(&s.ds_ready[0], n);
+        mma_mix<D>(tmem + DK, tmem + DP, q, n > 0);
+        ring.release(2 * n);
+      }
+      tc::mma_commit(&s.done);
+    }
   } else {
     const int g = warp >> 2, key = k0 + (tid & 127);
-    const uint32_t s_lane = tc::tmem_lane_addr(tmem, warp, Cf::S_COL + g * 64);
-    const uint32_t p_lane = tc::tmem_lane_addr(tmem, warp, Cf::P_COL + g * 64);
+    const uint32_t buf = tc::tmem_lane_addr(tmem, warp, g * 64);
     const float s2 = a.scale * kLog2e;
-    for (int n = g; n < count; n += 2) {
-      const int q0 = (qt0 + n % per) * 64, slot = n % Cf::STAGES;
-      const float4* rows = reinterpret_cast<const float4*>(sm + Cf::ROWS + slot * 512);
-      // the scores' commit follows the stage's arrival, but only this wait lets
-      // this thread read what the copy wrote
-      if (!warp_wait(&s.full[slot], (n / Cf::STAGES) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-      if (!warp_wait(&s.s_full[g], (n >> 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+    for (int n = 0; n < count; ++n) {
+      const int q0 = (qt0 + n % per) * 128, slot = 2 * n % Cf::SLOTS;
+      const float4* rows = reinterpret_cast<const float4*>(sm + Cf::ROWS + n % 2 * 1024) + g * 16;
+      // the scores' commit follows the arrival of q and its rows, but only this
+      // wait lets this thread read what the copy wrote
+      if (!warp_wait(&s.full[slot], (2 * n / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+      if (!warp_wait(&s.s_full[0], n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
-      const bool all = k0 + 127 <= q0 && (q0 + 63 - k0 < W || k0 + 127 < S) && q0 >= q_lo && q0 + 63 < q_hi;
+      float x[64];
+      tc::tmem_ld32(buf, x);
+      tc::tmem_ld32(buf + 32, x + 32);
+      tc::tmem_ld_wait();
+      const bool every = k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S) && q0 >= q_lo && q0 + 127 < q_hi;
+      if (!every) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const int t = q0 + g * 64 + e;
+          x[e] = t >= q_lo && t < q_hi && visible(t, key, W, S) ? x[e] : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        const float4 l = rows[e / 4];
+        x[e] = ex2(fmaf(x[e], s2, -l.x));
+        x[e + 1] = ex2(fmaf(x[e + 1], s2, -l.y));
+        x[e + 2] = ex2(fmaf(x[e + 2], s2, -l.z));
+        x[e + 3] = ex2(fmaf(x[e + 3], s2, -l.w));
+      }
+      store_weights(buf, x);
+      tc::mbar_arrive(&s.p_ready);
+      if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+      tc::tc_after_sync();
 #pragma unroll
       for (int c = 0; c < 64; c += 32) {
-        float x[32], dp[32], w[16];
-        tc::tmem_ld32(s_lane + c, x);
-        tc::tmem_ld32(p_lane + c, dp);
+        float dp[32];
+        tc::tmem_ld32(buf + DP + c, dp);
         tc::tmem_ld_wait();
-        if (!all) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int t = q0 + c + e;
-            x[e] = t >= q_lo && t < q_hi && visible(t, key, W, S) ? x[e] : -INFINITY;
-            if (single_key(t, W, S)) dp[e] = INFINITY;  // marks dS = 0 below
-          }
-        }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 l = rows[(c + e) / 4], d = rows[16 + (c + e) / 4];
-          const float ls[4] = {l.x, l.y, l.z, l.w}, ds[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[e + k] = ex2(fmaf(x[e + k], s2, -ls[k]));
-            dp[e + k] = !all && dp[e + k] == INFINITY ? 0.f : x[e + k] * (dp[e + k] - ds[k]);
-          }
+          const float4 d = rows[32 + (c + e) / 4];
+          x[c + e] *= dp[e] - d.x;
+          x[c + e + 1] *= dp[e + 1] - d.y;
+          x[c + e + 2] *= dp[e + 2] - d.z;
+          x[c + e + 3] *= dp[e + 3] - d.w;
         }
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[e], x[e + 1]);
-        tc::tmem_st16(s_lane + c / 2, w);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(dp[e], dp[e + 1]);
-        tc::tmem_st16(p_lane + c / 2, w);
       }
-      tc::tmem_st_wait();
-      tc::tc_before_sync();
-      tc::mbar_arrive(&s.w_full[g]);
+      if (!every) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (single_key(q0 + g * 64 + e, W, S)) x[e] = 0.f;
+      }
+      store_weights(buf + DP, x);
+      tc::mbar_arrive(&s.ds_ready[0]);
     }
     warp_wait(&s.done, 0, a.err, tc::kErrTimeoutMma, ab);
     tc::tc_after_sync();
     // group 0 writes dv, group 1 dk
-    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, g ? Cf::B_COL : Cf::A_COL);
+    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, g ? DK : DV);
     const float f = g ? a.scale : 1.f;
     const bool first = key < S && key < a.T && has_far;  // rows that other items add to: fp32 parts
     float* part = nullptr;
@@ -662,12 +795,10 @@ template <int D>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   using Cf = BwdCfg<D>;
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
-  CUtensorMap big[4], small[4];  // q, dO, k, v with 128 and 64 rows to a box
+  CUtensorMap m[4];
   const void* src[4] = {a.q, a.dO, a.k, a.v};
   for (int i = 0; i < 4; ++i)
-    if (!make_tmap_bthd(&big[i], src[i], 2, a.B, a.T, i < 2 ? a.H : a.Hk, D, 64, true, 128) ||
-        !make_tmap_bthd(&small[i], src[i], 2, a.B, a.T, i < 2 ? a.H : a.Hk, D, 64, true, 64))
-      return cudaErrorInvalidValue;
+    if (!make_tmap_bthd(&m[i], src[i], 2, a.B, a.T, i < 2 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
   cudaError_t e = allow_smem(swa_dkv_tc_kernel<D>, Cf::BYTES);
   if (e == cudaSuccess) e = allow_smem(swa_dq_tc_kernel<D>, Cf::BYTES);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
@@ -676,10 +807,10 @@ cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   const int has_far = a.sinks > 0 && 127 + a.window < a.T;
   prof_begin(st, "swa_dkv_tc");
   swa_dkv_tc_kernel<D><<<dim3(tiles + (has_far ? L.pieces : 0), has_far ? a.H : a.Hk, a.B), kTcThreads, Cf::BYTES, st>>>(
-      big[2], big[3], small[0], small[1], a, L, tiles, has_far);
+      m[2], m[3], m[0], m[1], a, L, tiles, has_far);
   prof_end(st);
   prof_begin(st, "swa_dq_tc");
-  swa_dq_tc_kernel<D><<<dim3(tiles, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(big[0], big[1], small[2], small[3], a, L);
+  swa_dq_tc_kernel<D><<<dim3(tiles, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(m[0], m[1], m[2], m[3], a, L);
   prof_end(st);
   e = cudaGetLastError();
   if (e == cudaSuccess && has_far) e = launch_swa_sink_sum(a, L, 128, st);
