@@ -26,9 +26,11 @@
 //
 // Backward: p is recomputed from the saved lse.  dk, dv: 128 keys per CTA
 // (rows are keys: S^T = k q^T, dP^T = v dO^T), 128 queries at a time; dv +=
-// P^T dO, dk += dS^T q.  dq: 128 queries per CTA; dq += dS k.  The weights go
-// over the scores in TMEM, and the two groups take half of the columns of each
-// tile; p is formed while dP is still being multiplied.  (64-column tiles, two
+// P^T dO, dk += dS^T q.  dq: 128 queries per CTA; dq += dS k.  The two groups
+// take half of the columns of each tile; p is formed while dP is still being
+// multiplied.  dS goes over dP (dq: over the scores, of which it has two
+// buffers) in TMEM; dkv's p goes to shared memory, so that the next scores
+// need not wait for dv.  (64-column tiles, two
 // at a time, a group to each: 0.88 and 0.75 ms in place of DKV_MS and DQ_MS at
 // H16 T16384 d128 window 2048.)  Seven products in place of the five of one
 // joint pass, but no atomics and no fp32 copy of dq: every sum has one order.
@@ -387,18 +389,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
 
 // ---- backward ----------------------------------------------------------------
 
-template <int D>
+// The CTA's own two tiles, a ring of tiles, and for dkv (which has one slot
+// less) the weights p.
+template <int D, bool kDkv>
 struct BwdCfg {
   static constexpr uint32_t TILE = 128 * D * 2;
-  static constexpr int SLOTS = 5;
-  static constexpr uint32_t RING = 2 * TILE;               // behind the CTA's own two tiles
-  static constexpr uint32_t ROWS = RING + SLOTS * TILE;    // dkv: lse2, delta of two query tiles
+  static constexpr int SLOTS = kDkv ? 4 : 5;
+  static constexpr uint32_t RING = 2 * TILE;
+  static constexpr uint32_t P = RING + SLOTS * TILE;
+  static constexpr uint32_t ROWS = P + (kDkv ? 32768 : 0);  // dkv: lse2, delta of two query tiles
   static constexpr uint32_t BARS = ROWS + 2 * 1024;
   static constexpr uint32_t BYTES = BARS + 256;            // no static shared memory: all 227 KB at d = 128
 };
 
 struct BwdBars {
-  uint64_t own, full[5], empty[5], s_full[2], dp_full, p_ready, ds_ready[2], done;
+  uint64_t own, full[5], empty[5], s_full[2], s_free, dp_full, p_ready, p_read, ds_ready[2], done;
   uint32_t tmem;
   int abort_flag;
 };
@@ -421,8 +426,10 @@ __device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int cha
     }
     tc::mbar_init(&s.s_full[0], 1);
     tc::mbar_init(&s.s_full[1], 1);
+    tc::mbar_init(&s.s_free, 256);
     tc::mbar_init(&s.dp_full, 1);
     tc::mbar_init(&s.p_ready, 256);
+    tc::mbar_init(&s.p_read, 1);
     tc::mbar_init(&s.ds_ready[0], 256);
     tc::mbar_init(&s.ds_ready[1], 256);
     tc::mbar_init(&s.done, chains);
@@ -444,9 +451,8 @@ __device__ __forceinline__ void bwd_finish(uint32_t tmem) {
 }
 
 // The ring of a backward kernel as its MMA threads see it.
-template <int D>
+template <typename Cf>
 struct BwdRing {
-  using Cf = BwdCfg<D>;
   BwdBars& s;
   uint32_t base;
   int loads;
@@ -483,7 +489,7 @@ template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, SwaArgs a, SwaBwdLayout L) {
-  using Cf = BwdCfg<D>;
+  using Cf = BwdCfg<D, false>;
   constexpr int DP = 256, DQ = 384;  // TMEM: two buffers of scores, dP, dq
   extern __shared__ __align__(1024) unsigned char sm[];
   BwdBars& s = *reinterpret_cast<BwdBars*>(sm + Cf::BARS);
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     }
   } else if (warp == kMmaWarp) {  // scores and dq
     if (lane == 0) {
-      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
       ring.ready(&s.own, 0);
       mma_scores<D>(tmem, ring.base, ring.landed(0));
       tc::mma_commit(&s.s_full[0]);
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     }
   } else if (warp == kMmaWarp + 1) {  // dP, when the groups have read the one before
     if (lane == 0) {
-      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
       ring.ready(&s.own, 0);
       for (int n = 0; n < count && !*ab; ++n) {
         const uint32_t v = ring.landed(2 * n + 1);
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg, SwaArgs a, SwaBwdLayout L,
     int tiles, int has_far) {
-  using Cf = BwdCfg<D>;
+  using Cf = BwdCfg<D, true>;
   constexpr int DP = 128, DV = 256, DK = 384;  // TMEM: scores, dP, dv, dk
   extern __shared__ __align__(1024) unsigned char sm[];
   BwdBars& s = *reinterpret_cast<BwdBars*>(sm + Cf::BARS);
@@ -628,11 +634,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
           tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
           load_tile<D>(st, &tg, h, t0, b, &s.full[slot]);
         } else {
-          // the rows of two tiles ago share this tile's place: the groups are
-          // through with them when that tile's q is released
-          if (i >= 2 && !tc::mbar_wait<false>(&s.empty[(n - 4) % Cf::SLOTS], ((n - 4) / Cf::SLOTS) & 1, a.err,
-                                              tc::kErrTimeoutLoad, ab))
-            break;
+          // the rows of two tiles ago were in this place, and that tile's q in
+          // this slot: the groups were through with them when it was released
+          static_assert(Cf::SLOTS == 4, "rows and q of a tile are replaced together");
           float* rows = reinterpret_cast<float*>(sm + Cf::ROWS + i % 2 * 1024);
           const size_t at = ((size_t)b * a.H + h) * L.Tp + t0;
           tc::mbar_expect_tx(&s.full[slot], Cf::TILE + 1024);
@@ -644,24 +648,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     }
   } else if (warp == kMmaWarp) {  // scores and dv
     if (lane == 0) {
-      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
       ring.ready(&s.own, 0);
-      for (int n = 0; n < count && !*ab; ++n) {
-        // over P of the tile before, which the product before reads: one
-        // thread's MMAs run in order
-        mma_scores<D>(tmem, ring.base, ring.landed(2 * n));
+      const auto scores = [&](int n) {
+        const uint32_t q = ring.landed(2 * n);
+        if (n > 0) ring.ready(&s.s_free, n - 1);
+        mma_scores<D>(tmem, ring.base, q);
         tc::mma_commit(&s.s_full[0]);
         ring.release(2 * n);
-        const uint32_t g = ring.landed(2 * n + 1);
+      };
+      scores(0);
+      for (int n = 0; n < count && !*ab; ++n) {
+        if (n + 1 < count) scores(n + 1);  // while the groups work on p
+        const uint32_t g = ring.landed(2 * n + 1), p = ring.base + Cf::P;
         ring.ready(&s.p_ready, n);
-        mma_mix<D>(tmem + DV, tmem, g, n > 0);
+        constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          tc::mma_bf16_ss(tmem + DV, tc::desc_sw128(p + i / 4 * 16384 + i % 4 * 32),
+                          tc::desc_sw128_mn(g + i * 2048, 16384u), id, n > 0 || i > 0);
+        tc::mma_commit(&s.p_read);
         ring.release(2 * n + 1);
       }
       tc::mma_commit(&s.done);
     }
   } else if (warp == kMmaWarp + 1) {  // dP and dk
     if (lane == 0) {
-      const BwdRing<D> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
       ring.ready(&s.own, 0);
       for (int n = 0; n < count && !*ab; ++n) {
         mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(2 * n + 1));
@@ -678,6 +691,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     const int g = warp >> 2, key = k0 + (tid & 127);
     const uint32_t buf = tc::tmem_lane_addr(tmem, warp, g * 64);
     const float s2 = a.scale * kLog2e;
+    // this key's row of the weights, the group's 64 columns: 16-byte chunk c at
+    // (c ^ (row & 7)) * 16
+    unsigned char* prow = sm + Cf::P + g * 16384 + (tid & 127) * 128;
     for (int n = 0; n < count; ++n) {
       const int q0 = (qt0 + n % per) * 128, slot = 2 * n % Cf::SLOTS;
       const float4* rows = reinterpret_cast<const float4*>(sm + Cf::ROWS + n % 2 * 1024) + g * 16;
@@ -690,6 +706,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       tc::tmem_ld32(buf, x);
       tc::tmem_ld32(buf + 32, x + 32);
       tc::tmem_ld_wait();
+      tc::tc_before_sync();
+      tc::mbar_arrive(&s.s_free);
       const bool every = k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S) && q0 >= q_lo && q0 + 127 < q_hi;
       if (!every) {
 #pragma unroll
@@ -706,7 +724,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
         x[e + 2] = ex2(fmaf(x[e + 2], s2, -l.z));
         x[e + 3] = ex2(fmaf(x[e + 3], s2, -l.w));
       }
-      store_weights(buf, x);
+      if (n > 0 && !warp_wait(&s.p_read, (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint4 w;
+        uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wp[e] = __float_as_uint(bf16_pair(x[c * 8 + 2 * e], x[c * 8 + 2 * e + 1]));
+        *reinterpret_cast<uint4*>(prow + (c ^ (tid & 7)) * 16) = w;
+      }
+      tc::fence_proxy_async();
       tc::mbar_arrive(&s.p_ready);
       if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
@@ -793,24 +820,25 @@ cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
-  using Cf = BwdCfg<D>;
+  using CfKv = BwdCfg<D, true>;
+  using CfQ = BwdCfg<D, false>;
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
   CUtensorMap m[4];
   const void* src[4] = {a.q, a.dO, a.k, a.v};
   for (int i = 0; i < 4; ++i)
     if (!make_tmap_bthd(&m[i], src[i], 2, a.B, a.T, i < 2 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(swa_dkv_tc_kernel<D>, Cf::BYTES);
-  if (e == cudaSuccess) e = allow_smem(swa_dq_tc_kernel<D>, Cf::BYTES);
+  cudaError_t e = allow_smem(swa_dkv_tc_kernel<D>, CfKv::BYTES);
+  if (e == cudaSuccess) e = allow_smem(swa_dq_tc_kernel<D>, CfQ::BYTES);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
   if (e != cudaSuccess) return e;
   const int tiles = (a.T + 127) / 128;
   const int has_far = a.sinks > 0 && 127 + a.window < a.T;
   prof_begin(st, "swa_dkv_tc");
-  swa_dkv_tc_kernel<D><<<dim3(tiles + (has_far ? L.pieces : 0), has_far ? a.H : a.Hk, a.B), kTcThreads, Cf::BYTES, st>>>(
+  swa_dkv_tc_kernel<D><<<dim3(tiles + (has_far ? L.pieces : 0), has_far ? a.H : a.Hk, a.B), kTcThreads, CfKv::BYTES, st>>>(
       m[2], m[3], m[0], m[1], a, L, tiles, has_far);
   prof_end(st);
   prof_begin(st, "swa_dq_tc");
-  swa_dq_tc_kernel<D><<<dim3(tiles, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(m[0], m[1], m[2], m[3], a, L);
+  swa_dq_tc_kernel<D><<<dim3(tiles, a.H, a.B), kTcThreads, CfQ::BYTES, st>>>(m[0], m[1], m[2], m[3], a, L);
   prof_end(st);
   e = cudaGetLastError();
   if (e == cudaSuccess && has_far) e = launch_swa_sink_sum(a, L, 128, st);
