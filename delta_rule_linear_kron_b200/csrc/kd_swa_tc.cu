@@ -1,8 +1,9 @@
 // kd_swa_tc.cu -- sliding-window attention with first tokens kept, on tcgen05
 // (bf16, d = 64 and 128).  The formulas are in kd_swa.cu.
 //
-// Every kernel has eleven warps: two groups of four (thread = TMEM lane = tile
-// row) for the elementwise work, one thread that loads tiles by TMA into a
+// Every kernel has 19 warps: four groups of four (thread = TMEM lane = tile row,
+// a part of its columns) for the elementwise work, which bounds these kernels
+// (half as many warps with twice the columns: DKV2, DQ2, FWD2), one thread that loads tiles by TMA into a
 // ring, and two that issue MMAs, each the products of one chain (scores, then
 // what is made of them), so that one chain's waits (250 cycles each, even for
 // a phase that is complete) lie beside the other's products.  Tiles are 128 x
@@ -43,8 +44,8 @@ namespace kd {
 
 namespace {
 
-constexpr int kTcThreads = 352;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;  // and 10
+constexpr int kTcThreads = 608;
+constexpr int kLoadWarp = 16, kMmaWarp = 17;  // and 18; 0-15 are the groups'
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -87,18 +88,18 @@ struct KeyRange {
   __device__ bool has(int kt) const { return kt < first || (kt >= band && kt <= end); }
 };
 
-// Row of D fp32 values of this thread's TMEM lane, scaled, to global bf16; the
+// N fp32 values of this thread's TMEM lane, scaled, to global bf16; the
 // rounding that is left over goes to `lo` where it is given.
-template <int D>
+template <int N>
 __device__ __forceinline__ void store_lane(uint32_t lanes, float scale, __nv_bfloat16* dst, __nv_bfloat16* lo) {
 #pragma unroll
-  for (int c = 0; c < D; c += 32) {
-    float v[32];
+  for (int c = 0; c < N; c += 16) {
+    float v[16];
     __syncwarp();  // rows without a destination skip the stores, not the warp's loads
-    tc::tmem_ld32(lanes + c, v);
+    tc::tmem_ld16(lanes + c, v);
     tc::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 32 && dst; i += 8) {
+    for (int i = 0; i < 16 && dst; i += 8) {
       float w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = v[i + e] * scale;
@@ -130,15 +131,14 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
   }
 }
 
-// D (+)= W X of 128 x d, K = 128: W in TMEM, the columns of group 0's half at
-// `w` and of group 1's at w + 64 (32 columns each), X a tile of 128 rows read
-// MN-major.
+// D (+)= W X of 128 x d, K = 128: W in TMEM, group g's 32 weights in 16 columns
+// at w + 32 g, X a tile of 128 rows read MN-major.
 template <int D>
 __device__ __forceinline__ void mma_mix(uint32_t d, uint32_t w, uint32_t x, bool acc) {
   constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
 #pragma unroll
   for (int s = 0; s < 8; ++s)
-    tc::mma_bf16_ts(d, w + s / 4 * 64 + s % 4 * 8, tc::desc_sw128_mn(x + s * 2048, 16384u), id, acc || s > 0);
+    tc::mma_bf16_ts(d, w + s / 2 * 32 + s % 2 * 8, tc::desc_sw128_mn(x + s * 2048, 16384u), id, acc || s > 0);
 }
 
 // ---- forward -----------------------------------------------------------------
@@ -149,9 +149,27 @@ struct FwdCfg {
   static constexpr int SLOTS = D == 128 ? 3 : 6;  // ring of key and value tiles
   static constexpr uint32_t P = 2 * TILE;         // behind the two query tiles: weights, 32 KB per group
   static constexpr uint32_t RING = P + 65536;
-  static constexpr uint32_t BYTES = RING + SLOTS * TILE + 1024;
-  static constexpr int S_COL = 0, O_COL = 256;    // 128 columns per group: scores; the output
+  static constexpr uint32_t HALF = RING + SLOTS * TILE;  // bf16 [tile parity][query tile][half][row]
+  static constexpr uint32_t BARS = HALF + 2048;
+  static constexpr uint32_t BYTES = BARS + 256;   // no static shared memory: all 227 KB at d = 128
+  static constexpr int S_COL = 0, O_COL = 256;    // 128 columns per query tile: scores; the output
 };
+
+struct FwdBars {
+  uint64_t q_full, full[6], empty[6], s_full[2], s_free[2], p_full[2], o_full[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(FwdBars) <= 256, "barriers fit behind the tiles");
+
+// The kernels' tiles need the dynamic shared memory to start on 1024 bytes,
+// which it does where there is no static one; checked, since the swizzle
+// depends on it.
+__device__ __forceinline__ bool tiles_aligned(const unsigned char* sm, int* err) {
+  if (!(tc::smem_u32(sm) & 1023u)) return true;
+  if (threadIdx.x == 0) atomicOr(err, tc::kErrTimeoutLoad);
+  return false;
+}
 
 // Order of the ring's loads: k0 k1 v0 k2 v1 k3 .. (count tiles of each).
 __device__ __forceinline__ int load_of_k(int n) { return n < 2 ? n : 2 * n - 1; }
@@ -162,11 +180,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
     const __grid_constant__ CUtensorMap tv, SwaArgs a) {
   using Cf = FwdCfg<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t q_full, full[Cf::SLOTS], empty[Cf::SLOTS], s_full[2], s_free[2], p_full[2], o_full[2];
-  __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  FwdBars& s = *reinterpret_cast<FwdBars*>(sm + Cf::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // heavy CTAs (late rows: full windows) first
   const int q0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * 256, h = blockIdx.y, b = blockIdx.z;
@@ -174,41 +189,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
   const auto upto = [&](int x) { return x < a.T ? x : a.T; };
   const KeyRange all(q0, upto(q0 + 256), W, S, 128);
 
+  if (!tiles_aligned(sm, a.err)) return;
   if (tid == 0) {
-    tc::mbar_init(&q_full, 1);
+    tc::mbar_init(&s.q_full, 1);
     for (int i = 0; i < Cf::SLOTS; ++i) {
-      tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], 2);
+      tc::mbar_init(&s.full[i], 1);
+      tc::mbar_init(&s.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&s_free[i], 128);
-      tc::mbar_init(&p_full[i], 128);
-      tc::mbar_init(&o_full[i], 1);
+      tc::mbar_init(&s.s_full[i], 1);
+      tc::mbar_init(&s.s_free[i], 256);
+      tc::mbar_init(&s.p_full[i], 256);
+      tc::mbar_init(&s.o_full[i], 1);
     }
     tc::mbar_init_fence();
-    abort_flag = 0;
+    s.abort_flag = 0;
   }
-  if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
+  if (warp == 0) tc::tmem_alloc(&s.tmem, 512);
   tc::tc_before_sync();
   __syncthreads();
   tc::tc_after_sync();
-  const uint32_t tmem = tmem_slot;
-  volatile int* ab = &abort_flag;
+  const uint32_t tmem = s.tmem;
+  volatile int* ab = &s.abort_flag;
   const int loads = 2 * all.count;
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
       const bool two = q0 + 128 < a.T;
-      tc::mbar_expect_tx(&q_full, (two ? 2 : 1) * Cf::TILE);
-      for (int i = 0; i < (two ? 2 : 1); ++i) load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &q_full);
+      tc::mbar_expect_tx(&s.q_full, (two ? 2 : 1) * Cf::TILE);
+      for (int i = 0; i < (two ? 2 : 1); ++i) load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &s.q_full);
       int kn = 0, vn = 0;
       for (int n = 0; n < loads; ++n) {
         const bool is_k = kn < all.count && load_of_k(kn) == n;
         const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS, tile = is_k ? kn++ : vn++;
-        if (use && !tc::mbar_wait<false>(&empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-        tc::mbar_expect_tx(&full[slot], Cf::TILE);
-        load_tile<D>(sm + Cf::RING + slot * Cf::TILE, is_k ? &tk : &tv, hk, all.tile(tile) * 128, b, &full[slot]);
+        if (use && !tc::mbar_wait<false>(&s.empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+        tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
+        load_tile<D>(sm + Cf::RING + slot * Cf::TILE, is_k ? &tk : &tv, hk, all.tile(tile) * 128, b, &s.full[slot]);
       }
     }
   } else if (warp >= kMmaWarp) {
@@ -220,15 +236,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       const uint32_t sc = tmem + Cf::S_COL + i * 128, o = tmem + Cf::O_COL + i * 128;
       int s_done = 0, p_done = 0;  // tiles whose scores, whose products are issued
       const auto landed = [&](int load) {
-        tc::mbar_wait<false>(&full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab);
+        tc::mbar_wait<false>(&s.full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab);
         return base + Cf::RING + load % Cf::SLOTS * Cf::TILE;
       };
       const auto release = [&](int load, bool used) {  // only where the slot is loaded again: every commit is waited for
         if (load + Cf::SLOTS >= loads) return;
         if (used)
-          tc::mma_commit(&empty[load % Cf::SLOTS]);
+          tc::mma_commit(&s.empty[load % Cf::SLOTS]);
         else
-          tc::mbar_arrive(&empty[load % Cf::SLOTS]);
+          tc::mbar_arrive(&s.empty[load % Cf::SLOTS]);
       };
       // S = q k^T of tile n, when the group has read the scores before
       const auto scores = [&](int n) {
@@ -238,10 +254,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
         const uint32_t k = landed(load_of_k(n));
         if (has) {
           const int m = s_done++;
-          if (m > 0) tc::mbar_wait<false>(&s_free[i], (m - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
+          if (m > 0) tc::mbar_wait<false>(&s.s_free[i], (m - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
           tc::tc_after_sync();
           mma_scores<D>(sc, q, k);
-          tc::mma_commit(&s_full[i]);
+          tc::mma_commit(&s.s_full[i]);
         }
         release(load_of_k(n), has);
       };
@@ -253,22 +269,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
         if (has) {
           constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
           const int m = p_done++;
-          tc::mbar_wait<false>(&p_full[i], m & 1, a.err, tc::kErrTimeoutMma, ab);
+          tc::mbar_wait<false>(&s.p_full[i], m & 1, a.err, tc::kErrTimeoutMma, ab);
           tc::tc_after_sync();
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            tc::mma_bf16_ss(o, tc::desc_sw128(p + s / 4 * 16384 + s % 4 * 32), tc::desc_sw128_mn(v + s * 2048, 16384u),
-                            id, m > 0 || s > 0);
+          for (int c = 0; c < 8; ++c)
+            tc::mma_bf16_ss(o, tc::desc_sw128(p + c / 4 * 16384 + c % 4 * 32), tc::desc_sw128_mn(v + c * 2048, 16384u),
+                            id, m > 0 || c > 0);
           if (kFine) {  // the low parts, over the scores
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              tc::mma_bf16_ts(o, sc + s * 8, tc::desc_sw128_mn(v + s * 2048, 16384u), id, 1);
+            for (int c = 0; c < 8; ++c)
+              tc::mma_bf16_ts(o, sc + c / 4 * 64 + c % 4 * 8, tc::desc_sw128_mn(v + c * 2048, 16384u), id, 1);
           }
-          tc::mma_commit(&o_full[i]);
+          tc::mma_commit(&s.o_full[i]);
         }
         release(load, has);
       };
-      if (mine.count) tc::mbar_wait<false>(&q_full, 0, a.err, tc::kErrTimeoutLoad, ab);
+      if (mine.count) tc::mbar_wait<false>(&s.q_full, 0, a.err, tc::kErrTimeoutLoad, ab);
       scores(0);
       for (int n = 0; n < all.count && !*ab; ++n) {
         const bool more = n + 1 < all.count;
@@ -278,49 +294,60 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       }
     }
   } else {
-    const int i = warp >> 2, r0 = upto(q0 + 128 * i), t = q0 + tid, r = tid & 127;
+    // query tile i, columns 64 g .. 64 g + 63 of row r
+    const int i = warp >> 3, g = (warp >> 2) & 1, r = tid & 127, r0 = upto(q0 + 128 * i), t = q0 + 128 * i + r;
     const KeyRange mine(r0, upto(q0 + 128 * i + 128), W, S, 128);
-    const uint32_t s_lane = tc::tmem_lane_addr(tmem, warp, Cf::S_COL + i * 128);
-    const uint32_t o_lane = tc::tmem_lane_addr(tmem, warp, Cf::O_COL + i * 128);
+    const uint32_t s_lane = tc::tmem_lane_addr(tmem, warp, Cf::S_COL + i * 128 + g * 64);
+    const uint32_t o_lane = tc::tmem_lane_addr(tmem, warp, Cf::O_COL + i * 128 + g * (D / 2));
     // this row of the group's weights: 16-byte chunk c of a block at (c ^ (row & 7)) * 16
-    unsigned char* prow = sm + Cf::P + i * 32768 + r * 128;
+    unsigned char* prow = sm + Cf::P + i * 32768 + g * 16384 + r * 128;
     const float s2 = a.scale * kLog2e;
+    // the two warps that share 32 rows meet to exchange a value per row: the
+    // maximum of their columns, rounded up to bf16 (any bound near the maximum
+    // will do as the reference, as long as both take the same), at the end the
+    // sum, over the weights that nothing reads any more
+    const auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory"); };
+    __nv_bfloat16* half = reinterpret_cast<__nv_bfloat16*>(sm + Cf::HALF) + i * 256 + r;
+    float* sums = reinterpret_cast<float*>(sm + Cf::P + i * 32768) + r;
     float top = -INFINITY, sum = 0.f;  // sums refer to 2^(s2 top)
     for (int n = 0; n < mine.count; ++n) {
       const int k0 = mine.tile(n) * 128;
-      if (!warp_wait(&s_full[i], n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+      if (!warp_wait(&s.s_full[i], n & 1, a.err, tc::kErrTimeoutMma, ab)) *ab = 1;  // both warps of the rows go on
       tc::tc_after_sync();
-      float x[128];
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) tc::tmem_ld32(s_lane + c, x + c);
+      float x[64];
+      tc::tmem_ld32(s_lane, x);
+      tc::tmem_ld32(s_lane + 32, x + 32);
       tc::tmem_ld_wait();
       if (!kFine) {
         tc::tc_before_sync();
-        tc::mbar_arrive(&s_free[i]);
+        tc::mbar_arrive(&s.s_free[i]);
       }
       if (!(k0 + 127 <= r0 && (r0 + 127 - k0 < W || k0 + 127 < S))) {
-        const int hi = t - k0, lo = hi - W, sk = S - k0;
+        const int hi = t - k0 - g * 64, lo = hi - W, sk = S - k0 - g * 64;
 #pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = c <= hi && (c > lo || c < sk) ? x[c] : -INFINITY;
+        for (int c = 0; c < 64; ++c) x[c] = c <= hi && (c > lo || c < sk) ? x[c] : -INFINITY;
       }
       float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
 #pragma unroll
-      for (int c = 4; c < 128; c += 4) {
+      for (int c = 4; c < 64; c += 4) {
         m0 = fmaxf(m0, x[c]);
         m1 = fmaxf(m1, x[c + 1]);
         m2 = fmaxf(m2, x[c + 2]);
         m3 = fmaxf(m3, x[c + 3]);
       }
-      const float m = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      const __nv_bfloat16 up = __float2bfloat16_ru(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+      half[(n & 1) * 512 + g * 128] = up;
+      meet();
+      const float m = __bfloat162float(__hmax(up, half[(n & 1) * 512 + (g ^ 1) * 128]));
       const bool grow = n == 0 ? m > top : (m - top) * s2 > 8.f;  // false while a row has seen no key
       if (n > 0) {  // the product before has read the weights, and the output is complete
-        warp_wait(&o_full[i], (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
-        if (__any_sync(0xffffffffu, grow)) {
+        warp_wait(&s.o_full[i], (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
+        if (__any_sync(0xffffffffu, grow)) {  // each warp its half of the channels
           tc::tc_after_sync();
           const float f = grow ? ex2((top - m) * s2) : 1.f;
           sum *= f;
 #pragma unroll
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < D / 2; c += 16) {
             float o[16];
             tc::tmem_ld16(o_lane + c, o);
             tc::tmem_ld_wait();
@@ -335,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       const float ref = top == -INFINITY ? 0.f : top * s2;
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-      for (int c = 0; c < 128; c += 8) {
+      for (int c = 0; c < 64; c += 8) {
         uint4 w;
         uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
@@ -346,7 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
           a0 += x[c + e];
           a1 += x[c + e + 1];
         }
-        *reinterpret_cast<uint4*>(prow + c / 64 * 16384 + ((c / 8 % 8) ^ (r & 7)) * 16) = w;
+        *reinterpret_cast<uint4*>(prow + ((c / 8) ^ (r & 7)) * 16) = w;
         if (kFine) {  // what the rounding left
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
@@ -358,7 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       sum += a0 + a1;
       if (kFine) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           float w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
@@ -368,17 +395,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       }
       tc::fence_proxy_async();
       tc::tc_before_sync();
-      tc::mbar_arrive(&p_full[i]);
-      if (kFine) tc::mbar_arrive(&s_free[i]);  // the next scores follow this tile's product
+      tc::mbar_arrive(&s.p_full[i]);
+      if (kFine) tc::mbar_arrive(&s.s_free[i]);  // the next scores follow this tile's product
     }
     if (mine.count) {
-      warp_wait(&o_full[i], (mine.count - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
+      warp_wait(&s.o_full[i], (mine.count - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
       tc::tc_after_sync();
+      sums[g * 128] = sum;
+      meet();
+      sum += sums[(g ^ 1) * 128];
       const bool live = t < a.T;
-      const size_t row = ((size_t)b * a.T + t) * a.H + h;
-      store_lane<D>(o_lane, 1.f / sum, live ? static_cast<__nv_bfloat16*>(a.out) + row * D : nullptr,
-                    live && a.olo ? static_cast<__nv_bfloat16*>(a.olo) + row * D : nullptr);
-      if (live) a.lse[row] = fmaf(top, s2, log2f(sum)) * kLn2;
+      const size_t row = ((size_t)b * a.T + t) * a.H + h, at = row * D + g * (D / 2);
+      store_lane<D / 2>(o_lane, 1.f / sum, live ? static_cast<__nv_bfloat16*>(a.out) + at : nullptr,
+                        live && a.olo ? static_cast<__nv_bfloat16*>(a.olo) + at : nullptr);
+      if (live && g == 0) a.lse[row] = fmaf(top, s2, log2f(sum)) * kLn2;
     }
   }
   tc::tc_before_sync();
@@ -409,15 +439,9 @@ struct BwdBars {
 };
 static_assert(sizeof(BwdBars) <= 256, "barriers fit behind the tiles");
 
-// The kernels' tiles need the dynamic shared memory to start on 1024 bytes,
-// which it does where there is no static one; checked, since the swizzle
-// depends on it.
 // `chains`: MMA chains that a slot's tile and an accumulator's end wait for.
 __device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int chains, int* err) {
-  if (tc::smem_u32(sm) & 1023u) {
-    if (threadIdx.x == 0) atomicOr(err, tc::kErrTimeoutLoad);
-    return false;
-  }
+  if (!tiles_aligned(sm, err)) return false;
   if (threadIdx.x == 0) {
     tc::mbar_init(&s.own, 1);
     for (int i = 0; i < 5; ++i) {
@@ -426,12 +450,12 @@ __device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int cha
     }
     tc::mbar_init(&s.s_full[0], 1);
     tc::mbar_init(&s.s_full[1], 1);
-    tc::mbar_init(&s.s_free, 256);
+    tc::mbar_init(&s.s_free, 512);
     tc::mbar_init(&s.dp_full, 1);
-    tc::mbar_init(&s.p_ready, 256);
+    tc::mbar_init(&s.p_ready, 512);
     tc::mbar_init(&s.p_read, 1);
-    tc::mbar_init(&s.ds_ready[0], 256);
-    tc::mbar_init(&s.ds_ready[1], 256);
+    tc::mbar_init(&s.ds_ready[0], 512);
+    tc::mbar_init(&s.ds_ready[1], 512);
     tc::mbar_init(&s.done, chains);
     tc::mbar_init_fence();
     s.abort_flag = 0;
@@ -472,15 +496,12 @@ struct BwdRing {
   }
 };
 
-// 64 weights of this thread's row, rounded, as the A operand at `dst`.
-__device__ __forceinline__ void store_weights(uint32_t dst, const float (&x)[64]) {
+// 32 weights of this thread's row, rounded, as the A operand at `dst`.
+__device__ __forceinline__ void store_weights(uint32_t dst, const float (&x)[32]) {
+  float w[16];
 #pragma unroll
-  for (int c = 0; c < 64; c += 32) {
-    float w[16];
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
-    tc::tmem_st16(dst + c / 2, w);
-  }
+  for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[e], x[e + 1]);
+  tc::tmem_st16(dst, w);
   tc::tmem_st_wait();
   tc::tc_before_sync();
 }
@@ -543,8 +564,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
       }
     }
   } else {
-    const int g = warp >> 2, t = q0 + (tid & 127);
-    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, g * 64);
+    const int g = warp >> 2, t = q0 + (tid & 127);  // columns 32 g .. 32 g + 31
+    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, g * 32);
     const size_t at = ((size_t)b * a.H + h) * L.Tp + t;
     const float lse2 = reinterpret_cast<const float*>(a.ws + L.lse2)[at];
     const float delta = reinterpret_cast<const float*>(a.ws + L.delta)[at];
@@ -554,37 +575,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
       const uint32_t buf = lanes + n % 2 * 128;
       if (!warp_wait(&s.s_full[n % 2], (n >> 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
-      float x[64];
+      float x[32], dp[32];
       tc::tmem_ld32(buf, x);
-      tc::tmem_ld32(buf + 32, x + 32);
       tc::tmem_ld_wait();
       if (!(k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S))) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          x[e] = visible(t, k0 + g * 64 + e, W, S) && !single_key(t, W, S) ? x[e] : -INFINITY;
+        for (int e = 0; e < 32; ++e)
+          x[e] = visible(t, k0 + g * 32 + e, W, S) && !single_key(t, W, S) ? x[e] : -INFINITY;
       }
 #pragma unroll
-      for (int e = 0; e < 64; ++e) x[e] = ex2(fmaf(x[e], s2, -lse2));
+      for (int e = 0; e < 32; ++e) x[e] = ex2(fmaf(x[e], s2, -lse2));
       if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
+      tc::tmem_ld32(lanes + DP, dp);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        float dp[32];
-        tc::tmem_ld32(lanes + DP + c, dp);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[c + e] *= dp[e] - delta;
-      }
+      for (int e = 0; e < 32; ++e) x[e] *= dp[e] - delta;
       store_weights(buf, x);
       tc::mbar_arrive(&s.ds_ready[n % 2]);
     }
     warp_wait(&s.done, 0, a.err, tc::kErrTimeoutMma, ab);
     tc::tc_after_sync();
-    if (g == 0) {
-      const size_t row = ((size_t)b * a.T + t) * a.H + h;
-      store_lane<D>(tc::tmem_lane_addr(tmem, warp, DQ), a.scale,
-                    t < a.T ? static_cast<__nv_bfloat16*>(a.dq) + row * D : nullptr, nullptr);
-    }
+    const size_t row = (((size_t)b * a.T + t) * a.H + h) * D + g * (D / 4);
+    store_lane<D / 4>(tc::tmem_lane_addr(tmem, warp, DQ + g * (D / 4)), a.scale,
+                      t < a.T ? static_cast<__nv_bfloat16*>(a.dq) + row : nullptr, nullptr);
   }
   bwd_finish(tmem);
 }
@@ -688,36 +702,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       tc::mma_commit(&s.done);
     }
   } else {
-    const int g = warp >> 2, key = k0 + (tid & 127);
-    const uint32_t buf = tc::tmem_lane_addr(tmem, warp, g * 64);
+    const int g = warp >> 2, key = k0 + (tid & 127);  // columns 32 g .. 32 g + 31
+    const uint32_t buf = tc::tmem_lane_addr(tmem, warp, g * 32);
     const float s2 = a.scale * kLog2e;
-    // this key's row of the weights, the group's 64 columns: 16-byte chunk c at
-    // (c ^ (row & 7)) * 16
-    unsigned char* prow = sm + Cf::P + g * 16384 + (tid & 127) * 128;
+    // this key's row of the weights, the group's 32 columns: 16-byte chunk c of a
+    // block of 64 at (c ^ (row & 7)) * 16
+    unsigned char* prow = sm + Cf::P + g / 2 * 16384 + (tid & 127) * 128;
     for (int n = 0; n < count; ++n) {
       const int q0 = (qt0 + n % per) * 128, slot = 2 * n % Cf::SLOTS;
-      const float4* rows = reinterpret_cast<const float4*>(sm + Cf::ROWS + n % 2 * 1024) + g * 16;
+      const float4* rows = reinterpret_cast<const float4*>(sm + Cf::ROWS + n % 2 * 1024) + g * 8;
       // the scores' commit follows the arrival of q and its rows, but only this
       // wait lets this thread read what the copy wrote
       if (!warp_wait(&s.full[slot], (2 * n / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
       if (!warp_wait(&s.s_full[0], n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
-      float x[64];
+      float x[32], dp[32];
       tc::tmem_ld32(buf, x);
-      tc::tmem_ld32(buf + 32, x + 32);
       tc::tmem_ld_wait();
       tc::tc_before_sync();
       tc::mbar_arrive(&s.s_free);
       const bool every = k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S) && q0 >= q_lo && q0 + 127 < q_hi;
       if (!every) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const int t = q0 + g * 64 + e;
+        for (int e = 0; e < 32; ++e) {
+          const int t = q0 + g * 32 + e;
           x[e] = t >= q_lo && t < q_hi && visible(t, key, W, S) ? x[e] : -INFINITY;
         }
       }
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) {
+      for (int e = 0; e < 32; e += 4) {
         const float4 l = rows[e / 4];
         x[e] = ex2(fmaf(x[e], s2, -l.x));
         x[e + 1] = ex2(fmaf(x[e + 1], s2, -l.y));
@@ -726,57 +739,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       }
       if (n > 0 && !warp_wait(&s.p_read, (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint4 w;
         uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) wp[e] = __float_as_uint(bf16_pair(x[c * 8 + 2 * e], x[c * 8 + 2 * e + 1]));
-        *reinterpret_cast<uint4*>(prow + (c ^ (tid & 7)) * 16) = w;
+        *reinterpret_cast<uint4*>(prow + ((g % 2 * 4 + c) ^ (tid & 7)) * 16) = w;
       }
       tc::fence_proxy_async();
       tc::mbar_arrive(&s.p_ready);
       if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
+      tc::tmem_ld32(buf + DP, dp);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        float dp[32];
-        tc::tmem_ld32(buf + DP + c, dp);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d = rows[32 + (c + e) / 4];
-          x[c + e] *= dp[e] - d.x;
-          x[c + e + 1] *= dp[e + 1] - d.y;
-          x[c + e + 2] *= dp[e + 2] - d.z;
-          x[c + e + 3] *= dp[e + 3] - d.w;
-        }
+      for (int e = 0; e < 32; e += 4) {
+        const float4 d = rows[32 + e / 4];
+        x[e] *= dp[e] - d.x;
+        x[e + 1] *= dp[e + 1] - d.y;
+        x[e + 2] *= dp[e + 2] - d.z;
+        x[e + 3] *= dp[e + 3] - d.w;
       }
       if (!every) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (single_key(q0 + g * 64 + e, W, S)) x[e] = 0.f;
+        for (int e = 0; e < 32; ++e)
+          if (single_key(q0 + g * 32 + e, W, S)) x[e] = 0.f;
       }
       store_weights(buf + DP, x);
       tc::mbar_arrive(&s.ds_ready[0]);
     }
     warp_wait(&s.done, 0, a.err, tc::kErrTimeoutMma, ab);
     tc::tc_after_sync();
-    // group 0 writes dv, group 1 dk
-    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, g ? DK : DV);
-    const float f = g ? a.scale : 1.f;
+    // groups 0 and 1 write the halves of dv, 2 and 3 of dk
+    const bool is_k = g >= 2;
+    const int c0 = g % 2 * (D / 2);
+    const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, (is_k ? DK : DV) + c0);
+    const float f = is_k ? a.scale : 1.f;
     const bool first = key < S && key < a.T && has_far;  // rows that other items add to: fp32 parts
     float* part = nullptr;
     if (first && far)
       part = reinterpret_cast<float*>(a.ws + L.part) +
-             (((((size_t)(g ? 0 : 1) * L.pieces + piece) * a.B + b) * a.H + h0) * S + key) * D;
+             (((((size_t)(is_k ? 0 : 1) * L.pieces + piece) * a.B + b) * a.H + h0) * S + key) * D + c0;
     else if (first)
-      part = reinterpret_cast<float*>(a.ws + L.band) + ((((size_t)(g ? 0 : 1) * a.B + b) * a.Hk + hk) * S + key) * D;
+      part = reinterpret_cast<float*>(a.ws + L.band) +
+             ((((size_t)(is_k ? 0 : 1) * a.B + b) * a.Hk + hk) * S + key) * D + c0;
     const bool plain = !far && !first && key < a.T;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(g ? a.dk : a.dv) + (((size_t)b * a.T + key) * a.Hk + hk) * D;
-    store_lane<D>(lanes, f, plain ? dst : nullptr, nullptr);
+    __nv_bfloat16* dst =
+        static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + (((size_t)b * a.T + key) * a.Hk + hk) * D + c0;
+    store_lane<D / 2>(lanes, f, plain ? dst : nullptr, nullptr);
     if (k0 < S && has_far) {
 #pragma unroll
-      for (int c = 0; c < D; c += 16) {
+      for (int c = 0; c < D / 2; c += 16) {
         float v[16];
         __syncwarp();
         tc::tmem_ld16(lanes + c, v);
