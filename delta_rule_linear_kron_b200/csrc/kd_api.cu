@@ -1054,7 +1054,7 @@ size_t kron_delta_swa_workspace_size(int kind, int B, int T, int H, int Hk, int 
     case KD_SWA_WS_BWD: ok(); return kd::swa_bwd_layout(B, T, H, Hk, d, clamp_to(window, T), clamp_to(sinks, T)).bytes;
     case KD_SWA_WS_DECODE:
       ok();
-      return kd::swa_decode_bytes(B, H, d, kd::swa_decode_splits(B, H, Hk, d, window, sinks, dtype));
+      return kd::swa_decode_bytes(B, H, d, kd::swa_decode_splits(B, H, Hk, window, sinks, dtype));
     default: fail(KD_ERR_INVALID_ARG, "unknown workspace kind %d", kind); return 0;
   }
 }
@@ -1130,11 +1130,12 @@ int kron_delta_swa_decode(const void* q, const void* k, const void* v, void* k_c
   KD_TRY(check_ptr(v_cache, "v_cache", true));
   KD_TRY(check_ptr8(pos, "pos", true));
   KD_TRY(check_ptr(out, "out", true));
-  const int splits = kd::swa_decode_splits(B, H, Hk, d, window, sinks, dtype);
-  KD_TRY(check_ws(workspace, ws_bytes, kd::swa_decode_bytes(B, H, d, splits), "decode workspace"));
+  const int splits = kd::swa_decode_splits(B, H, Hk, window, sinks, dtype);
+  const size_t need = kd::swa_decode_bytes(B, H, d, splits);
+  KD_TRY(check_ws(workspace, ws_bytes, need, "decode workspace"));
   KD_TRY(check_stream(stream));
   kd::SwaDecodeArgs a{q, k, v, k_cache, v_cache, pos, out, B, H, Hk, d, window, sinks, dtype, scale,
-                      static_cast<float*>(workspace), splits};
+                      need ? static_cast<float*>(workspace) : nullptr, splits};
   return launched(kd::launch_swa_decode(a, static_cast<cudaStream_t>(stream)), "swa decode launch");
 }
 

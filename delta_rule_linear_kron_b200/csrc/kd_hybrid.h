@@ -69,11 +69,11 @@ struct SwaDecodeArgs {
   void* out;
   int B, H, Hk, d, window, sinks, dtype;
   float scale;
-  float* part;  // partial results of the splits
+  float* part;  // partial results of more splits than a cluster joins, or null
   int splits;
 };
 // number of parts that a sequence's cache is read in, and the scratch they need
-int swa_decode_splits(int B, int H, int Hk, int d, int window, int sinks, int dtype);
+int swa_decode_splits(int B, int H, int Hk, int window, int sinks, int dtype);
 size_t swa_decode_bytes(int B, int H, int d, int splits);
 cudaError_t launch_swa_decode(const SwaDecodeArgs& a, cudaStream_t st);
 

@@ -7,7 +7,10 @@
 // in an order that a softmax does not depend on.
 //
 // HBM-bound: every key and value in use is read once, for all query heads of
-// its group.  The parts of a long cache are joined by a second kernel.
+// its group.  Where there are few sequences, a cache is read in parts by
+// several CTAs.  Up to 8 parts are a cluster, whose CTAs join them through
+// distributed shared memory; more (a long window) are joined by a second
+// kernel from the workspace.
 //
 // bf16: m16n8k16 products, the (up to 16) query heads of a key head as the 16
 // rows.  tcgen05 would want 128 rows, of which a group fills 1 to 16, and the
@@ -24,12 +27,15 @@
 // over the row's lanes, the values weighted in the same layout.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
+#include "kd_tc.cuh"
 
 namespace kd {
 
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kDecodeCluster = 8;
+constexpr int kDecodeClusterSlots = 8192;
 constexpr int kBatch = 8;  // rows of keys (then of values) in flight per lane
 constexpr float kLog2e = 1.44269504088896f;
 
@@ -40,6 +46,89 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ long long slot_of(long long p, int W, int S) { return p < S ? p : S + (p - S) % W; }
+
+__device__ __forceinline__ float2 peer_f2(const float* p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(tc::mapa(tc::smem_u32(p), rank))
+               : "memory");
+  return v;
+}
+
+// A CTA's results for `heads` query heads from h0 on: sh_m, sh_l [warp][R] and
+// sh_o [warp][R][D] of its warps become its part, and the parts the output.
+template <typename T, int D, int R>
+__device__ __forceinline__ void finish(const SwaDecodeArgs& a, size_t b, int h0, int heads, int n, float* sh_m,
+                                       float* sh_l, float* sh_o) {
+  const int tid = threadIdx.x;
+  const bool cluster = a.splits > 1 && !a.part;
+  // two channels per thread: the CTA's own (maximum, sum, weighted values), in
+  // place of warp 0's
+  for (int i = tid; i < heads * (D / 2); i += kWarps * 32) {
+    const int r = i / (D / 2), c = i % (D / 2) * 2;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w * R + r]);
+    float sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sh_m[w * R + r] == -INFINITY ? 0.f : ex2(sh_m[w * R + r] - top);
+      const float2 v = *reinterpret_cast<const float2*>(sh_o + (w * R + r) * D + c);
+      sum = fmaf(f, sh_l[w * R + r], sum);
+      acc = make_float2(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y));
+    }
+    if (a.splits == 1) {
+      T* out = static_cast<T*>(a.out) + (b * a.H + h0 + r) * D + c;
+      out[0] = from_f<T>(n ? acc.x / sum : 0.f);
+      out[1] = from_f<T>(n ? acc.y / sum : 0.f);
+    } else if (!cluster) {
+      float* part = a.part + ((b * a.H + h0 + r) * a.splits + blockIdx.x) * (size_t)(D + 2);
+      *reinterpret_cast<float2*>(part + 2 + c) = acc;
+      if (c == 0) *reinterpret_cast<float2*>(part) = make_float2(top, sum);
+    } else {
+      *reinterpret_cast<float2*>(sh_o + r * D + c) = acc;  // only this thread reads these two of warp 0
+    }
+  }
+  if (!cluster) return;
+  __syncthreads();  // every thread has read the warps' maxima and sums
+  for (int r = tid; r < heads; r += kWarps * 32) {
+    float top = -INFINITY, sum = 0.f;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w * R + r]);
+    for (int w = 0; w < kWarps; ++w)
+      sum += sh_m[w * R + r] == -INFINITY ? 0.f : ex2(sh_m[w * R + r] - top) * sh_l[w * R + r];
+    *reinterpret_cast<float2*>(sh_o + R * D + r * 2) = make_float2(top, sum);  // over warp 1's values
+  }
+  tc::cluster_sync();
+  // each CTA a share of the channels of every head
+  for (int i = blockIdx.x * kWarps * 32 + tid; i < heads * (D / 2); i += a.splits * kWarps * 32) {
+    const int r = i / (D / 2), c = i % (D / 2) * 2;
+    float2 ms[8], v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < a.splits) {
+        ms[s] = peer_f2(sh_o + R * D + r * 2, s);
+        v[s] = peer_f2(sh_o + r * D + c, s);
+      }
+    float top = -INFINITY, sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < a.splits) top = fmaxf(top, ms[s].x);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < a.splits) {
+        const float f = ms[s].x == -INFINITY ? 0.f : ex2(ms[s].x - top);  // 0 for an empty part
+        sum = fmaf(f, ms[s].y, sum);
+        acc = make_float2(fmaf(f, v[s].x, acc.x), fmaf(f, v[s].y, acc.y));
+      }
+    T* out = static_cast<T*>(a.out) + (b * a.H + h0 + r) * D + c;
+    out[0] = from_f<T>(n ? acc.x / sum : 0.f);
+    out[1] = from_f<T>(n ? acc.y / sum : 0.f);
+  }
+  tc::cluster_sync();  // no CTA leaves while another still reads its part
+}
 
 template <typename T, int D>
 struct Row {
@@ -153,30 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
       for (int e = 0; e < E; ++e) sh_o[warp][g][c + e] = o[g][e];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < GC * D; i += kWarps * 32) {
-    const int g = i / D, ch = i % D, h = hk * group + g0 + g;
-    if (g0 + g >= group) continue;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][g]);
-    float sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = sh_m[w][g] == -INFINITY ? 0.f : ex2(sh_m[w][g] - top);
-      sum = fmaf(f, sh_l[w][g], sum);
-      acc = fmaf(f, sh_o[w][g][ch], acc);
-    }
-    if (a.splits == 1) {
-      static_cast<T*>(a.out)[(b * a.H + h) * D + ch] = from_f<T>(n ? acc / sum : 0.f);
-    } else {
-      float* part = a.part + ((b * a.H + h) * a.splits + blockIdx.x) * (size_t)(D + 2);
-      part[2 + ch] = acc;
-      if (ch == 0) {
-        part[0] = top;
-        part[1] = sum;
-      }
-    }
-  }
+  finish<T, D, GC>(a, b, hk * group + g0, min(GC, group - g0), n, &sh_m[0][0], &sh_l[0][0], &sh_o[0][0][0]);
 }
 
 // ---- bf16 -------------------------------------------------------------------
@@ -377,29 +443,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecod
       *reinterpret_cast<float2*>(so + (warp * 16 + g + 8) * D + i * 8 + tq * 2) = make_float2(o[i][2], o[i][3]);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < heads * D; i += kWarps * 32) {
-    const int r = i / D, ch = i % D, h = hk * group + g0 + r;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][r]);
-    float sum = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = sh_m[w][r] == -INFINITY ? 0.f : ex2(sh_m[w][r] - top);
-      sum = fmaf(f, sh_l[w][r], sum);
-      acc = fmaf(f, so[(w * 16 + r) * D + ch], acc);
-    }
-    if (a.splits == 1) {
-      static_cast<T*>(a.out)[(b * a.H + h) * D + ch] = from_f<T>(n ? acc / sum : 0.f);
-    } else {
-      float* part = a.part + ((b * a.H + h) * a.splits + blockIdx.x) * (size_t)(D + 2);
-      part[2 + ch] = acc;
-      if (ch == 0) {
-        part[0] = top;
-        part[1] = sum;
-      }
-    }
-  }
+  finish<T, D, 16>(a, b, hk * group + g0, heads, n, &sh_m[0][0], &sh_l[0][0], so);
 }
 
 // Joins the parts of one head: weights of the parts first, then the channels.
@@ -423,31 +467,40 @@ __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restr
 // query heads of a key head that one CTA takes
 int heads_per_cta(int group, int dtype) { return dtype == 1 ? 16 : group >= 3 ? 4 : group; }
 
-template <typename T, int D>
-cudaError_t join(const SwaDecodeArgs& a, cudaStream_t st) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.splits == 1) return e;
+// One CTA per part, key head (or 16, 4 of its query heads) and sequence; the
+// parts of up to kDecodeCluster are a cluster.
+template <typename T, int D, typename K>
+cudaError_t decode_go(const SwaDecodeArgs& a, K kernel, size_t smem, cudaStream_t st) {
+  const int gc = heads_per_cta(a.H / a.Hk, a.dtype);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.splits, a.Hk * ((a.H / a.Hk + gc - 1) / gc), a.B);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = a.part ? 1 : a.splits;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = a.splits > 1 && !a.part ? 1 : 0;
+  prof_begin(st, "swa_decode");
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  prof_end(st);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || !a.part) return e;
   prof_begin(st, "swa_decode_join");
   swa_decode_join_kernel<T, D><<<a.B * a.H, D, 0, st>>>(a.part, a.splits, static_cast<T*>(a.out));
   prof_end(st);
   return cudaGetLastError();
 }
 
-dim3 decode_grid(const SwaDecodeArgs& a) {
-  const int gc = heads_per_cta(a.H / a.Hk, a.dtype);
-  return dim3(a.splits, a.Hk * ((a.H / a.Hk + gc - 1) / gc), a.B);
-}
-
 template <int D>
 cudaError_t decode_f32(const SwaDecodeArgs& a, cudaStream_t st) {
-  prof_begin(st, "swa_decode");
   switch (heads_per_cta(a.H / a.Hk, 0)) {
-    case 1: swa_decode_kernel<float, D, 1><<<decode_grid(a), kWarps * 32, 0, st>>>(a); break;
-    case 2: swa_decode_kernel<float, D, 2><<<decode_grid(a), kWarps * 32, 0, st>>>(a); break;
-    default: swa_decode_kernel<float, D, 4><<<decode_grid(a), kWarps * 32, 0, st>>>(a);
+    case 1: return decode_go<float, D>(a, swa_decode_kernel<float, D, 1>, 0, st);
+    case 2: return decode_go<float, D>(a, swa_decode_kernel<float, D, 2>, 0, st);
+    default: return decode_go<float, D>(a, swa_decode_kernel<float, D, 4>, 0, st);
   }
-  prof_end(st);
-  return join<float, D>(a, st);
 }
 
 template <int D>
@@ -455,11 +508,7 @@ cudaError_t decode_bf16(const SwaDecodeArgs& a, cudaStream_t st) {
   using Cf = MmaCfg<D>;
   const cudaError_t e =
       cudaFuncSetAttribute(swa_decode_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::BYTES);
-  if (e != cudaSuccess) return e;
-  prof_begin(st, "swa_decode");
-  swa_decode_mma_kernel<D><<<decode_grid(a), kWarps * 32, Cf::BYTES, st>>>(a);
-  prof_end(st);
-  return join<__nv_bfloat16, D>(a, st);
+  return e != cudaSuccess ? e : decode_go<__nv_bfloat16, D>(a, swa_decode_mma_kernel<D>, Cf::BYTES, st);
 }
 
 // Per slot: the newest of the first n tokens that belongs there.
@@ -484,19 +533,20 @@ __global__ void __launch_bounds__(256) swa_fill_kernel(const uint4* __restrict__
 
 }  // namespace
 
-// Parts of a cache: enough CTAs for four on each of 148 SMs, but at least 64
-// slots to a part.
-int swa_decode_splits(int B, int H, int Hk, int d, int window, int sinks, int dtype) {
+// Parts of a cache: enough CTAs for two on each of 148 SMs, at least 64 slots
+// to a part.  A cluster's 8 parts are enough up to kDecodeClusterSlots; beyond,
+// as many as wanted, through the workspace.
+int swa_decode_splits(int B, int H, int Hk, int window, int sinks, int dtype) {
   const int gc = heads_per_cta(H / Hk, dtype);
-  const long long units = (long long)B * Hk * ((H / Hk + gc - 1) / gc);
-  const long long most = ((long long)window + sinks + 63) / 64;
-  long long s = (592 + units - 1) / units;
-  if (s > most) s = most;
+  const long long units = (long long)B * Hk * ((H / Hk + gc - 1) / gc), slots = (long long)window + sinks;
+  long long s = (296 + units - 1) / units;
+  if (s > (slots + 63) / 64) s = (slots + 63) / 64;
+  if (s > kDecodeCluster && slots <= kDecodeClusterSlots) s = kDecodeCluster;
   return s < 1 ? 1 : (int)s;
 }
 
 size_t swa_decode_bytes(int B, int H, int d, int splits) {
-  return splits == 1 ? 0 : (size_t)B * H * splits * (d + 2) * sizeof(float);
+  return splits <= kDecodeCluster ? 0 : (size_t)B * H * splits * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_swa_decode(const SwaDecodeArgs& a, cudaStream_t st) {

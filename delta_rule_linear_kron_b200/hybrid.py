@@ -55,6 +55,15 @@ def _arg(t, name, dev, dtype, shape):
     raise _invalid(f"{name} is on {t.device}, the call's first tensor on device {dev}")
 
 
+def _out(out, like, dev):
+    """The output tensor, made like `like` if none is given, and its address."""
+    import torch
+    if out is None:
+        out = torch.empty_like(like)
+        return out, out.data_ptr()
+    return out, _arg(out, "out", dev, like.dtype, like.shape)
+
+
 def _bytes_arg(t, name, dev):
     """Address and size of a workspace."""
     if t is None:
@@ -164,14 +173,18 @@ def _rotary(q, k, freqs, pos, interleaved, scale, inverse, out):
         k_shape = _dims(k, "k", len(shape))
         Hk = k_shape[-2]
     half = _dims(freqs, "freqs", 1)[0]
-    oq, ok = (torch.empty_like(q), None if k is None else torch.empty_like(k)) if out is None else out
-    if (ok is None) != (k is None):
-        raise _invalid("out must be a pair like (q, k)")
     kk = (*lead, Hk, d)
+    if out is None:
+        oq, ok = torch.empty_like(q), None if k is None else torch.empty_like(k)
+        pq, pk = oq.data_ptr(), None if k is None else ok.data_ptr()
+    else:
+        oq, ok = out
+        if (ok is None) != (k is None):
+            raise _invalid("out must be a pair like (q, k)")
+        pq, pk = _arg(oq, "out[0]", dev, dtype, shape), _arg(ok, "out[1]", dev, dtype, kk)
     _call(lib().kron_delta_rotary, dev, _arg(q, "q", dev, dtype, shape), _arg(k, "k", dev, dtype, kk),
           _arg(freqs, "freqs", dev, torch.float64, (half,)), _arg(pos, "pos", dev, torch.int64, lead),
-          _arg(oq, "out[0]", dev, dtype, shape), _arg(ok, "out[1]", dev, dtype, kk), B, T, H, Hk, d, 2 * half,
-          1 if interleaved else 0, inverse, scale, dt)
+          pq, pk, B, T, H, Hk, d, 2 * half, 1 if interleaved else 0, inverse, scale, dt)
     return oq, ok
 
 
@@ -218,14 +231,12 @@ def swa_fwd(q, k, v, window, sinks=0, *, scale=None, out=None, save=False, works
     workspace or None); pass all three (save=True) to swa_bwd."""
     import torch
     B, T, H, Hk, d, dt, dev, ptrs = _swa_inputs(q, k, v)
-    if out is None:
-        out = torch.empty_like(q)
-    lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+    out, p_out = _out(out, q, dev)
+    lse = q.new_empty((B, T, H), dtype=torch.float32)
     if save and workspace is None:
         n = swa_workspace_size(KD_SWA_WS_SAVE, B, T, H, Hk, d, window, sinks, dt)
         workspace = _alloc_ws(n, q.device) if n else None
-    _call(lib().kron_delta_swa_fwd, dev, *ptrs, _arg(out, "out", dev, q.dtype, q.shape), lse.data_ptr(), B, T,
-          H, Hk, d, window, sinks, _scale(scale, d), dt, *_bytes_arg(workspace, "workspace", dev), 1 if save else 0)
+    _call(lib().kron_delta_swa_fwd, dev, *ptrs, p_out, lse.data_ptr(), B, T, H, Hk, d, window, sinks, _scale(scale, d), dt, *_bytes_arg(workspace, "workspace", dev), 1 if save else 0)
     return out, lse, workspace
 
 
@@ -260,15 +271,14 @@ def swa_decode(q, k, v, k_cache, v_cache, pos, window, sinks=0, *, scale=None, o
     Hk = _dims(k, "k", 3)[1]
     dev, dtype, dt = _device(q, "q"), q.dtype, _dtype_code(q)
     kv, cache = (B, Hk, d), (B, sinks + window, Hk, d)
-    if out is None:
-        out = torch.empty_like(q)
+    out, p_out = _out(out, q, dev)
     if workspace is None:
         n = swa_workspace_size(KD_SWA_WS_DECODE, B, 1, H, Hk, d, window, sinks, dt)
         workspace = _alloc_ws(n, q.device) if n else None
     _call(lib().kron_delta_swa_decode, dev, _arg(q, "q", dev, dtype, shape), _arg(k, "k", dev, dtype, kv),
           _arg(v, "v", dev, dtype, kv), _arg(k_cache, "k_cache", dev, dtype, cache),
           _arg(v_cache, "v_cache", dev, dtype, cache), _arg(pos, "pos", dev, torch.int64, (B,)),
-          _arg(out, "out", dev, dtype, shape), B, H, Hk, d, window, sinks, _scale(scale, d), dt,
+          p_out, B, H, Hk, d, window, sinks, _scale(scale, d), dt,
           *_bytes_arg(workspace, "workspace", dev))
     return out
 
@@ -312,13 +322,12 @@ def glr_fwd(x, i_pre, f_pre, a_log, h0=None, *, out=None, want_state=True, save=
     import torch
     shape, dt, dev, ptrs = _glr_inputs(x, i_pre, f_pre, a_log, 3)
     B, T, D = shape
-    if out is None:
-        out = torch.empty_like(x)
-    hT = torch.empty((B, D), dtype=torch.float32, device=x.device) if want_state else None
+    out, p_out = _out(out, x, dev)
+    hT = x.new_empty((B, D), dtype=torch.float32) if want_state else None
     if save and workspace is None:
         workspace = _alloc_ws(glr_workspace_size(KD_GLR_WS_SAVE, B, T, D, dt), x.device)
     _call(lib().kron_delta_glr_fwd, dev, *ptrs, _arg(h0, "h0", dev, torch.float32, (B, D)),
-          _arg(out, "out", dev, x.dtype, shape), hT.data_ptr() if want_state else None, B, T, D, dt,
+          p_out, hT.data_ptr() if want_state else None, B, T, D, dt,
           *_bytes_arg(workspace, "workspace", dev), 1 if save else 0)
     return out, hT, workspace
 
@@ -351,10 +360,9 @@ def glr_decode(x, i_pre, f_pre, a_log, h, *, out=None, stream=None):
     import torch
     shape, dt, dev, ptrs = _glr_inputs(x, i_pre, f_pre, a_log, 2)
     B, D = shape
-    if out is None:
-        out = torch.empty_like(x)
+    out, p_out = _out(out, x, dev)
     _call(lib().kron_delta_glr_decode, dev, *ptrs, _arg(h, "h", dev, torch.float32, shape),
-          _arg(out, "out", dev, x.dtype, shape), B, D, dt)
+          p_out, B, D, dt)
     return out
 
 

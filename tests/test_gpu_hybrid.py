@@ -292,9 +292,11 @@ def test_swa_decode_heads(dtype, d, H, Hk):
     check_decode(H, Hk, d, 40, 3, dtype, [0, 1, 2, 3, 41, 42, 43, 44, 100, -1], seed=H + d)
 
 
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 128), (7, 0), (500, 4), (1000, 1)])
-def test_swa_decode_windows(window, sinks):
-    check_decode(4, 1, 64, window, sinks, "bf16", [0, window - 1, window, window + sinks, 2 * window + sinks + 3, -7], seed=window)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 128), (7, 0), (500, 4), (1000, 1), (9000, 3)])
+def test_swa_decode_windows(window, sinks, dtype):
+    """One CTA, a cluster's parts, and (9000) parts through the workspace."""
+    check_decode(4, 1, 64, window, sinks, dtype, [0, window - 1, window, window + sinks, 2 * window + sinks + 3, -7], seed=window)
 
 
 def test_swa_decode_far_position():
@@ -319,12 +321,12 @@ def test_swa_decode_captured_graphs_with_their_own_workspaces():
     args = []
     for seed in (0, 1):
         torch.manual_seed(seed)
-        B, H, Hk, d, window, sinks = 2, 4, 2, 128, 700, 4
+        B, H, Hk, d, window, sinks = 2, 4, 2, 128, 9000, 4
         a = dict(q=torch.randn(B, H, d, device="cuda").bfloat16(), k=torch.randn(B, Hk, d, device="cuda").bfloat16(),
                  v=torch.randn(B, Hk, d, device="cuda").bfloat16(),
                  k_cache=torch.randn(B, window + sinks, Hk, d, device="cuda").bfloat16(),
                  v_cache=torch.randn(B, window + sinks, Hk, d, device="cuda").bfloat16(),
-                 pos=torch.tensor([900, 350], device="cuda"), window=window, sinks=sinks)
+                 pos=torch.tensor([12000, 350], device="cuda"), window=window, sinks=sinks)
         n = kd.swa_workspace_size(kd.KD_SWA_WS_DECODE, B, 1, H, Hk, d, window, sinks, kd.KD_BF16)
         assert n > 0  # a split cache
         a["workspace"] = torch.empty(n, dtype=torch.uint8, device="cuda")

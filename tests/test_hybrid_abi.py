@@ -83,7 +83,7 @@ DEC = dict(q=P, k=P, v=P, kc=P, vc=P, pos=P, out=P, B=1, H=4, Hk=2, d=64, window
 
 @pytest.mark.parametrize("over,code,word", SHAPES + [
     (dict(kc=None), INV, b"k_cache"), (dict(pos=None), INV, b"pos"), (dict(pos=ODD), INV, b"aligned"),
-    (dict(window=5000), WS, b"decode workspace"),
+    (dict(window=20000), WS, b"decode workspace"),
 ])
 def test_swa_decode_refusals(L, over, code, word):
     assert L.kron_delta_swa_decode(*_with(DEC, over)) == code
@@ -147,7 +147,8 @@ def test_workspace_sizes(L):
     assert kd.swa_workspace_size(kd.KD_SWA_WS_BWD, 2, 100, 4, 2, 64, 8, 2, 1) > base
     assert kd.swa_workspace_size(kd.KD_SWA_WS_BWD, 2, 100, 4, 2, 64, 100, 2, 1) == base  # the window is the sequence
     assert kd.swa_workspace_size(kd.KD_SWA_WS_DECODE, 512, 1, 16, 4, 128, 64, 0, 1) == 0
-    assert kd.swa_workspace_size(kd.KD_SWA_WS_DECODE, 1, 1, 16, 4, 128, 4096, 4, 1) > 0
+    assert kd.swa_workspace_size(kd.KD_SWA_WS_DECODE, 1, 1, 16, 4, 128, 4096, 4, 1) == 0  # a cluster joins the parts
+    assert kd.swa_workspace_size(kd.KD_SWA_WS_DECODE, 1, 1, 16, 4, 128, 20000, 4, 1) > 0
     assert kd.glr_workspace_size(kd.KD_GLR_WS_SAVE, 3, 65, 16, 1) == 3 * 2 * 16 * 4
     for bad in (lambda: kd.swa_workspace_size(7, 1, 1, 1, 1, 32, 1, 0, 1),
                 lambda: kd.swa_workspace_size(kd.KD_SWA_WS_SAVE, 1, 0, 1, 1, 32, 1, 0, 0),
