@@ -21,9 +21,7 @@
 // Hk4 T16384 d128 window 2048).  The output stays in TMEM and is rescaled only
 // when a row's maximum has grown by more than 2^8 over the one its sums refer
 // to (then p <= 2^8, still exact enough in bf16, whose precision does not
-// depend on the size).  Short rows (kFine) take the weights as bf16 high and
-// low parts: over a few keys the roundings of p do not average out, and the
-// backward's delta = dO.o would pass them on to every gradient.
+// depend on the size).
 //
 // Backward: p is recomputed from the saved lse.  dk, dv: 128 keys per CTA
 // (rows are keys: S^T = k q^T, dP^T = v dO^T), 128 queries at a time; dv +=
@@ -54,7 +52,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ bool visible(int t, int j, int W, int S) { return j <= t && (t - j < W || j < S); }
 __device__ __forceinline__ bool single_key(int t, int W, int S) { return t == 0 || (W == 1 && S == 0); }
 
 // A wait that a whole warp gives up together (its TMEM loads need all lanes).
@@ -88,26 +85,44 @@ struct KeyRange {
   __device__ bool has(int kt) const { return kt < first || (kt >= band && kt <= end); }
 };
 
-// N fp32 values of this thread's TMEM lane, scaled, to global bf16; the
-// rounding that is left over goes to `lo` where it is given.
+// Scores of N columns from column 0 on: visible are those below `end` that are
+// at `begin` or later, or below `first` (first tokens).  `upper`, `lower`: which
+// bounds the tile needs at all (one for the whole warp).
 template <int N>
-__device__ __forceinline__ void store_lane(uint32_t lanes, float scale, __nv_bfloat16* dst, __nv_bfloat16* lo) {
+__device__ __forceinline__ void hide(float (&x)[N], bool upper, bool lower, int end, int begin, int first) {
+  if (upper) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = c < end ? x[c] : -INFINITY;
+  }
+  if (lower) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = c >= begin || c < first ? x[c] : -INFINITY;
+  }
+}
+
+// N fp32 values of this thread's TMEM lane, scaled, as bf16 into row r of a
+// swizzled tile (column c0 on) for a TMA store; the rounding that is left over
+// into the same place of `lo` where it is given.
+template <int N>
+__device__ __forceinline__ void stage_lane(uint32_t lanes, float scale, unsigned char* tile, unsigned char* lo, int r,
+                                           int c0) {
 #pragma unroll
   for (int c = 0; c < N; c += 16) {
     float v[16];
-    __syncwarp();  // rows without a destination skip the stores, not the warp's loads
     tc::tmem_ld16(lanes + c, v);
     tc::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16 && dst; i += 8) {
+    for (int i = 0; i < 16; i += 8) {
+      const int k = (c0 + c + i) / 8;  // 16-byte chunk of the row
+      const uint32_t at = k / 8 * 16384 + r * 128 + ((k % 8) ^ (r & 7)) * 16;
       float w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = v[i + e] * scale;
-      store_row<__nv_bfloat16, 8>(dst + c + i, w);
+      store_row<__nv_bfloat16, 8>(reinterpret_cast<__nv_bfloat16*>(tile + at), w);
       if (lo) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] -= __bfloat162float(__float2bfloat16_rn(w[e]));
-        store_row<__nv_bfloat16, 8>(lo + c + i, w);
+        store_row<__nv_bfloat16, 8>(reinterpret_cast<__nv_bfloat16*>(lo + at), w);
       }
     }
   }
@@ -118,6 +133,13 @@ template <int D>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* m, int h, int t0, int b, uint64_t* bar) {
 #pragma unroll
   for (int c = 0; c < D; c += 64) tc::tma_load_4d(dst + c * 256, m, c, h, t0, b, bar);
+}
+
+// The same the other way; rows behind T are not written.
+template <int D>
+__device__ __forceinline__ void store_tile(const unsigned char* src, const CUtensorMap* m, int h, int t0, int b) {
+#pragma unroll
+  for (int c = 0; c < D; c += 64) tc::tma_store_4d(m, src + c * 256, c, h, t0, b);
 }
 
 // D = A B^T of 128 x 128, K = d: both tiles of 128 rows, K-major.
@@ -132,7 +154,8 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
 }
 
 // D (+)= W X of 128 x d, K = 128: W in TMEM, group g's 32 weights in 16 columns
-// at w + 32 g, X a tile of 128 rows read MN-major.
+// at w + 32 g (their low parts in the 16 behind), X a tile of 128 rows read
+// MN-major.
 template <int D>
 __device__ __forceinline__ void mma_mix(uint32_t d, uint32_t w, uint32_t x, bool acc) {
   constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
@@ -149,7 +172,7 @@ struct FwdCfg {
   static constexpr int SLOTS = D == 128 ? 3 : 6;  // ring of key and value tiles
   static constexpr uint32_t P = 2 * TILE;         // behind the two query tiles: weights, 32 KB per group
   static constexpr uint32_t RING = P + 65536;
-  static constexpr uint32_t HALF = RING + SLOTS * TILE;  // bf16 [tile parity][query tile][half][row]
+  static constexpr uint32_t HALF = RING + SLOTS * TILE;  // fp32 [query tile][half of the columns][row]
   static constexpr uint32_t BARS = HALF + 2048;
   static constexpr uint32_t BYTES = BARS + 256;   // no static shared memory: all 227 KB at d = 128
   static constexpr int S_COL = 0, O_COL = 256;    // 128 columns per query tile: scores; the output
@@ -178,7 +201,8 @@ __device__ __forceinline__ int load_of_v(int n, int count) { return (n + 2 < cou
 template <int D, bool kFine>
 __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-    const __grid_constant__ CUtensorMap tv, SwaArgs a) {
+    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+    const __grid_constant__ CUtensorMap tl, SwaArgs a) {
   using Cf = FwdCfg<D>;
   extern __shared__ __align__(1024) unsigned char sm[];
   FwdBars& s = *reinterpret_cast<FwdBars*>(sm + Cf::BARS);
@@ -190,7 +214,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
   const KeyRange all(q0, upto(q0 + 256), W, S, 128);
 
   if (!tiles_aligned(sm, a.err)) return;
-  if (tid == 0) {
+  const int loads = 2 * all.count;
+  volatile int* ab = &s.abort_flag;
+  int kn = 0, vn = 0;
+  const auto load = [&](int n) {  // the ring's n-th tile
+    const bool is_k = kn < all.count && load_of_k(kn) == n;
+    const int slot = n % Cf::SLOTS, tile = is_k ? kn++ : vn++;
+    tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
+    load_tile<D>(sm + Cf::RING + slot * Cf::TILE, is_k ? &tk : &tv, hk, all.tile(tile) * 128, b, &s.full[slot]);
+  };
+  if (warp == kLoadWarp && lane == 0) {  // the first loads fly while the CTA sets up
     tc::mbar_init(&s.q_full, 1);
     for (int i = 0; i < Cf::SLOTS; ++i) {
       tc::mbar_init(&s.full[i], 1);
@@ -204,27 +237,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     }
     tc::mbar_init_fence();
     s.abort_flag = 0;
+    const int two = q0 + 128 < a.T ? 2 : 1;
+    tc::mbar_expect_tx(&s.q_full, two * Cf::TILE);
+    for (int i = 0; i < two; ++i) load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &s.q_full);
+    for (int n = 0; n < Cf::SLOTS && n < loads; ++n) load(n);
   }
   if (warp == 0) tc::tmem_alloc(&s.tmem, 512);
   tc::tc_before_sync();
   __syncthreads();
   tc::tc_after_sync();
   const uint32_t tmem = s.tmem;
-  volatile int* ab = &s.abort_flag;
-  const int loads = 2 * all.count;
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      const bool two = q0 + 128 < a.T;
-      tc::mbar_expect_tx(&s.q_full, (two ? 2 : 1) * Cf::TILE);
-      for (int i = 0; i < (two ? 2 : 1); ++i) load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &s.q_full);
-      int kn = 0, vn = 0;
-      for (int n = 0; n < loads; ++n) {
-        const bool is_k = kn < all.count && load_of_k(kn) == n;
-        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS, tile = is_k ? kn++ : vn++;
-        if (use && !tc::mbar_wait<false>(&s.empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-        tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
-        load_tile<D>(sm + Cf::RING + slot * Cf::TILE, is_k ? &tk : &tv, hk, all.tile(tile) * 128, b, &s.full[slot]);
+      for (int n = Cf::SLOTS; n < loads; ++n) {
+        if (!tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+        load(n);
       }
     }
   } else if (warp >= kMmaWarp) {
@@ -303,12 +331,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     unsigned char* prow = sm + Cf::P + i * 32768 + g * 16384 + r * 128;
     const float s2 = a.scale * kLog2e;
     // the two warps that share 32 rows meet to exchange a value per row: the
-    // maximum of their columns, rounded up to bf16 (any bound near the maximum
-    // will do as the reference, as long as both take the same), at the end the
-    // sum, over the weights that nothing reads any more
+    // maximum of their columns (both have read it before the next scores can
+    // come: s_free follows), at the end the sum (the last product waited for
+    // both)
     const auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + i * 4 + (warp & 3)) : "memory"); };
-    __nv_bfloat16* half = reinterpret_cast<__nv_bfloat16*>(sm + Cf::HALF) + i * 256 + r;
-    float* sums = reinterpret_cast<float*>(sm + Cf::P + i * 32768) + r;
+    float* half = reinterpret_cast<float*>(sm + Cf::HALF) + i * 256 + r;
     float top = -INFINITY, sum = 0.f;  // sums refer to 2^(s2 top)
     for (int n = 0; n < mine.count; ++n) {
       const int k0 = mine.tile(n) * 128;
@@ -318,15 +345,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       tc::tmem_ld32(s_lane, x);
       tc::tmem_ld32(s_lane + 32, x + 32);
       tc::tmem_ld_wait();
-      if (!kFine) {
-        tc::tc_before_sync();
-        tc::mbar_arrive(&s.s_free[i]);
-      }
-      if (!(k0 + 127 <= r0 && (r0 + 127 - k0 < W || k0 + 127 < S))) {
-        const int hi = t - k0 - g * 64, lo = hi - W, sk = S - k0 - g * 64;
-#pragma unroll
-        for (int c = 0; c < 64; ++c) x[c] = c <= hi && (c > lo || c < sk) ? x[c] : -INFINITY;
-      }
+      const int end = t - k0 - g * 64 + 1;
+      hide(x, k0 + 127 > r0, r0 + 127 - k0 >= W && k0 + 127 >= S, end, end - W, S - k0 - g * 64);
       float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
 #pragma unroll
       for (int c = 4; c < 64; c += 4) {
@@ -335,10 +355,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
         m2 = fmaxf(m2, x[c + 2]);
         m3 = fmaxf(m3, x[c + 3]);
       }
-      const __nv_bfloat16 up = __float2bfloat16_ru(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
-      half[(n & 1) * 512 + g * 128] = up;
+      float m = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      half[g * 128] = m;
       meet();
-      const float m = __bfloat162float(__hmax(up, half[(n & 1) * 512 + (g ^ 1) * 128]));
+      m = fmaxf(m, half[(g ^ 1) * 128]);
+      if (!kFine) {
+        tc::tc_before_sync();
+        tc::mbar_arrive(&s.s_free[i]);
+      }
       const bool grow = n == 0 ? m > top : (m - top) * s2 > 8.f;  // false while a row has seen no key
       if (n > 0) {  // the product before has read the weights, and the output is complete
         warp_wait(&s.o_full[i], (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
@@ -401,14 +425,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     if (mine.count) {
       warp_wait(&s.o_full[i], (mine.count - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
       tc::tc_after_sync();
-      sums[g * 128] = sum;
+      half[g * 128] = sum;
       meet();
-      sum += sums[(g ^ 1) * 128];
-      const bool live = t < a.T;
-      const size_t row = ((size_t)b * a.T + t) * a.H + h, at = row * D + g * (D / 2);
-      store_lane<D / 2>(o_lane, 1.f / sum, live ? static_cast<__nv_bfloat16*>(a.out) + at : nullptr,
-                        live && a.olo ? static_cast<__nv_bfloat16*>(a.olo) + at : nullptr);
-      if (live && g == 0) a.lse[row] = fmaf(top, s2, log2f(sum)) * kLn2;
+      sum += half[(g ^ 1) * 128];
+      // out over the queries, its rounding over the weights: nothing reads them any more
+      unsigned char *out = sm + i * Cf::TILE, *lo = sm + Cf::P + i * 32768;
+      stage_lane<D / 2>(o_lane, 1.f / sum, out, a.olo ? lo : nullptr, r, g * (D / 2));
+      if (t < a.T && g == 0) a.lse[((size_t)b * a.T + t) * a.H + h] = fmaf(top, s2, log2f(sum)) * kLn2;
+      tc::fence_proxy_async();
+      asm volatile("bar.sync %0, 256;" ::"r"(9 + i) : "memory");
+      if ((tid & 255) == 0) {
+        store_tile<D>(out, &to, h, r0, b);
+        if (a.olo) store_tile<D>(lo, &tl, h, r0, b);
+        tc::bulk_commit();
+        tc::bulk_wait_read();
+      }
     }
   }
   tc::tc_before_sync();
@@ -440,9 +471,10 @@ struct BwdBars {
 static_assert(sizeof(BwdBars) <= 256, "barriers fit behind the tiles");
 
 // `chains`: MMA chains that a slot's tile and an accumulator's end wait for.
-__device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int chains, int* err) {
+template <typename F>
+__device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int chains, int* err, F first_loads) {
   if (!tiles_aligned(sm, err)) return false;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kLoadWarp * 32) {  // the first loads fly while the CTA sets up
     tc::mbar_init(&s.own, 1);
     for (int i = 0; i < 5; ++i) {
       tc::mbar_init(&s.full[i], 1);
@@ -459,6 +491,7 @@ __device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int cha
     tc::mbar_init(&s.done, chains);
     tc::mbar_init_fence();
     s.abort_flag = 0;
+    first_loads();
   }
   if (threadIdx.x < 32) tc::tmem_alloc(&s.tmem, 512);
   tc::tc_before_sync();
@@ -496,20 +529,31 @@ struct BwdRing {
   }
 };
 
-// 32 weights of this thread's row, rounded, as the A operand at `dst`.
+// 32 weights of this thread's row, rounded, as the A operand at `dst`, and with
+// kFine what the rounding leaves in the 16 columns behind.
+template <bool kFine>
 __device__ __forceinline__ void store_weights(uint32_t dst, const float (&x)[32]) {
   float w[16];
 #pragma unroll
   for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[e], x[e + 1]);
   tc::tmem_st16(dst, w);
+  if (kFine) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint32_t hi = __float_as_uint(w[e / 2]);
+      w[e / 2] = bf16_pair(x[e] - __uint_as_float(hi << 16), x[e + 1] - __uint_as_float(hi & 0xffff0000u));
+    }
+    tc::tmem_st16(dst + 16, w);
+  }
   tc::tmem_st_wait();
   tc::tc_before_sync();
 }
 
-template <int D>
+template <int D, bool kFine>
 __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
-    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, SwaArgs a, SwaBwdLayout L) {
+    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    const __grid_constant__ CUtensorMap tdq, SwaArgs a, SwaBwdLayout L) {
   using Cf = BwdCfg<D, false>;
   constexpr int DP = 256, DQ = 384;  // TMEM: two buffers of scores, dP, dq
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -518,20 +562,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
   const int q0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * 128, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (a.H / a.Hk), W = a.window, S = a.sinks;
   const KeyRange keys(q0, q0 + 128 < a.T ? q0 + 128 : a.T, W, S, 128);
-  if (!bwd_setup(sm, s, 1, a.err)) return;
+  const int count = keys.count;
+  const auto load = [&](int n) {  // k0 v0 k1 v1 ..
+    const int slot = n % Cf::SLOTS;
+    tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
+    load_tile<D>(sm + Cf::RING + slot * Cf::TILE, n & 1 ? &tv : &tk, hk, keys.tile(n / 2) * 128, b, &s.full[slot]);
+  };
+  if (!bwd_setup(sm, s, 1, a.err, [&] {
+        tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
+        load_tile<D>(sm, &tq, h, q0, b, &s.own);
+        load(0);
+        load_tile<D>(sm + Cf::TILE, &tg, h, q0, b, &s.own);
+        for (int n = 1; n < Cf::SLOTS && n < 2 * count; ++n) load(n);
+      }))
+    return;
   const uint32_t tmem = s.tmem;
   volatile int* ab = &s.abort_flag;
-  const int count = keys.count;
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
-      load_tile<D>(sm, &tq, h, q0, b, &s.own);
-      load_tile<D>(sm + Cf::TILE, &tg, h, q0, b, &s.own);
-      for (int n = 0; n < 2 * count; ++n) {  // k0 v0 k1 v1 ..
-        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS;
-        if (use && !tc::mbar_wait<false>(&s.empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-        tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
-        load_tile<D>(sm + Cf::RING + slot * Cf::TILE, n & 1 ? &tv : &tk, hk, keys.tile(n / 2) * 128, b, &s.full[slot]);
+      for (int n = Cf::SLOTS; n < 2 * count; ++n) {
+        if (!tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+        load(n);
       }
     }
   } else if (warp == kMmaWarp) {  // scores and dq
@@ -547,6 +598,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
         }
         ring.ready(&s.ds_ready[n % 2], n >> 1);
         mma_mix<D>(tmem + DQ, tmem + n % 2 * 128, ring.at(2 * n), n > 0);
+        if (kFine) mma_mix<D>(tmem + DQ, tmem + n % 2 * 128 + 16, ring.at(2 * n), true);
         ring.release(2 * n);
       }
       tc::mma_commit(&s.done);
@@ -570,6 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     const float lse2 = reinterpret_cast<const float*>(a.ws + L.lse2)[at];
     const float delta = reinterpret_cast<const float*>(a.ws + L.delta)[at];
     const float s2 = a.scale * kLog2e;
+    const bool lone = single_key(t, W, S);  // dS is exactly 0; its one key is in the tile with an upper bound
     for (int n = 0; n < count; ++n) {
       const int k0 = keys.tile(n) * 128;
       const uint32_t buf = lanes + n % 2 * 128;
@@ -578,11 +631,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
       float x[32], dp[32];
       tc::tmem_ld32(buf, x);
       tc::tmem_ld_wait();
-      if (!(k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S))) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          x[e] = visible(t, k0 + g * 32 + e, W, S) && !single_key(t, W, S) ? x[e] : -INFINITY;
-      }
+      const int end = t - k0 - g * 32 + 1;
+      hide(x, k0 + 127 > q0, q0 + 127 - k0 >= W && k0 + 127 >= S, lone ? 0 : end, end - W, S - k0 - g * 32);
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = ex2(fmaf(x[e], s2, -lse2));
       if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
@@ -591,24 +641,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
       tc::tmem_ld_wait();
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] *= dp[e] - delta;
-      store_weights(buf, x);
+      store_weights<kFine>(buf, x);
       tc::mbar_arrive(&s.ds_ready[n % 2]);
     }
     warp_wait(&s.done, 0, a.err, tc::kErrTimeoutMma, ab);
     tc::tc_after_sync();
-    const size_t row = (((size_t)b * a.T + t) * a.H + h) * D + g * (D / 4);
-    store_lane<D / 4>(tc::tmem_lane_addr(tmem, warp, DQ + g * (D / 4)), a.scale,
-                      t < a.T ? static_cast<__nv_bfloat16*>(a.dq) + row : nullptr, nullptr);
+    stage_lane<D / 4>(tc::tmem_lane_addr(tmem, warp, DQ + g * (D / 4)), a.scale, sm, nullptr, tid & 127, g * (D / 4));
+    tc::fence_proxy_async();
+    asm volatile("bar.sync 1, 512;" ::: "memory");
+    if (tid == 0) {  // over q, which nothing reads any more
+      store_tile<D>(sm, &tdq, h, q0, b);
+      tc::bulk_commit();
+      tc::bulk_wait_read();
+    }
   }
   bwd_finish(tmem);
 }
 
 // blockIdx.x < tiles: a key tile's band, all query heads of its group (only
 // blockIdx.y < Hk); beyond: a piece of the first tokens' far queries, one head.
-template <int D>
+template <int D, bool kFine>
 __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg, SwaArgs a, SwaBwdLayout L,
+    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
+    const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, SwaArgs a, SwaBwdLayout L,
     int tiles, int has_far) {
   using Cf = BwdCfg<D, true>;
   constexpr int DP = 128, DV = 256, DK = 384;  // TMEM: scores, dP, dv, dk
@@ -632,32 +688,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     q_hi = band_end;
   }
   const int hk = h0 / group, qt0 = q_lo / 128, per = (q_hi - 1) / 128 - qt0 + 1, count = per * heads;
-  if (!bwd_setup(sm, s, 2, a.err)) return;
+  const auto load = [&](int n) {  // q0 dO0 q1 dO1 ..; lse2 and delta with q
+    const int slot = n % Cf::SLOTS, i = n / 2, h = h0 + i / per, t0 = (qt0 + i % per) * 128;
+    unsigned char* st = sm + Cf::RING + slot * Cf::TILE;
+    if (n & 1) {
+      tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
+      load_tile<D>(st, &tg, h, t0, b, &s.full[slot]);
+    } else {
+      // the rows of two tiles ago were in this place, and that tile's q in
+      // this slot: the groups were through with them when it was released
+      static_assert(Cf::SLOTS == 4, "rows and q of a tile are replaced together");
+      float* rows = reinterpret_cast<float*>(sm + Cf::ROWS + i % 2 * 1024);
+      const size_t at = ((size_t)b * a.H + h) * L.Tp + t0;
+      tc::mbar_expect_tx(&s.full[slot], Cf::TILE + 1024);
+      load_tile<D>(st, &tq, h, t0, b, &s.full[slot]);
+      tc::bulk_g2s(rows, reinterpret_cast<const float*>(a.ws + L.lse2) + at, 512, &s.full[slot]);
+      tc::bulk_g2s(rows + 128, reinterpret_cast<const float*>(a.ws + L.delta) + at, 512, &s.full[slot]);
+    }
+  };
+  if (!bwd_setup(sm, s, 2, a.err, [&] {
+        tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
+        load_tile<D>(sm, &tk, hk, k0, b, &s.own);
+        load(0);
+        load_tile<D>(sm + Cf::TILE, &tv, hk, k0, b, &s.own);
+        for (int n = 1; n < Cf::SLOTS && n < 2 * count; ++n) load(n);
+      }))
+    return;
   const uint32_t tmem = s.tmem;
   volatile int* ab = &s.abort_flag;
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
-      load_tile<D>(sm, &tk, hk, k0, b, &s.own);
-      load_tile<D>(sm + Cf::TILE, &tv, hk, k0, b, &s.own);
-      for (int n = 0; n < 2 * count; ++n) {  // q0 dO0 q1 dO1 ..; lse2 and delta with q
-        const int slot = n % Cf::SLOTS, use = n / Cf::SLOTS, i = n / 2, h = h0 + i / per, t0 = (qt0 + i % per) * 128;
-        if (use && !tc::mbar_wait<false>(&s.empty[slot], (use - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
-        unsigned char* st = sm + Cf::RING + slot * Cf::TILE;
-        if (n & 1) {
-          tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
-          load_tile<D>(st, &tg, h, t0, b, &s.full[slot]);
-        } else {
-          // the rows of two tiles ago were in this place, and that tile's q in
-          // this slot: the groups were through with them when it was released
-          static_assert(Cf::SLOTS == 4, "rows and q of a tile are replaced together");
-          float* rows = reinterpret_cast<float*>(sm + Cf::ROWS + i % 2 * 1024);
-          const size_t at = ((size_t)b * a.H + h) * L.Tp + t0;
-          tc::mbar_expect_tx(&s.full[slot], Cf::TILE + 1024);
-          load_tile<D>(st, &tq, h, t0, b, &s.full[slot]);
-          tc::bulk_g2s(rows, reinterpret_cast<const float*>(a.ws + L.lse2) + at, 512, &s.full[slot]);
-          tc::bulk_g2s(rows + 128, reinterpret_cast<const float*>(a.ws + L.delta) + at, 512, &s.full[slot]);
-        }
+      for (int n = Cf::SLOTS; n < 2 * count; ++n) {
+        if (!tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+        load(n);
       }
     }
   } else if (warp == kMmaWarp) {  // scores and dv
@@ -673,7 +736,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       };
       scores(0);
       for (int n = 0; n < count && !*ab; ++n) {
-        if (n + 1 < count) scores(n + 1);  // while the groups work on p
+        if (!kFine && n + 1 < count) scores(n + 1);  // while the groups work on p
         const uint32_t g = ring.landed(2 * n + 1), p = ring.base + Cf::P;
         ring.ready(&s.p_ready, n);
         constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
@@ -681,8 +744,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
         for (int i = 0; i < 8; ++i)
           tc::mma_bf16_ss(tmem + DV, tc::desc_sw128(p + i / 4 * 16384 + i % 4 * 32),
                           tc::desc_sw128_mn(g + i * 2048, 16384u), id, n > 0 || i > 0);
+        if (kFine) mma_mix<D>(tmem + DV, tmem, g, true);  // p's low parts, over the scores
         tc::mma_commit(&s.p_read);
         ring.release(2 * n + 1);
+        if (kFine && n + 1 < count) scores(n + 1);
       }
       tc::mma_commit(&s.done);
     }
@@ -697,6 +762,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
         const uint32_t q = ring.landed(2 * n);
         ring.ready(&s.ds_ready[0], n);
         mma_mix<D>(tmem + DK, tmem + DP, q, n > 0);
+        if (kFine) mma_mix<D>(tmem + DK, tmem + DP + 16, q, true);
         ring.release(2 * n);
       }
       tc::mma_commit(&s.done);
@@ -719,16 +785,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       float x[32], dp[32];
       tc::tmem_ld32(buf, x);
       tc::tmem_ld_wait();
-      tc::tc_before_sync();
-      tc::mbar_arrive(&s.s_free);
-      const bool every = k0 + 127 <= q0 && (q0 + 127 - k0 < W || k0 + 127 < S) && q0 >= q_lo && q0 + 127 < q_hi;
-      if (!every) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int t = q0 + g * 32 + e;
-          x[e] = t >= q_lo && t < q_hi && visible(t, key, W, S) ? x[e] : -INFINITY;
-        }
+      if (!kFine) {
+        tc::tc_before_sync();
+        tc::mbar_arrive(&s.s_free);
       }
+      // queries from the key on, up to the window's end (a first token: any)
+      const int c0 = q0 + g * 32, from = (key > q_lo ? key : q_lo) - c0;
+      const int end = (key >= S && key + W < q_hi ? key + W : q_hi) - c0;
+      hide(x, q0 + 127 >= q_hi || (k0 + 127 >= S && q0 + 127 - k0 >= W), q0 < q_lo || q0 < k0 + 127, end, from, 0);
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 l = rows[e / 4];
@@ -738,15 +802,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
         x[e + 3] = ex2(fmaf(x[e + 3], s2, -l.w));
       }
       if (n > 0 && !warp_wait(&s.p_read, (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab)) break;
+      float lo[16];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint4 w;
         uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) wp[e] = __float_as_uint(bf16_pair(x[c * 8 + 2 * e], x[c * 8 + 2 * e + 1]));
+        for (int e = 0; e < 4; ++e) {
+          wp[e] = __float_as_uint(bf16_pair(x[c * 8 + 2 * e], x[c * 8 + 2 * e + 1]));
+          if (kFine)
+            lo[c * 4 + e] = bf16_pair(x[c * 8 + 2 * e] - __uint_as_float(wp[e] << 16),
+                                      x[c * 8 + 2 * e + 1] - __uint_as_float(wp[e] & 0xffff0000u));
+        }
         *reinterpret_cast<uint4*>(prow + ((g % 2 * 4 + c) ^ (tid & 7)) * 16) = w;
       }
       tc::fence_proxy_async();
+      if (kFine) {
+        tc::tmem_st16(buf, lo);
+        tc::tmem_st_wait();
+        tc::tc_before_sync();
+        tc::mbar_arrive(&s.s_free);  // the next scores follow this tile's product
+      }
       tc::mbar_arrive(&s.p_ready);
       if (!warp_wait(&s.dp_full, n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
@@ -760,12 +836,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
         x[e + 2] *= dp[e + 2] - d.z;
         x[e + 3] *= dp[e + 3] - d.w;
       }
-      if (!every) {
+      if (c0 == 0) x[0] = 0.f;  // the first query has one key: dS is exactly 0
+      if (W == 1 && S == 0) {   // and so has every query of a window of one
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (single_key(q0 + g * 32 + e, W, S)) x[e] = 0.f;
+        for (int e = 0; e < 32; ++e) x[e] = 0.f;
       }
-      store_weights(buf + DP, x);
+      store_weights<kFine>(buf + DP, x);
       tc::mbar_arrive(&s.ds_ready[0]);
     }
     warp_wait(&s.done, 0, a.err, tc::kErrTimeoutMma, ab);
@@ -783,22 +859,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     else if (first)
       part = reinterpret_cast<float*>(a.ws + L.band) +
              ((((size_t)(is_k ? 0 : 1) * a.B + b) * a.Hk + hk) * S + key) * D + c0;
-    const bool plain = !far && !first && key < a.T;
-    __nv_bfloat16* dst =
-        static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + (((size_t)b * a.T + key) * a.Hk + hk) * D + c0;
-    store_lane<D / 2>(lanes, f, plain ? dst : nullptr, nullptr);
-    if (k0 < S && has_far) {
+    if (k0 < S && has_far) {  // the tile of the first tokens: row by row
+      __nv_bfloat16* dst =
+          static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + (((size_t)b * a.T + key) * a.Hk + hk) * D + c0;
+      const bool plain = !far && !first && key < a.T;
 #pragma unroll
       for (int c = 0; c < D / 2; c += 16) {
         float v[16];
         __syncwarp();
         tc::tmem_ld16(lanes + c, v);
         tc::tmem_ld_wait();
-        if (part) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(part + c + e) = make_float4(v[e] * f, v[e + 1] * f, v[e + 2] * f, v[e + 3] * f);
-        }
+        for (int e = 0; e < 16; ++e) v[e] *= f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          if (part) *reinterpret_cast<float4*>(part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        if (plain) store_row<__nv_bfloat16, 16>(dst + c, v);
+      }
+    } else {  // dk over k, dv over v, which nothing reads any more
+      stage_lane<D / 2>(lanes, f, sm + (is_k ? 0 : Cf::TILE), nullptr, tid & 127, c0);
+      tc::fence_proxy_async();
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (tid == 0) {
+        store_tile<D>(sm, &tdk, hk, k0, b);
+        store_tile<D>(sm + Cf::TILE, &tdv, hk, k0, b);
+        tc::bulk_commit();
+        tc::bulk_wait_read();
       }
     }
   }
@@ -810,48 +896,55 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-// Rows of at most this many keys take the finer weights.  Measured with bf16
-// gradients, relative to their own rounding (1.41 is what rounding dS alone
-// costs): dq 1.72 at 1 to 2 keys, 1.52 at 9, 1.45 at 129 with one bf16 weight.
+// Rows of at most this many keys take the finer weights.  Errors of dq against
+// its own rounding to bf16, with one bf16 weight: 1.72 at 1 to 2 keys (the
+// forward's rounding of p reaches it through delta), 1.52 at 9, 1.45 at 129,
+// and by chance up to 1.84 where a batch has only some ten rows; from some
+// hundred keys on 1.43, which is what rounding dS alone costs.  With the finer
+// ones 1.00 throughout.  They cost FINE_COST.
 constexpr int kFineKeys = 256;
+bool fine(const SwaArgs& a) {
+  return (a.window + a.sinks < a.T ? a.window + a.sinks : a.T) <= kFineKeys;  // window, sinks <= T
+}
 
 template <int D, bool kFine>
 cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
   using Cf = FwdCfg<D>;
-  CUtensorMap tq, tk, tv;
-  if (!make_tmap_bthd(&tq, a.q, 2, a.B, a.T, a.H, D, 64, true, 128) ||
+  CUtensorMap tq, tk, tv, to, tl;
+  if (!make_tmap_bthd(&to, a.out, 2, a.B, a.T, a.H, D, 64, true, 128) ||
+      !make_tmap_bthd(&tl, a.olo ? a.olo : a.out, 2, a.B, a.T, a.H, D, 64, true, 128) || !make_tmap_bthd(&tq, a.q, 2, a.B, a.T, a.H, D, 64, true, 128) ||
       !make_tmap_bthd(&tk, a.k, 2, a.B, a.T, a.Hk, D, 64, true, 128) ||
       !make_tmap_bthd(&tv, a.v, 2, a.B, a.T, a.Hk, D, 64, true, 128))
     return cudaErrorInvalidValue;
   cudaError_t e = allow_smem(swa_fwd_tc_kernel<D, kFine>, Cf::BYTES);
   if (e != cudaSuccess) return e;
   prof_begin(st, "swa_fwd_tc");
-  swa_fwd_tc_kernel<D, kFine><<<dim3((a.T + 255) / 256, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(tq, tk, tv, a);
+  swa_fwd_tc_kernel<D, kFine><<<dim3((a.T + 255) / 256, a.H, a.B), kTcThreads, Cf::BYTES, st>>>(tq, tk, tv, to, tl, a);
   prof_end(st);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool kFine>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   using CfKv = BwdCfg<D, true>;
   using CfQ = BwdCfg<D, false>;
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
-  CUtensorMap m[4];
-  const void* src[4] = {a.q, a.dO, a.k, a.v};
-  for (int i = 0; i < 4; ++i)
-    if (!make_tmap_bthd(&m[i], src[i], 2, a.B, a.T, i < 2 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(swa_dkv_tc_kernel<D>, CfKv::BYTES);
-  if (e == cudaSuccess) e = allow_smem(swa_dq_tc_kernel<D>, CfQ::BYTES);
+  CUtensorMap m[7];
+  const void* src[7] = {a.q, a.dO, a.dq, a.k, a.v, a.dk, a.dv};
+  for (int i = 0; i < 7; ++i)
+    if (!make_tmap_bthd(&m[i], src[i], 2, a.B, a.T, i < 3 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem(swa_dkv_tc_kernel<D, kFine>, CfKv::BYTES);
+  if (e == cudaSuccess) e = allow_smem(swa_dq_tc_kernel<D, kFine>, CfQ::BYTES);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
   if (e != cudaSuccess) return e;
   const int tiles = (a.T + 127) / 128;
   const int has_far = a.sinks > 0 && 127 + a.window < a.T;
   prof_begin(st, "swa_dkv_tc");
-  swa_dkv_tc_kernel<D><<<dim3(tiles + (has_far ? L.pieces : 0), has_far ? a.H : a.Hk, a.B), kTcThreads, CfKv::BYTES, st>>>(
-      m[2], m[3], m[0], m[1], a, L, tiles, has_far);
+  swa_dkv_tc_kernel<D, kFine><<<dim3(tiles + (has_far ? L.pieces : 0), has_far ? a.H : a.Hk, a.B), kTcThreads, CfKv::BYTES, st>>>(
+      m[3], m[4], m[0], m[1], m[5], m[6], a, L, tiles, has_far);
   prof_end(st);
   prof_begin(st, "swa_dq_tc");
-  swa_dq_tc_kernel<D><<<dim3(tiles, a.H, a.B), kTcThreads, CfQ::BYTES, st>>>(m[0], m[1], m[2], m[3], a, L);
+  swa_dq_tc_kernel<D, kFine><<<dim3(tiles, a.H, a.B), kTcThreads, CfQ::BYTES, st>>>(m[0], m[1], m[3], m[4], m[2], a, L);
   prof_end(st);
   e = cudaGetLastError();
   if (e == cudaSuccess && has_far) e = launch_swa_sink_sum(a, L, 128, st);
@@ -862,10 +955,12 @@ cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
 
 bool swa_tc_supported(int d, int dtype) { return dtype == 1 && (d == 64 || d == 128); }
 cudaError_t launch_swa_fwd_tc(const SwaArgs& a, cudaStream_t st) {
-  const int keys = a.window + a.sinks < a.T ? a.window + a.sinks : a.T;  // window, sinks <= T
-  if (keys <= kFineKeys) return a.d == 64 ? fwd_go<64, true>(a, st) : fwd_go<128, true>(a, st);
+  if (fine(a)) return a.d == 64 ? fwd_go<64, true>(a, st) : fwd_go<128, true>(a, st);
   return a.d == 64 ? fwd_go<64, false>(a, st) : fwd_go<128, false>(a, st);
 }
-cudaError_t launch_swa_bwd_tc(const SwaArgs& a, cudaStream_t st) { return a.d == 64 ? bwd_go<64>(a, st) : bwd_go<128>(a, st); }
+cudaError_t launch_swa_bwd_tc(const SwaArgs& a, cudaStream_t st) {
+  if (fine(a)) return a.d == 64 ? bwd_go<64, true>(a, st) : bwd_go<128, true>(a, st);
+  return a.d == 64 ? bwd_go<64, false>(a, st) : bwd_go<128, false>(a, st);
+}
 
 }  // namespace kd
