@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kB = 64;  // queries and keys of a tile
 constexpr int kThreads = 256;
+constexpr int kPitch = kB + 4;  // of a row of weights: 16-byte aligned
 constexpr float kLog2e = 1.44269504088896f;
 
 __device__ __forceinline__ float* floats(char* ws, size_t off) { return reinterpret_cast<float*>(ws + off); }
@@ -72,20 +73,49 @@ __device__ __forceinline__ void dot_tile(const float* A, const float* B, int ra,
   }
 }
 
-// acc[i][jj] += sum_r Wt[ra + 16 i][r] X[r][rb + 16 jj]
+// The D / 16 columns of thread tx: vectors of E consecutive ones, 16 E apart.
 template <int D>
-__device__ __forceinline__ void mix_tile(const float* Wt, const float* X, int ra, int rb, float (&acc)[4][D / 16]) {
-#pragma unroll 4
-  for (int r = 0; r < kB; ++r) {
-    float w[4];
+struct Cols {
+  static constexpr int N = D / 16, E = N < 4 ? N : 4;
+  static __device__ __forceinline__ int at(int tx, int n) { return n / E * 16 * E + tx * E + n % E; }
+};
+
+// acc[i][n] += sum_r Wt[ra + 16 i][r] X[r][column n of tx], four r at a time:
+// a row of weights and a row of X are one vector access each.
+template <int D>
+__device__ __forceinline__ void mix_tile(const float* Wt, const float* X, int ra, int tx, float (&acc)[4][D / 16]) {
+  using C = Cols<D>;
+  using V = Pack<float, C::E>;
+#pragma unroll 2
+  for (int r = 0; r < kB; r += 4) {
+    float4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = Wt[(ra + 16 * i) * (kB + 1) + r];
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(Wt + (ra + 16 * i) * kPitch + r);
 #pragma unroll
-    for (int jj = 0; jj < D / 16; ++jj) {
-      const float x = X[r * (D + 4) + rb + 16 * jj];
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i][jj] = fmaf(w[i], x, acc[i][jj]);
-    }
+      for (int n = 0; n < C::N; n += C::E) {
+        const V x = *reinterpret_cast<const V*>(X + (r + k) * (D + 4) + C::at(tx, n));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = k == 0 ? w[i].x : k == 1 ? w[i].y : k == 2 ? w[i].z : w[i].w;
+#pragma unroll
+          for (int e = 0; e < C::E; ++e) acc[i][n + e] = fmaf(f, x.x[e], acc[i][n + e]);
+        }
+      }
+  }
+}
+
+// Row of this thread's columns, rounded to T.
+template <typename T, int D>
+__device__ __forceinline__ void store_cols(T* row, int tx, const float (&v)[D / 16]) {
+  using C = Cols<D>;
+#pragma unroll
+  for (int n = 0; n < C::N; n += C::E) {
+    float p[C::E];
+#pragma unroll
+    for (int e = 0; e < C::E; ++e) p[e] = v[n + e];
+    store_row<T, C::E>(row + C::at(tx, n), p);
   }
 }
 
@@ -153,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float e = exp2f(x[i][j] - ms);
-        Pt[(ty + 16 * i) * (kB + 1) + tx + 16 * j] = e;
+        Pt[(ty + 16 * i) * kPitch + tx + 16 * j] = e;
         p += e;
       }
       top[i] = m;
@@ -172,11 +202,12 @@ __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
     const size_t row = (b * a.T + t) * (size_t)a.H + h;
     const float r = 1.f / l;
 #pragma unroll
-    for (int jj = 0; jj < D / 16; ++jj) {
-      const size_t at = row * D + tx + 16 * jj;
-      const T y = from_f<T>(o[i][jj] * r);
-      static_cast<T*>(a.out)[at] = y;
-      if (a.olo) static_cast<T*>(a.olo)[at] = from_f<T>(o[i][jj] * r - to_f(y));
+    for (int n = 0; n < D / 16; ++n) o[i][n] *= r;
+    store_cols<T, D>(static_cast<T*>(a.out) + row * D, tx, o[i]);
+    if (a.olo) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) o[i][n] -= to_f(from_f<T>(o[i][n]));
+      store_cols<T, D>(static_cast<T*>(a.olo) + row * D, tx, o[i]);
     }
     if (tx == 0) a.lse[row] = (top[i] + log2f(l)) * 0.693147180559945f;
   }
@@ -198,7 +229,7 @@ __device__ __forceinline__ void weights(float (&x)[4][4], float (&dp)[4][4], con
       const bool see = t < T_ && visible(t, key, W, S);
       const float p = see ? exp2f(fmaf(x[i][j], s2, -lse2[qi])) : 0.f;
       const float ds = single_key(t, W, S) ? 0.f : p * (dp[i][j] - delta[qi]);
-      const int at = (ty + 16 * i) * (kB + 1) + tx + 16 * j;
+      const int at = (ty + 16 * i) * kPitch + tx + 16 * j;
       if (Pt) Pt[at] = p;
       Dt[at] = ds;
     }
@@ -211,7 +242,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaArgs a, SwaBwdLayout L, int tiles, int far_tiles) {
   extern __shared__ float sm[];
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *G = V + kB * (D + 4);
-  float *Pt = G + kB * (D + 4), *Dt = Pt + kB * (kB + 1), *lse2 = Dt + kB * (kB + 1), *delta = lse2 + kB;
+  float *Pt = G + kB * (D + 4), *Dt = Pt + kB * kPitch, *lse2 = Dt + kB * kPitch, *delta = lse2 + kB;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, group = a.H / a.Hk;
   const size_t b = blockIdx.z;
   const bool far = (int)blockIdx.x >= tiles;
@@ -277,15 +308,13 @@ __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaArgs a, SwaBwdLayo
     }
     const size_t row = ((b * a.T + j) * (size_t)a.Hk + hk) * D;
 #pragma unroll
-    for (int jj = 0; jj < D / 16; ++jj) {
-      const int c = tx + 16 * jj;
-      if (pk) {
-        pk[c] = dk[i][jj] * a.scale;
-        pv[c] = dv[i][jj];
-      } else {
-        static_cast<T*>(a.dk)[row + c] = from_f<T>(dk[i][jj] * a.scale);
-        static_cast<T*>(a.dv)[row + c] = from_f<T>(dv[i][jj]);
-      }
+    for (int n = 0; n < D / 16; ++n) dk[i][n] *= a.scale;
+    if (pk) {
+      store_cols<float, D>(pk, tx, dk[i]);
+      store_cols<float, D>(pv, tx, dv[i]);
+    } else {
+      store_cols<T, D>(static_cast<T*>(a.dk) + row, tx, dk[i]);
+      store_cols<T, D>(static_cast<T*>(a.dv) + row, tx, dv[i]);
     }
   }
 }
@@ -294,7 +323,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) swa_dq_kernel(SwaArgs a, SwaBwdLayout L) {
   extern __shared__ float sm[];
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *G = V + kB * (D + 4);
-  float *Dt = G + kB * (D + 4), *lse2 = Dt + kB * (kB + 1), *delta = lse2 + kB;
+  float *Dt = G + kB * (D + 4), *lse2 = Dt + kB * kPitch, *delta = lse2 + kB;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int q0 = blockIdx.x * kB, h = blockIdx.y, hk = h / (a.H / a.Hk);
   const size_t b = blockIdx.z;
@@ -331,7 +360,8 @@ __global__ void __launch_bounds__(kThreads) swa_dq_kernel(SwaArgs a, SwaBwdLayou
     if (t >= a.T) continue;
     const size_t row = ((b * a.T + t) * (size_t)a.H + h) * D;
 #pragma unroll
-    for (int jj = 0; jj < D / 16; ++jj) static_cast<T*>(a.dq)[row + tx + 16 * jj] = from_f<T>(dq[i][jj] * a.scale);
+    for (int n = 0; n < D / 16; ++n) dq[i][n] *= a.scale;
+    store_cols<T, D>(static_cast<T*>(a.dq) + row, tx, dq[i]);
   }
 }
 
@@ -407,7 +437,7 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 
 template <typename T, int D>
 cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
-  const size_t smem = (3 * kB * (D + 4) + kB * (kB + 1)) * sizeof(float);
+  const size_t smem = (3 * kB * (D + 4) + kB * kPitch) * sizeof(float);
   cudaError_t e = allow_smem(swa_fwd_kernel<T, D>, smem);
   if (e != cudaSuccess) return e;
   prof_begin(st, "swa_fwd_simt");
@@ -419,7 +449,7 @@ cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
-  const size_t tile4 = 4 * kB * (D + 4), w = kB * (kB + 1);
+  const size_t tile4 = 4 * kB * (D + 4), w = kB * kPitch;
   const size_t smem_kv = (tile4 + 2 * w + 2 * kB) * sizeof(float), smem_q = (tile4 + w + 2 * kB) * sizeof(float);
   cudaError_t e = allow_smem(swa_dkv_kernel<T, D>, smem_kv);
   if (e == cudaSuccess) e = allow_smem(swa_dq_kernel<T, D>, smem_q);
