@@ -21,10 +21,10 @@
 // exchanges long.
 //
 // Accuracy: the state's error builds up over 1 / (1 - f) steps, so f must not
-// carry a bias.  With L = log2 f = n + r, |r| <= 1/2, f = 2^n (1 + q), q by the
-// series of 2^r - 1; where n = 0 (every gate that keeps more than 0.7), q is
-// f - 1 without cancellation, and 1 - f^2 = -(f - 1)(1 + f) keeps its relative
-// precision however close f is to 1.
+// carry a bias.  With L = log2 f = n + r, |r| <= 1/2, and q = 2^r - 1 by a
+// polynomial, f = 2^n + 2^n q and f - 1 = (2^n - 1) + 2^n q; where n = 0 (every
+// gate that keeps more than 0.7) f - 1 is q itself, and 1 - f^2 = -(f - 1)(1 + f)
+// keeps its relative precision however close f is to 1.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 #include "kd_tc.cuh"
@@ -88,7 +88,7 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 }
 
 struct Gates {
-  F2 L;  // log2 f
+  F2 L;  // log2 f, with kBack
   F2 f;
   F2 w;  // 1 - f^2
   F2 i;  // sigma(i~)
@@ -102,9 +102,9 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   const float ex = ex2(-kLog2e * fabsf(zf.x)), ey = ex2(-kLog2e * fabsf(zf.y));
   const F2 e = pk(ex, ey);
   const F2 d = add2(e, pk(2.f));
-  // sigma(i~) = 1 / (1 + 2^k), 0 beyond 2^60
-  const float kx = -kLog2e * zi.x, ky = -kLog2e * zi.y;
-  const F2 k2 = pk(ex2(fminf(kx, 60.f)), ex2(fminf(ky, 60.f)));
+  // sigma(i~) = 1 / (1 + 2^k); the bound (2e-37, 0 for every purpose) keeps the
+  // product of reciprocals below in range
+  const F2 k2 = pk(ex2(fminf(-kLog2e * zi.x, 122.f)), ex2(fminf(-kLog2e * zi.y, 122.f)));
   const F2 c = add2(k2, pk(1.f));
   // the reciprocals of 2 + e, 1 + 2^k (and 1 + e) from one of their product
   F2 dc = mul2(d, c), one = add2(e, pk(1.f));
@@ -121,8 +121,6 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
     g.i = mul2(r, d);
     rd = mul2(r, c);
   }
-  const float2 gi = un(g.i);
-  g.i = pk(kx > 60.f ? 0.f : gi.x, ky > 60.f ? 0.f : gi.y);
   // log(1 + e) = 2 artanh(u), u = e / (2 + e) <= 1/3: artanh(u) = u + u z p(z),
   // z = u^2, p of least error on [0, 1/9] (1.6e-8 of the sum)
   const F2 u = mul2(e, rd), z = mul2(u, u);
@@ -131,15 +129,17 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   p = fma2(z, p, pk(3.33333194e-1f));
   p = fma2(mul2(u, z), p, u);
   const F2 soft = fma2(p, pk(2.f), pk(fmaxf(-zf.x, 0.f), fmaxf(-zf.y, 0.f)));
-  // f~ at the type's lowest value starts a new sequence: L stays finite so
-  // that the backward's dl L is 0 there and not 0 * infinity
   const float2 Lf = un(mul2(soft, na2));
-  const float Lx = fmaxf(Lf.x, -1e30f), Ly = fmaxf(Lf.y, -1e30f);
-  g.L = pk(Lx, Ly);
-  const F2 Lc = pk(fmaxf(Lx, -126.f), fmaxf(Ly, -126.f));
+  // the backward's dl L must be 0, not 0 * infinity, where f~ starts a new sequence
+  if (kBack) g.L = pk(fmaxf(Lf.x, -1e30f), fmaxf(Lf.y, -1e30f));
+  const F2 Lc = pk(fmaxf(Lf.x, -127.f), fmaxf(Lf.y, -127.f));
   const float kMagic = 12582912.f;  // 1.5 2^23: rounds to an integer, kept in the low bits
   const F2 t = add2(Lc, pk(kMagic));
   const F2 n = add2(t, pk(-kMagic)), x = fma2(n, pk(-1.f), Lc);
+  // 2^n by its bits; n = -127 gives exactly 0
+  const float2 t2 = un(t);
+  const F2 s = pk(__uint_as_float((__float_as_uint(t2.x) << 23) + 0x3f800000u),
+                  __uint_as_float((__float_as_uint(t2.y) << 23) + 0x3f800000u));
   // (2^x - 1) / x of least error on [-1/2, 1/2] (1.3e-8 of it)
   F2 q = fma2(x, pk(1.54697351e-4f), pk(1.33908668e-3f));
   q = fma2(x, q, pk(9.61803086e-3f));
@@ -147,14 +147,8 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   q = fma2(x, q, pk(2.40226507e-1f));
   q = fma2(x, q, pk(6.93147182e-1f));
   q = mul2(q, x);
-  const float2 t2 = un(t), m2 = un(add2(q, pk(1.f))), q2 = un(q);
-  float fx = __uint_as_float(__float_as_uint(m2.x) + (__float_as_uint(t2.x) << 23));
-  float fy = __uint_as_float(__float_as_uint(m2.y) + (__float_as_uint(t2.y) << 23));
-  fx = Lx < -126.f ? 0.f : fx;
-  fy = Ly < -126.f ? 0.f : fy;
-  g.f = pk(fx, fy);
-  const float2 y2 = un(add2(g.f, pk(-1.f)));
-  const F2 y = pk(t2.x == kMagic ? q2.x : y2.x, t2.y == kMagic ? q2.y : y2.y);
+  g.f = fma2(s, q, s);
+  const F2 y = fma2(s, q, add2(s, pk(-1.f)));  // f - 1; for n = 0 it is q
   g.w = mul2(y, fma2(g.f, pk(-1.f), pk(-1.f)));
   return g;
 }
@@ -292,20 +286,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
     if (threadIdx.x == 0 && n + 2 * C < NC)
       load_stage<T, 3>(sm, par, maps, c0, (n + 2 * C) * kChunk, b, &full[par]);
     Run pre = {pk(1.f), pk(0.f)};
-    for (int w = 0; w < warp; ++w) pre = then(pre, runs[par][w][lane]);
-    Run all = pre;
-    for (int w = warp; w < kWarps; ++w) all = then(all, runs[par][w][lane]);
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) pre = then(pre, runs[par][w][lane]);
+    const Run all = then(pre, run);  // in the last warp: the whole chunk
     F2 mine = carry;  // state at the start of this CTA's chunk
     if (C > 1) {
       // warp w hands the chunk's run to CTA w; the buffer's readers of two steps
       // ago are through: their CTA's runs of the step before have arrived here
-      if (warp < C) send(&cruns[par][rank][lane], &runs_in[par], warp, all);
+      if (warp == kWarps - 1)
+        for (int q = 0; q < C; ++q) send(&cruns[par][rank][lane], &runs_in[par], q, all);
       tc::mbar_wait<true>(&runs_in[par], (s >> 1) & 1, err, tc::kErrTimeoutCluster, &abort_flag);
-      for (int q = 0; q < rank; ++q) mine = fma2(cruns[par][q][lane].f, mine, cruns[par][q][lane].h);
-      carry = mine;
-      for (int q = rank; q < C; ++q) carry = fma2(cruns[par][q][lane].f, carry, cruns[par][q][lane].h);
+#pragma unroll
+      for (int q = 0; q < kGlrMaxCluster; ++q)
+        if (q < C) {
+          const Run v = cruns[par][q][lane];
+          if (q == rank) mine = carry;
+          carry = fma2(v.f, carry, v.h);
+        }
     } else {
-      carry = fma2(all.f, carry, all.h);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) carry = fma2(runs[par][w][lane].f, carry, runs[par][w][lane].h);
     }
     const F2 h = fma2(pre.f, mine, pre.h);
     if (states && warp == 0 && live && n < NC) *reinterpret_cast<F2*>(states + ((size_t)b * NC + n) * D + c) = mine;
@@ -416,15 +417,19 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
       load_stage<T, 4>(sm, par ^ 1, maps, c0, chunk(s + 1) * kChunk, b, &full[par ^ 1]);
     // what this warp's last token gets from the later ones: runs of (f products, u)
     Run post = {pk(1.f), pk(0.f)};
-    for (int w = kWarps - 1; w > warp; --w) post = then(post, {runs[par][w][lane].f, us[par][w][lane]});
-    Run all = post;
-    for (int w = warp; w >= 0; --w) all = then(all, {runs[par][w][lane].f, us[par][w][lane]});
+#pragma unroll
+    for (int w = kWarps - 1; w > 0; --w)
+      if (w > warp) post = then(post, {runs[par][w][lane].f, us[par][w][lane]});
+    const Run all = then(post, {run.f, u});  // in the first warp: the whole chunk
     if (C > 1) {
-      if (warp < C) send(&cruns[par][rank][lane], &runs_in[par], warp, all);
+      if (warp == 0)
+        for (int q = 0; q < C; ++q) send(&cruns[par][rank][lane], &runs_in[par], q, all);
     }
     // state before this warp's first token, then before each of its tokens
     F2 h = start;
-    for (int w = 0; w < warp; ++w) h = fma2(runs[par][w][lane].f, h, runs[par][w][lane].h);
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) h = fma2(runs[par][w][lane].f, h, runs[par][w][lane].h);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       const float2 x = P::f(xs[j * 32]);
@@ -434,11 +439,16 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
     F2 mine = carry;
     if (C > 1) {
       tc::mbar_wait<true>(&runs_in[par], (s >> 1) & 1, err, tc::kErrTimeoutCluster, &abort_flag);
-      for (int q = C - 1; q > rank; --q) mine = fma2(cruns[par][q][lane].f, mine, cruns[par][q][lane].h);
-      carry = mine;
-      for (int q = rank; q >= 0; --q) carry = fma2(cruns[par][q][lane].f, carry, cruns[par][q][lane].h);
+#pragma unroll
+      for (int q = kGlrMaxCluster - 1; q >= 0; --q)
+        if (q < C) {
+          const Run v = cruns[par][q][lane];
+          if (q == rank) mine = carry;
+          carry = fma2(v.f, carry, v.h);
+        }
     } else {
-      carry = fma2(all.f, carry, all.h);
+#pragma unroll
+      for (int w = kWarps - 1; w >= 0; --w) carry = fma2(runs[par][w][lane].f, carry, us[par][w][lane]);
     }
     F2 v = fma2(post.f, mine, post.h);
     const size_t off = ((size_t)b * T_ + t0) * D + c;
