@@ -35,7 +35,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kDecodeCluster = 8;
-constexpr int kDecodeClusterSlots = 8192;
+constexpr int kDecodeParts = 64;
+// slots times bytes per channel up to which a cluster's 8 parts are used where
+// more would be wanted.  One sequence, d = 128 bf16 (d = 64 fp32), us by a
+// cluster and by 64 parts and a second kernel: 5.3 and 5.8 (6.9 and 6.4) for
+// 1024 slots, 9.5 and 8.0 (17 and 8.7) for 4096, 24 and 10.5 (58 and 14) for
+// 16384; the second kernel costs the caller 5 us of launch and workspace.
+constexpr int kDecodeClusterBytes = 2 * (4096 + 128);
 constexpr int kBatch = 8;  // rows of keys (then of values) in flight per lane
 constexpr float kLog2e = 1.44269504088896f;
 
@@ -446,21 +452,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecod
   finish<T, D, 16>(a, b, hk * group + g0, heads, n, &sh_m[0][0], &sh_l[0][0], so);
 }
 
-// Joins the parts of one head: weights of the parts first, then the channels.
+// Joins the parts (at most kDecodeParts) of one head: the parts' weights first,
+// in shared memory, then each channel's sum with its loads in flight together.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restrict__ part, int splits,
                                                             T* __restrict__ out) {
+  __shared__ float m[kDecodeParts], w[kDecodeParts];
   const float* p = part + (size_t)blockIdx.x * splits * (D + 2);
-  float top = -INFINITY;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, p[(size_t)s * (D + 2)]);
-  float sum = 0.f, acc = 0.f;
-  if (top != -INFINITY)
-    for (int s = 0; s < splits; ++s) {
-      const float* q = p + (size_t)s * (D + 2);
-      const float f = ex2(q[0] - top);  // 0 for an empty part
-      sum = fmaf(f, q[1], sum);
-      acc = fmaf(f, q[2 + threadIdx.x], acc);
-    }
+  for (int s = threadIdx.x; s < splits; s += D) {
+    const float2 v = *reinterpret_cast<const float2*>(p + (size_t)s * (D + 2));
+    m[s] = v.x;
+    w[s] = v.y;
+  }
+  __syncthreads();
+  float top = -INFINITY, sum = 0.f, acc = 0.f;
+  for (int s = 0; s < splits; ++s) top = fmaxf(top, m[s]);
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float f = m[s] == -INFINITY ? 0.f : ex2(m[s] - top);  // 0 for an empty part
+    sum = fmaf(f, w[s], sum);
+    acc = fmaf(f, p[(size_t)s * (D + 2) + 2 + threadIdx.x], acc);
+  }
   out[(size_t)blockIdx.x * D + threadIdx.x] = from_f<T>(sum > 0.f ? acc / sum : 0.f);
 }
 
@@ -534,14 +546,14 @@ __global__ void __launch_bounds__(256) swa_fill_kernel(const uint4* __restrict__
 }  // namespace
 
 // Parts of a cache: enough CTAs for two on each of 148 SMs, at least 64 slots
-// to a part.  A cluster's 8 parts are enough up to kDecodeClusterSlots; beyond,
-// as many as wanted, through the workspace.
+// to a part.
 int swa_decode_splits(int B, int H, int Hk, int window, int sinks, int dtype) {
   const int gc = heads_per_cta(H / Hk, dtype);
   const long long units = (long long)B * Hk * ((H / Hk + gc - 1) / gc), slots = (long long)window + sinks;
   long long s = (296 + units - 1) / units;
   if (s > (slots + 63) / 64) s = (slots + 63) / 64;
-  if (s > kDecodeCluster && slots <= kDecodeClusterSlots) s = kDecodeCluster;
+  if (s > kDecodeParts) s = kDecodeParts;
+  if (s > kDecodeCluster && slots * (dtype == 1 ? 2 : 4) <= kDecodeClusterBytes) s = kDecodeCluster;
   return s < 1 ? 1 : (int)s;
 }
 

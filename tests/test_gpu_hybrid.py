@@ -293,7 +293,7 @@ def test_swa_decode_heads(dtype, d, H, Hk):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 128), (7, 0), (500, 4), (1000, 1), (9000, 3)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 128), (7, 0), (500, 4), (1000, 1), (3000, 2), (9000, 3)])
 def test_swa_decode_windows(window, sinks, dtype):
     """One CTA, a cluster's parts, and (9000) parts through the workspace."""
     check_decode(4, 1, 64, window, sinks, dtype, [0, window - 1, window, window + sinks, 2 * window + sinks + 3, -7], seed=window)
