@@ -235,31 +235,23 @@ __device__ __forceinline__ void weights(float (&x)[4][4], float (&dp)[4][4], con
     }
 }
 
-// dk, dv of one key tile.  blockIdx.x < tiles: the queries of the tile's band,
-// all query heads of the key head (blockIdx.y < Hk only).  Beyond: the far
-// queries of a tile of first tokens, one piece of them for one query head.
+// dk, dv of key tile `tile` from its band's queries, all query heads of key
+// head h0 / group (piece < 0); or of a tile of first tokens from piece `piece`
+// of the queries beyond its band, query head h0.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaArgs a, SwaBwdLayout L, int tiles, int far_tiles) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void dkv_item(const SwaArgs& a, const SwaBwdLayout& L, float* sm, int tile, int piece, int h0,
+                                         size_t b, bool has_far) {
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *G = V + kB * (D + 4);
   float *Pt = G + kB * (D + 4), *Dt = Pt + kB * kPitch, *lse2 = Dt + kB * kPitch, *delta = lse2 + kB;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, group = a.H / a.Hk;
-  const size_t b = blockIdx.z;
-  const bool far = (int)blockIdx.x >= tiles;
-  const int item = far ? (int)blockIdx.x - tiles : 0, piece = far ? item / far_tiles : 0;
-  const int tile = far ? item % far_tiles : (int)blockIdx.x, k0 = tile * kB;
+  const bool far = piece >= 0;
+  const int k0 = tile * kB, h1 = far ? h0 + 1 : h0 + group;
   const int band_end = (long long)k0 + kB - 1 + a.window < a.T ? k0 + kB - 1 + a.window : a.T;
-  int h0 = blockIdx.y, h1 = h0 + 1, q_lo, q_hi;
+  int q_lo = k0, q_hi = band_end;
   if (far) {
     q_lo = piece * kSwaPiece > band_end ? piece * kSwaPiece : band_end;
     q_hi = (piece + 1) * kSwaPiece < a.T ? (piece + 1) * kSwaPiece : a.T;
     if (q_lo >= q_hi) return;  // the sum skips it too
-  } else {
-    if ((int)blockIdx.y >= a.Hk) return;
-    h0 = blockIdx.y * group;
-    h1 = h0 + group;
-    q_lo = k0;
-    q_hi = band_end;
   }
   const int hk = h0 / group;
   load_tile<T, D>(K, static_cast<const T*>(a.k), k0, a.T, a.Hk, hk, b);
@@ -302,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaArgs a, SwaBwdLayo
       if (j >= a.sinks) continue;
       pk = floats(a.ws, L.part) + ((((size_t)piece * a.B + b) * a.H + h0) * a.sinks + j) * D;
       pv = pk + part;
-    } else if (far_tiles && j < a.sinks) {
+    } else if (has_far && j < a.sinks) {
       pk = floats(a.ws, L.band) + ((b * a.Hk + hk) * a.sinks + j) * D;
       pv = pk + band;
     }
@@ -319,14 +311,13 @@ __global__ void __launch_bounds__(kThreads) swa_dkv_kernel(SwaArgs a, SwaBwdLayo
   }
 }
 
+// dq of query tile `tile`, head h.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) swa_dq_kernel(SwaArgs a, SwaBwdLayout L) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void dq_item(const SwaArgs& a, const SwaBwdLayout& L, float* sm, int tile, int h, size_t b) {
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *G = V + kB * (D + 4);
   float *Dt = G + kB * (D + 4), *lse2 = Dt + kB * kPitch, *delta = lse2 + kB;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int q0 = blockIdx.x * kB, h = blockIdx.y, hk = h / (a.H / a.Hk);
-  const size_t b = blockIdx.z;
+  const int q0 = tile * kB, hk = h / (a.H / a.Hk);
   const int q1 = q0 + kB < a.T ? q0 + kB : a.T;
   load_tile<T, D>(Q, static_cast<const T*>(a.q), q0, a.T, a.H, h, b);
   load_tile<T, D>(G, static_cast<const T*>(a.dO), q0, a.T, a.H, h, b);
@@ -363,6 +354,29 @@ __global__ void __launch_bounds__(kThreads) swa_dq_kernel(SwaArgs a, SwaBwdLayou
     for (int n = 0; n < D / 16; ++n) dq[i][n] *= a.scale;
     store_cols<T, D>(static_cast<T*>(a.dq) + row, tx, dq[i]);
   }
+}
+
+// One launch for all of them: the key tiles, the first tokens' far pieces (far
+// items of `far_tiles` tiles) and the query tiles.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) swa_bwd_kernel(SwaArgs a, SwaBwdLayout L, int tiles, int far_tiles,
+                                                           int key_items, int far_items) {
+  extern __shared__ float sm[];
+  int i = blockIdx.x;
+  if (i < key_items) {
+    const int kb = i / tiles;
+    dkv_item<T, D>(a, L, sm, i % tiles, -1, kb % a.Hk * (a.H / a.Hk), kb / a.Hk, far_tiles > 0);
+    return;
+  }
+  i -= key_items;
+  if (i < far_items) {
+    const int per = L.pieces * far_tiles, hb = i / per;
+    dkv_item<T, D>(a, L, sm, i % far_tiles, i % per / far_tiles, hb % a.H, hb / a.H, true);
+    return;
+  }
+  i -= far_items;
+  const int hb = i / tiles;
+  dq_item<T, D>(a, L, sm, i % tiles, hb % a.H, hb / a.H);
 }
 
 // delta = dO . o (o with its rounding added back) and lse in base 2, by head:
@@ -449,21 +463,18 @@ cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
-  const size_t tile4 = 4 * kB * (D + 4), w = kB * kPitch;
-  const size_t smem_kv = (tile4 + 2 * w + 2 * kB) * sizeof(float), smem_q = (tile4 + w + 2 * kB) * sizeof(float);
-  cudaError_t e = allow_smem(swa_dkv_kernel<T, D>, smem_kv);
-  if (e == cudaSuccess) e = allow_smem(swa_dq_kernel<T, D>, smem_q);
+  const size_t smem = (4 * kB * (D + 4) + 2 * kB * kPitch + 2 * kB) * sizeof(float);
+  cudaError_t e = allow_smem(swa_bwd_kernel<T, D>, smem);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
   if (e != cudaSuccess) return e;
   const int tiles = (a.T + kB - 1) / kB;
   const bool has_far = a.sinks > 0 && kB - 1 + a.window < a.T;
-  const int far_tiles = has_far ? ((a.sinks < a.T ? a.sinks : a.T) + kB - 1) / kB : 0;
-  prof_begin(st, "swa_dkv_simt");
-  swa_dkv_kernel<T, D><<<dim3(tiles + far_tiles * L.pieces, has_far ? a.H : a.Hk, a.B), kThreads, smem_kv, st>>>(
-      a, L, tiles, far_tiles);
-  prof_end(st);
-  prof_begin(st, "swa_dq_simt");
-  swa_dq_kernel<T, D><<<dim3(tiles, a.H, a.B), kThreads, smem_q, st>>>(a, L);
+  const int far_tiles = has_far ? (a.sinks + kB - 1) / kB : 0;  // sinks <= T
+  const long long key_items = (long long)tiles * a.Hk * a.B, far_items = (long long)L.pieces * far_tiles * a.H * a.B;
+  const long long items = key_items + far_items + (long long)tiles * a.H * a.B;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  prof_begin(st, "swa_bwd_simt");
+  swa_bwd_kernel<T, D><<<(unsigned)items, kThreads, smem, st>>>(a, L, tiles, far_tiles, (int)key_items, (int)far_items);
   prof_end(st);
   e = cudaGetLastError();
   if (e == cudaSuccess && has_far) e = launch_swa_sink_sum(a, L, kB, st);

@@ -1,38 +1,40 @@
 // kd_swa_tc.cu -- sliding-window attention with first tokens kept, on tcgen05
 // (bf16, d = 64 and 128).  The formulas are in kd_swa.cu.
 //
+// Times are at H16 Hk16 T16384 d128 window 2048, in us.
+//
 // Every kernel has 19 warps: four groups of four (thread = TMEM lane = tile row,
 // a part of its columns) for the elementwise work, which bounds these kernels
-// (half as many warps with twice the columns: DKV2, DQ2, FWD2), one thread that loads tiles by TMA into a
-// ring, and two that issue MMAs, each the products of one chain (scores, then
-// what is made of them), so that one chain's waits (250 cycles each, even for
-// a phase that is complete) lie beside the other's products.  Tiles are 128 x
-// 128: an MMA of 128 x 64 x 16 takes 50 cycles where one of 128 x 128 x 16
-// takes 68.  B operands of the second products (v, k, dO, q) are read MN-major
-// from the same shared-memory tile that the score product reads K-major, so no
-// tile is stored twice or transposed.
+// (with half as many warps of twice the columns: dk and dv 685 in place of 530,
+// dq 505 in place of 400, the forward 370 in place of 315), one thread that
+// loads tiles by TMA into a ring, and two that issue MMAs, each the products of
+// one chain (scores, then what is made of them), so that one chain's waits (250
+// cycles each, even for a phase that is complete) lie beside the other's
+// products.  Tiles are 128 x 128: an MMA of 128 x 64 x 16 takes 50 cycles where
+// one of 128 x 128 x 16 takes 68.  B operands of the second products (v, k, dO,
+// q) are read MN-major from the same shared-memory tile that the score product
+// reads K-major, so no tile is stored twice or transposed.
 //
-// Forward: 256 queries of one head per CTA, a group to each 128.  Scores are
-// read into registers at once and their TMEM columns given back for the next
-// tile's, p goes to shared memory as the next product's A operand; per tile
-// pair 32 MMAs (2,200 cycles) stand against 2,050 cycles of the hardware
-// exponential.  With p over the scores in TMEM, where a group waits for both
-// products between two tiles, the forward took 0.41 ms in place of FWD_MS (H16
-// Hk4 T16384 d128 window 2048).  The output stays in TMEM and is rescaled only
-// when a row's maximum has grown by more than 2^8 over the one its sums refer
-// to (then p <= 2^8, still exact enough in bf16, whose precision does not
-// depend on the size).
+// Forward: 315, 0.82 PFLOP/s over the visible pairs.  256 queries of one head
+// per CTA, a group to each 128.  Scores are read into registers at once and
+// their TMEM columns given back for the next tile's, p goes to shared memory as
+// the next product's A operand; per tile pair 32 MMAs (2,200 cycles) stand
+// against 2,050 cycles of the hardware exponential.  With p over the scores in
+// TMEM, where a group waits for both products between two tiles, it took 410.
+// The output stays in TMEM and is rescaled only when a row's maximum has grown
+// by more than 2^8 over the one its sums refer to (then p <= 2^8, still exact
+// enough in bf16, whose precision does not depend on the size).
 //
-// Backward: p is recomputed from the saved lse.  dk, dv: 128 keys per CTA
-// (rows are keys: S^T = k q^T, dP^T = v dO^T), 128 queries at a time; dv +=
-// P^T dO, dk += dS^T q.  dq: 128 queries per CTA; dq += dS k.  The two groups
-// take half of the columns of each tile; p is formed while dP is still being
-// multiplied.  dS goes over dP (dq: over the scores, of which it has two
-// buffers) in TMEM; dkv's p goes to shared memory, so that the next scores
-// need not wait for dv.  (64-column tiles, two
-// at a time, a group to each: 0.88 and 0.75 ms in place of DKV_MS and DQ_MS at
-// H16 T16384 d128 window 2048.)  Seven products in place of the five of one
-// joint pass, but no atomics and no fp32 copy of dq: every sum has one order.
+// Backward: 930, 0.97 PFLOP/s over the visible pairs' seven products.  p
+// is recomputed from the saved lse.  dk, dv: 128 keys per CTA (rows are keys:
+// S^T = k q^T, dP^T = v dO^T), 128 queries at a time; dv += P^T dO, dk += dS^T q.
+// dq: 128 queries per CTA; dq += dS k.  The groups take the columns of each tile
+// in parts; p is formed while dP is still being multiplied.  dS goes over dP
+// (dq: over the scores, of which it has two buffers) in TMEM; dkv's p goes to
+// shared memory, so that the next scores need not wait for dv.  (64-column
+// tiles, two at a time, a group to each: dk and dv 880, dq 750.)  Seven products
+// in place of the five of one joint pass, but no atomics and no fp32 copy of
+// dq: every sum has one order.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 #include "kd_tc.cuh"
@@ -549,30 +551,31 @@ __device__ __forceinline__ void store_weights(uint32_t dst, const float (&x)[32]
   tc::tc_before_sync();
 }
 
+struct BwdMaps {  // tiles of 128 rows
+  CUtensorMap q, g, dq, k, v, dk, dv;  // g: dO
+};
+
+// dq of query tile `tile`, head h, batch entry b.
 template <int D, bool kFine>
-__global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
-    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
-    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-    const __grid_constant__ CUtensorMap tdq, SwaArgs a, SwaBwdLayout L) {
+__device__ __forceinline__ void dq_item(const BwdMaps& m, const SwaArgs& a, const SwaBwdLayout& L, unsigned char* sm,
+                                        int tile, int h, int b) {
   using Cf = BwdCfg<D, false>;
   constexpr int DP = 256, DQ = 384;  // TMEM: two buffers of scores, dP, dq
-  extern __shared__ __align__(1024) unsigned char sm[];
   BwdBars& s = *reinterpret_cast<BwdBars*>(sm + Cf::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int q0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * 128, h = blockIdx.y, b = blockIdx.z;
-  const int hk = h / (a.H / a.Hk), W = a.window, S = a.sinks;
+  const int q0 = tile * 128, hk = h / (a.H / a.Hk), W = a.window, S = a.sinks;
   const KeyRange keys(q0, q0 + 128 < a.T ? q0 + 128 : a.T, W, S, 128);
   const int count = keys.count;
   const auto load = [&](int n) {  // k0 v0 k1 v1 ..
     const int slot = n % Cf::SLOTS;
     tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
-    load_tile<D>(sm + Cf::RING + slot * Cf::TILE, n & 1 ? &tv : &tk, hk, keys.tile(n / 2) * 128, b, &s.full[slot]);
+    load_tile<D>(sm + Cf::RING + slot * Cf::TILE, n & 1 ? &m.v : &m.k, hk, keys.tile(n / 2) * 128, b, &s.full[slot]);
   };
   if (!bwd_setup(sm, s, 1, a.err, [&] {
         tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
-        load_tile<D>(sm, &tq, h, q0, b, &s.own);
+        load_tile<D>(sm, &m.q, h, q0, b, &s.own);
         load(0);
-        load_tile<D>(sm + Cf::TILE, &tg, h, q0, b, &s.own);
+        load_tile<D>(sm + Cf::TILE, &m.g, h, q0, b, &s.own);
         for (int n = 1; n < Cf::SLOTS && n < 2 * count; ++n) load(n);
       }))
     return;
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
     tc::fence_proxy_async();
     asm volatile("bar.sync 1, 512;" ::: "memory");
     if (tid == 0) {  // over q, which nothing reads any more
-      store_tile<D>(sm, &tdq, h, q0, b);
+      store_tile<D>(sm, &m.dq, h, q0, b);
       tc::bulk_commit();
       tc::bulk_wait_read();
     }
@@ -658,34 +661,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dq_tc_kernel(
   bwd_finish(tmem);
 }
 
-// blockIdx.x < tiles: a key tile's band, all query heads of its group (only
-// blockIdx.y < Hk); beyond: a piece of the first tokens' far queries, one head.
+// dk, dv of key tile `tile` from its band's queries, all query heads of key
+// head h0 / group (piece < 0); or the first tokens' part from piece `piece` of the
+// queries beyond their tile's band, query head h0.
 template <int D, bool kFine>
-__global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
-    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
-    const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, SwaArgs a, SwaBwdLayout L,
-    int tiles, int has_far) {
+__device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, const SwaBwdLayout& L, unsigned char* sm,
+                                         int tile, int piece, int h0, int b, bool has_far) {
   using Cf = BwdCfg<D, true>;
   constexpr int DP = 128, DV = 256, DK = 384;  // TMEM: scores, dP, dv, dk
-  extern __shared__ __align__(1024) unsigned char sm[];
   BwdBars& s = *reinterpret_cast<BwdBars*>(sm + Cf::BARS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.z, group = a.H / a.Hk, W = a.window, S = a.sinks;
-  const bool far = (int)blockIdx.x >= tiles;
-  const int piece = far ? (int)blockIdx.x - tiles : 0, k0 = far ? 0 : (int)blockIdx.x * 128;
+  const int group = a.H / a.Hk, W = a.window, S = a.sinks, k0 = tile * 128;
+  const bool far = piece >= 0;
   const int band_end = k0 + 127 + W < a.T ? k0 + 127 + W : a.T;
-  int h0 = blockIdx.y, heads = 1, q_lo, q_hi;
+  const int heads = far ? 1 : group;
+  int q_lo = k0, q_hi = band_end;
   if (far) {
     q_lo = piece * kSwaPiece > band_end ? piece * kSwaPiece : band_end;
     q_hi = (piece + 1) * kSwaPiece < a.T ? (piece + 1) * kSwaPiece : a.T;
     if (q_lo >= q_hi) return;  // the sum skips it too
-  } else {
-    if ((int)blockIdx.y >= a.Hk) return;
-    h0 = blockIdx.y * group;
-    heads = group;
-    q_lo = k0;
-    q_hi = band_end;
   }
   const int hk = h0 / group, qt0 = q_lo / 128, per = (q_hi - 1) / 128 - qt0 + 1, count = per * heads;
   const auto load = [&](int n) {  // q0 dO0 q1 dO1 ..; lse2 and delta with q
@@ -693,7 +687,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
     unsigned char* st = sm + Cf::RING + slot * Cf::TILE;
     if (n & 1) {
       tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
-      load_tile<D>(st, &tg, h, t0, b, &s.full[slot]);
+      load_tile<D>(st, &m.g, h, t0, b, &s.full[slot]);
     } else {
       // the rows of two tiles ago were in this place, and that tile's q in
       // this slot: the groups were through with them when it was released
@@ -701,16 +695,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       float* rows = reinterpret_cast<float*>(sm + Cf::ROWS + i % 2 * 1024);
       const size_t at = ((size_t)b * a.H + h) * L.Tp + t0;
       tc::mbar_expect_tx(&s.full[slot], Cf::TILE + 1024);
-      load_tile<D>(st, &tq, h, t0, b, &s.full[slot]);
+      load_tile<D>(st, &m.q, h, t0, b, &s.full[slot]);
       tc::bulk_g2s(rows, reinterpret_cast<const float*>(a.ws + L.lse2) + at, 512, &s.full[slot]);
       tc::bulk_g2s(rows + 128, reinterpret_cast<const float*>(a.ws + L.delta) + at, 512, &s.full[slot]);
     }
   };
   if (!bwd_setup(sm, s, 2, a.err, [&] {
         tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
-        load_tile<D>(sm, &tk, hk, k0, b, &s.own);
+        load_tile<D>(sm, &m.k, hk, k0, b, &s.own);
         load(0);
-        load_tile<D>(sm + Cf::TILE, &tv, hk, k0, b, &s.own);
+        load_tile<D>(sm + Cf::TILE, &m.v, hk, k0, b, &s.own);
         for (int n = 1; n < Cf::SLOTS && n < 2 * count; ++n) load(n);
       }))
     return;
@@ -881,14 +875,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_dkv_tc_kernel(
       tc::fence_proxy_async();
       asm volatile("bar.sync 1, 512;" ::: "memory");
       if (tid == 0) {
-        store_tile<D>(sm, &tdk, hk, k0, b);
-        store_tile<D>(sm + Cf::TILE, &tdv, hk, k0, b);
+        store_tile<D>(sm, &m.dk, hk, k0, b);
+        store_tile<D>(sm + Cf::TILE, &m.dv, hk, k0, b);
         tc::bulk_commit();
         tc::bulk_wait_read();
       }
     }
   }
   bwd_finish(tmem);
+}
+
+// One launch for all of them: the key tiles, the first tokens' far pieces and
+// the query tiles.  One launch and two, delta pass included: 61 and 77 us (T1024
+// H16 Hk4 window 512), 485 and 500 (T16384), 330 and 400 (T4096 Hk1 window
+// 1024), the same where every SM has many tiles of each kind.
+template <int D, bool kFine>
+__global__ void __launch_bounds__(kTcThreads, 1) swa_bwd_tc_kernel(const __grid_constant__ BwdMaps m, SwaArgs a,
+                                                                   SwaBwdLayout L, int tiles, int far_items,
+                                                                   int key_items) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  int i = blockIdx.x;
+  if (i < key_items) {
+    const int group = a.H / a.Hk, kb = i / tiles;
+    dkv_item<D, kFine>(m, a, L, sm, i % tiles, -1, kb % a.Hk * group, kb / a.Hk, far_items > 0);
+    return;
+  }
+  i -= key_items;
+  if (i < far_items) {
+    const int hb = i / L.pieces;
+    dkv_item<D, kFine>(m, a, L, sm, 0, i % L.pieces, hb % a.H, hb / a.H, true);
+    return;
+  }
+  i -= far_items;
+  const int hb = i / tiles;
+  dq_item<D, kFine>(m, a, L, sm, tiles - 1 - i % tiles, hb % a.H, hb / a.H);
 }
 
 template <typename K>
@@ -901,7 +921,8 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 // forward's rounding of p reaches it through delta), 1.52 at 9, 1.45 at 129,
 // and by chance up to 1.84 where a batch has only some ten rows; from some
 // hundred keys on 1.43, which is what rounding dS alone costs.  With the finer
-// ones 1.00 throughout.  They cost FINE_COST.
+// ones 1.00 throughout.  They cost 144 -> 175 us forward and 376 -> 469
+// backward at T16384 H16 Hk4 d128 window 252, 10 -> 11.5 and 11 -> 13 at T200.
 constexpr int kFineKeys = 256;
 bool fine(const SwaArgs& a) {
   return (a.window + a.sinks < a.T ? a.window + a.sinks : a.T) <= kFineKeys;  // window, sinks <= T
@@ -912,7 +933,8 @@ cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
   using Cf = FwdCfg<D>;
   CUtensorMap tq, tk, tv, to, tl;
   if (!make_tmap_bthd(&to, a.out, 2, a.B, a.T, a.H, D, 64, true, 128) ||
-      !make_tmap_bthd(&tl, a.olo ? a.olo : a.out, 2, a.B, a.T, a.H, D, 64, true, 128) || !make_tmap_bthd(&tq, a.q, 2, a.B, a.T, a.H, D, 64, true, 128) ||
+      !make_tmap_bthd(&tl, a.olo ? a.olo : a.out, 2, a.B, a.T, a.H, D, 64, true, 128) ||
+      !make_tmap_bthd(&tq, a.q, 2, a.B, a.T, a.H, D, 64, true, 128) ||
       !make_tmap_bthd(&tk, a.k, 2, a.B, a.T, a.Hk, D, 64, true, 128) ||
       !make_tmap_bthd(&tv, a.v, 2, a.B, a.T, a.Hk, D, 64, true, 128))
     return cudaErrorInvalidValue;
@@ -926,25 +948,24 @@ cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
 
 template <int D, bool kFine>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
-  using CfKv = BwdCfg<D, true>;
-  using CfQ = BwdCfg<D, false>;
+  constexpr uint32_t kBytes = BwdCfg<D, true>::BYTES > BwdCfg<D, false>::BYTES ? BwdCfg<D, true>::BYTES
+                                                                               : BwdCfg<D, false>::BYTES;
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
-  CUtensorMap m[7];
+  BwdMaps m;
+  CUtensorMap* maps[7] = {&m.q, &m.g, &m.dq, &m.k, &m.v, &m.dk, &m.dv};
   const void* src[7] = {a.q, a.dO, a.dq, a.k, a.v, a.dk, a.dv};
   for (int i = 0; i < 7; ++i)
-    if (!make_tmap_bthd(&m[i], src[i], 2, a.B, a.T, i < 3 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem(swa_dkv_tc_kernel<D, kFine>, CfKv::BYTES);
-  if (e == cudaSuccess) e = allow_smem(swa_dq_tc_kernel<D, kFine>, CfQ::BYTES);
+    if (!make_tmap_bthd(maps[i], src[i], 2, a.B, a.T, i < 3 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
+  cudaError_t e = allow_smem(swa_bwd_tc_kernel<D, kFine>, kBytes);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
   if (e != cudaSuccess) return e;
   const int tiles = (a.T + 127) / 128;
-  const int has_far = a.sinks > 0 && 127 + a.window < a.T;
-  prof_begin(st, "swa_dkv_tc");
-  swa_dkv_tc_kernel<D, kFine><<<dim3(tiles + (has_far ? L.pieces : 0), has_far ? a.H : a.Hk, a.B), kTcThreads, CfKv::BYTES, st>>>(
-      m[3], m[4], m[0], m[1], m[5], m[6], a, L, tiles, has_far);
-  prof_end(st);
-  prof_begin(st, "swa_dq_tc");
-  swa_dq_tc_kernel<D, kFine><<<dim3(tiles, a.H, a.B), kTcThreads, CfQ::BYTES, st>>>(m[0], m[1], m[3], m[4], m[2], a, L);
+  const bool has_far = a.sinks > 0 && 127 + a.window < a.T;
+  const long long key_items = (long long)tiles * a.Hk * a.B, far_items = has_far ? (long long)L.pieces * a.H * a.B : 0;
+  const long long items = key_items + far_items + (long long)tiles * a.H * a.B;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  prof_begin(st, "swa_bwd_tc");
+  swa_bwd_tc_kernel<D, kFine><<<(unsigned)items, kTcThreads, kBytes, st>>>(m, a, L, tiles, (int)far_items, (int)key_items);
   prof_end(st);
   e = cudaGetLastError();
   if (e == cudaSuccess && has_far) e = launch_swa_sink_sum(a, L, 128, st);
