@@ -510,12 +510,15 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const T* __restrict__ x
   *reinterpret_cast<V*>(out + at) = P::of(y);
 }
 
-// CTAs of a cluster (chunks taken at a time): enough CTAs for two on each of
-// 148 SMs, as far as the sequence has chunks, and at most the portable 8.
+// CTAs of a cluster (chunks taken at a time): enough CTAs for all of 148 SMs,
+// as far as the sequence has chunks, and at most the portable 8.  Forward and
+// backward in us, clusters of 8 and of 1: 113 and 433, 186 and 786 (B1 T16384
+// D2048: 256 CTAs and 32); where D and B make 256 CTAs by themselves, clusters
+// of 1 and of 2: 179 and 189, 317 and 328 (B8 T4096 D2048).
 int cluster_size(const GlrArgs& a, int NC) {
   const long long lanes = (long long)((a.D + kChans - 1) / kChans) * a.B;
   int C = 1;
-  while (C < kGlrMaxCluster && C < NC && lanes * C < 2 * 148) C *= 2;
+  while (C < kGlrMaxCluster && C < NC && lanes * C < 148) C *= 2;
   return C;
 }
 

@@ -127,8 +127,9 @@ cudaError_t rotary_copy(const RotaryArgs& a, const RotaryShape& s, cudaStream_t 
 
 template <typename T>
 cudaError_t rotary_t(const RotaryArgs& a, const RotaryShape& s, cudaStream_t st) {
-  // 16-byte vectors where the number of pairs allows them: a half-layout item
-  // is two vectors of V channels, an interleaved one a vector of 2V
+  // 16-byte vectors where the number of pairs allows them (at 16384 x 32 heads
+  // of 128 bf16 48 us; 4-byte ones 66, single channels 108): a half-layout
+  // item is two vectors of V channels, an interleaved one a vector of 2V
   constexpr int W = 16 / sizeof(T);
   if (a.interleaved) {
     switch (pow2_in(s.pairs, W / 2)) {
@@ -154,7 +155,13 @@ cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st) {
   s.d = a.d;
   s.rot = a.rot;
   s.pairs = a.rot / 2;
-  s.tokens = a.rows >= 4096 ? 4 : 1;
+  // Tokens per CTA: up to 8 while that leaves 512 CTAs and at most 32 KB to one.
+  // 1 and 4 (8) tokens, us: 2.8 and 4.1 for 256 tokens of 16 + 16 heads of 128
+  // bf16, 14.7 and 13.9 for 4096, 57.7 and 48.4 for 16384; 25.6 and 10.2 (9.5)
+  // for 16384 of 8 + 2 heads of 64.
+  const long long row = (long long)(a.heads[0] + a.heads[1]) * a.d * (a.dtype == 1 ? 2 : 4);
+  s.tokens = 1;
+  while (s.tokens < 8 && a.rows / (2 * s.tokens) >= 512 && 2 * s.tokens * row <= 32768) s.tokens *= 2;
   return a.dtype == 1 ? rotary_t<__nv_bfloat16>(a, s, st) : rotary_t<float>(a, s, st);
 }
 

@@ -42,6 +42,10 @@ constexpr int kDecodeParts = 64;
 // 1024 slots, 9.5 and 8.0 (17 and 8.7) for 4096, 24 and 10.5 (58 and 14) for
 // 16384; the second kernel costs the caller 5 us of launch and workspace.
 constexpr int kDecodeClusterBytes = 2 * (4096 + 128);
+// CTAs of a call that run at once: two on each of 148 SMs, less what clusters
+// leave free.  64 x 4 key heads in 2, 1 parts: 31, 25 us (512, 256 CTAs); 16 x 4
+// in 5, 4, 3, 2 parts: 36, 25, 27, 27 us; 24 x 4 in 3, 2 parts: 50, 37 us.
+constexpr int kDecodeCtas = 272;
 constexpr int kBatch = 8;  // rows of keys (then of values) in flight per lane
 constexpr float kLog2e = 1.44269504088896f;
 
@@ -476,14 +480,28 @@ __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restr
   out[(size_t)blockIdx.x * D + threadIdx.x] = from_f<T>(sum > 0.f ? acc / sum : 0.f);
 }
 
-// query heads of a key head that one CTA takes
-int heads_per_cta(int group, int dtype) { return dtype == 1 ? 16 : group >= 3 ? 4 : group; }
+int pieces_of(long long slots) { return (int)((slots + 63) / 64 < kDecodeParts ? (slots + 63) / 64 : kDecodeParts); }
+
+// Query heads of a key head that one CTA takes.  bf16: all, up to the 16 rows
+// of a product.  fp32, where each costs arithmetic: the fewest of 1, 2, 4 whose
+// CTAs still run at once when a cluster shares each cache.  H16 Hk4 d128 window
+// 1024, us with 4, 2, 1: 12, 10, 9 for one sequence, 14, 12, 13 for 4, 23, 24,
+// 40 for 16, 90, 106, 152 for 64 (each in its best number of parts).
+int heads_per_cta(int B, int H, int Hk, int window, int sinks, int dtype) {
+  if (dtype == 1) return 16;
+  const int group = H / Hk, parts = pieces_of((long long)window + sinks);
+  int gc = 1;
+  while (gc < 4 && gc < group &&
+         (long long)B * Hk * ((group + gc - 1) / gc) * (parts < kDecodeCluster ? parts : kDecodeCluster) > kDecodeCtas)
+    gc *= 2;
+  return gc;
+}
 
 // One CTA per part, key head (or 16, 4 of its query heads) and sequence; the
 // parts of up to kDecodeCluster are a cluster.
 template <typename T, int D, typename K>
 cudaError_t decode_go(const SwaDecodeArgs& a, K kernel, size_t smem, cudaStream_t st) {
-  const int gc = heads_per_cta(a.H / a.Hk, a.dtype);
+  const int gc = heads_per_cta(a.B, a.H, a.Hk, a.window, a.sinks, a.dtype);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.splits, a.Hk * ((a.H / a.Hk + gc - 1) / gc), a.B);
   cfg.blockDim = dim3(kWarps * 32);
@@ -508,7 +526,7 @@ cudaError_t decode_go(const SwaDecodeArgs& a, K kernel, size_t smem, cudaStream_
 
 template <int D>
 cudaError_t decode_f32(const SwaDecodeArgs& a, cudaStream_t st) {
-  switch (heads_per_cta(a.H / a.Hk, 0)) {
+  switch (heads_per_cta(a.B, a.H, a.Hk, a.window, a.sinks, 0)) {
     case 1: return decode_go<float, D>(a, swa_decode_kernel<float, D, 1>, 0, st);
     case 2: return decode_go<float, D>(a, swa_decode_kernel<float, D, 2>, 0, st);
     default: return decode_go<float, D>(a, swa_decode_kernel<float, D, 4>, 0, st);
@@ -545,14 +563,12 @@ __global__ void __launch_bounds__(256) swa_fill_kernel(const uint4* __restrict__
 
 }  // namespace
 
-// Parts of a cache: enough CTAs for two on each of 148 SMs, at least 64 slots
-// to a part.
+// Parts of a cache: as many as run at once, at least 64 slots to a part.
 int swa_decode_splits(int B, int H, int Hk, int window, int sinks, int dtype) {
-  const int gc = heads_per_cta(H / Hk, dtype);
+  const int gc = heads_per_cta(B, H, Hk, window, sinks, dtype);
   const long long units = (long long)B * Hk * ((H / Hk + gc - 1) / gc), slots = (long long)window + sinks;
-  long long s = (296 + units - 1) / units;
-  if (s > (slots + 63) / 64) s = (slots + 63) / 64;
-  if (s > kDecodeParts) s = kDecodeParts;
+  long long s = kDecodeCtas / units;
+  if (s > pieces_of(slots)) s = pieces_of(slots);
   if (s > kDecodeCluster && slots * (dtype == 1 ? 2 : 4) <= kDecodeClusterBytes) s = kDecodeCluster;
   return s < 1 ? 1 : (int)s;
 }
