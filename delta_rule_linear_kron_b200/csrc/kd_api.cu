@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -955,6 +956,8 @@ int check_dtype(int dtype) {
   return KD_OK;
 }
 
+size_t width(int dtype) { return dtype == KD_BF16 ? 2 : 4; }
+
 int check_ptr8(const void* p, const char* name, bool required) {
   if (!p) return required ? fail(KD_ERR_INVALID_ARG, "%s must not be NULL", name) : KD_OK;
   if (!aligned(p, 8)) return fail(KD_ERR_INVALID_ARG, "%s must be 8-byte aligned", name);
@@ -966,6 +969,26 @@ int check_in_place(const void* in, const void* out, size_t bytes, const char* na
   const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
   if (a != b && a < b + bytes && b < a + bytes)
     return fail(KD_ERR_INVALID_ARG, "%s overlaps its input (only exactly in place is allowed)", name);
+  return KD_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+  const char* name;
+};
+// No output may share memory with an input or with another output.
+int check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  const auto apart = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return !a.p || !b.p || x >= y + b.n || y >= x + a.n;
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& s : ins)
+      if (!apart(*o, s)) return fail(KD_ERR_INVALID_ARG, "%s overlaps %s", o->name, s.name);
+    for (const Span* s = outs.begin(); s != o; ++s)
+      if (!apart(*o, *s)) return fail(KD_ERR_INVALID_ARG, "%s overlaps %s", o->name, s->name);
+  }
   return KD_OK;
 }
 
@@ -1038,7 +1061,11 @@ int kron_delta_rotary(const void* q, const void* k, const double* freqs, const l
   KD_TRY(check_ptr(k_out, "k_out", Hk > 0));
   const size_t row = (size_t)B * T * d * (dtype == KD_BF16 ? 2 : 4);
   KD_TRY(check_in_place(q, q_out, row * H, "q_out"));
-  if (Hk > 0) KD_TRY(check_in_place(k, k_out, row * Hk, "k_out"));
+  if (Hk > 0) {
+    KD_TRY(check_in_place(k, k_out, row * Hk, "k_out"));
+    KD_TRY(check_apart({{q_out, row * H, "q_out"}}, {{k, row * Hk, "k"}}));
+    KD_TRY(check_apart({{k_out, row * Hk, "k_out"}}, {{q, row * H, "q"}, {q_out, row * H, "q_out"}}));
+  }
   KD_TRY(check_stream(stream));
   kd::RotaryArgs a{};
   a.x[0] = q; a.x[1] = k; a.y[0] = q_out; a.y[1] = k_out; a.heads[0] = H; a.heads[1] = Hk;
@@ -1072,6 +1099,9 @@ int kron_delta_swa_fwd(const void* q, const void* k, const void* v, void* out, f
   if (save != 0 && save != 1) return fail(KD_ERR_INVALID_ARG, "save must be 0 or 1 (got %d)", save);
   const size_t need = save ? swa_save_bytes(B, T, H, d, dtype) : 0;
   KD_TRY(check_ws(workspace, ws_bytes, need, "workspace"));
+  const size_t nq = (size_t)B * T * H * d * width(dtype), nk = nq / H * Hk;
+  KD_TRY(check_apart({{out, nq, "out"}, {lse, (size_t)B * T * H * 4, "lse"}, {need ? workspace : nullptr, need, "workspace"}},
+                     {{q, nq, "q"}, {k, nk, "k"}, {v, nk, "v"}}));
   KD_TRY(check_stream(stream));
   kd::SwaArgs a{};
   a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse; a.olo = need ? workspace : nullptr;
@@ -1104,6 +1134,10 @@ int kron_delta_swa_bwd(const void* q, const void* k, const void* v, const void* 
   KD_TRY(check_ws(fwd_ws, fwd_ws_bytes, saved, "the forward's workspace (save=1)"));
   const kd::SwaBwdLayout L = kd::swa_bwd_layout(B, T, H, Hk, d, clamp_to(window, T), clamp_to(sinks, T));
   KD_TRY(check_ws(workspace, ws_bytes, L.bytes, "backward workspace"));
+  const size_t nq = (size_t)B * T * H * d * width(dtype), nk = nq / H * Hk;
+  KD_TRY(check_apart({{dq, nq, "dq"}, {dk, nk, "dk"}, {dv, nk, "dv"}, {workspace, L.bytes, "workspace"}},
+                     {{q, nq, "q"}, {k, nk, "k"}, {v, nk, "v"}, {out, nq, "out"}, {dO, nq, "dO"},
+                      {lse, (size_t)B * T * H * 4, "lse"}, {saved ? fwd_ws : nullptr, saved, "the forward's workspace"}}));
   KD_TRY(check_stream(stream));
   kd::SwaArgs a{};
   a.q = q; a.k = k; a.v = v; a.o = out; a.lse_in = lse; a.dO = dO; a.dq = dq; a.dk = dk; a.dv = dv;
@@ -1133,6 +1167,9 @@ int kron_delta_swa_decode(const void* q, const void* k, const void* v, void* k_c
   const int splits = kd::swa_decode_splits(B, H, Hk, window, sinks, dtype);
   const size_t need = kd::swa_decode_bytes(B, H, d, splits);
   KD_TRY(check_ws(workspace, ws_bytes, need, "decode workspace"));
+  const size_t nq = (size_t)B * H * d * width(dtype), nk = nq / H * Hk, nc = nk * ((size_t)window + sinks);
+  KD_TRY(check_apart({{out, nq, "out"}, {k_cache, nc, "k_cache"}, {v_cache, nc, "v_cache"}, {need ? workspace : nullptr, need, "workspace"}},
+                     {{q, nq, "q"}, {k, nk, "k"}, {v, nk, "v"}, {pos, (size_t)B * 8, "pos"}}));
   KD_TRY(check_stream(stream));
   kd::SwaDecodeArgs a{q, k, v, k_cache, v_cache, pos, out, B, H, Hk, d, window, sinks, dtype, scale,
                       need ? static_cast<float*>(workspace) : nullptr, splits};
@@ -1149,6 +1186,9 @@ int kron_delta_swa_fill(const void* k, const void* v, const long long* lens, voi
   KD_TRY(check_ptr(v_cache, "v_cache", true));
   const size_t vectors = ((size_t)window + sinks) * B * Hk * d * (dtype == KD_BF16 ? 2 : 4) / 16;
   if (vectors / 256 >= 0x7fffffffu) return fail(KD_ERR_INVALID_ARG, "cache too large (%zu vectors)", vectors);
+  const size_t nk = (size_t)B * T * Hk * d * width(dtype);
+  KD_TRY(check_apart({{k_cache, vectors * 16, "k_cache"}, {v_cache, vectors * 16, "v_cache"}},
+                     {{k, nk, "k"}, {v, nk, "v"}, {lens, (size_t)B * 8, "lens"}}));
   KD_TRY(check_stream(stream));
   kd::SwaFillArgs a{k, v, lens, k_cache, v_cache, B, T, Hk, d, window, sinks, dtype};
   return launched(kd::launch_swa_fill(a, static_cast<cudaStream_t>(stream)), "swa fill launch");
@@ -1182,6 +1222,10 @@ int kron_delta_glr_fwd(const void* x, const void* i_pre, const void* f_pre, cons
   KD_TRY(check_ptr(hT, "hT", false));
   if (save != 0 && save != 1) return fail(KD_ERR_INVALID_ARG, "save must be 0 or 1 (got %d)", save);
   KD_TRY(check_ws(workspace, ws_bytes, save ? glr_save_bytes(B, T, D) : 0, "workspace"));
+  const size_t n = (size_t)B * T * D * width(dtype), nh = (size_t)B * D * 4;
+  const size_t saved = glr_save_bytes(B, T, D);
+  KD_TRY(check_apart({{out, n, "out"}, {hT, nh, "hT"}, {save ? workspace : nullptr, saved, "workspace"}},
+                     {{x, n, "x"}, {i_pre, n, "i_pre"}, {f_pre, n, "f_pre"}, {a_log, (size_t)D * 4, "a_log"}, {h0, nh, "h0"}}));
   KD_TRY(check_stream(stream));
   kd::GlrArgs a{};
   a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.h0 = h0; a.out = out; a.hT = hT;
@@ -1208,6 +1252,11 @@ int kron_delta_glr_bwd(const void* x, const void* i_pre, const void* f_pre, cons
   KD_TRY(check_ptr(dh0, "dh0", false));
   KD_TRY(check_ws(fwd_ws, fwd_ws_bytes, glr_save_bytes(B, T, D), "the forward's workspace (save=1)"));
   KD_TRY(check_ws(workspace, ws_bytes, glr_bwd_bytes(B, D), "backward workspace"));
+  const size_t n = (size_t)B * T * D * width(dtype), nh = (size_t)B * D * 4;
+  KD_TRY(check_apart({{dx, n, "dx"}, {di_pre, n, "di_pre"}, {df_pre, n, "df_pre"}, {da_log, (size_t)D * 4, "da_log"},
+                      {dh0, nh, "dh0"}, {workspace, glr_bwd_bytes(B, D), "workspace"}},
+                     {{x, n, "x"}, {i_pre, n, "i_pre"}, {f_pre, n, "f_pre"}, {a_log, (size_t)D * 4, "a_log"}, {dh, n, "dh"},
+                      {dhT, nh, "dhT"}, {fwd_ws, glr_save_bytes(B, T, D), "the forward's workspace"}}));
   KD_TRY(check_stream(stream));
   kd::GlrArgs a{};
   a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.dh = dh; a.dhT = dhT;
@@ -1227,6 +1276,9 @@ int kron_delta_glr_decode(const void* x, const void* i_pre, const void* f_pre, c
   KD_TRY(check_glr_inputs(x, i_pre, f_pre, a_log));
   KD_TRY(check_ptr(h, "h", true));
   KD_TRY(check_ptr(out, "out", true));
+  const size_t n = (size_t)B * D * width(dtype);
+  KD_TRY(check_apart({{out, n, "out"}, {h, (size_t)B * D * 4, "h"}},
+                     {{x, n, "x"}, {i_pre, n, "i_pre"}, {f_pre, n, "f_pre"}, {a_log, (size_t)D * 4, "a_log"}}));
   KD_TRY(check_stream(stream));
   kd::GlrArgs a{};
   a.x = x; a.i_pre = i_pre; a.f_pre = f_pre; a.a_log = a_log; a.hT = h; a.out = out;

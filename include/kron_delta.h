@@ -517,7 +517,7 @@ KD_API int kron_delta_gdn2_decode(const void *q, const void *k, const void *v, c
  * precision.  Channels rot .. d-1 are copied.
  *   q, q_out : [B,T,H,d] (dtype).  k, k_out : [B,T,Hk,d] (dtype), or NULL with
  *         Hk = 0.  q_out = q and k_out = k (in place) are allowed; any other
- *         overlap is not.
+ *         overlap of an output is refused.
  *   freqs : [rot/2] fp64 (radians per position; scaled contexts change only
  *         these and `scale`).
  *   pos : positions [B,T], 64-bit integers, or NULL for 0 .. T-1.
@@ -553,10 +553,15 @@ KD_API size_t kron_delta_swa_workspace_size(int kind, int B, int T, int H, int H
  *         kron_delta_swa_workspace_size(KD_SWA_WS_SAVE, ...) bytes, 256-byte
  *         aligned (the rounding of the bf16 output, which the backward adds
  *         back; zero bytes for fp32), else NULL.
- * bf16 with d = 64 or 128 runs on tensor cores, the probabilities rounded to
- * bf16 for their product with v; other shapes run on CUDA cores in fp32.
- * Preconditions not checked on the device: q, k, v finite; d in {32, 64, 128}
- * is checked.  Errors as for kron_delta_fwd.  Asynchronous on `stream`.
+ * d in {32, 64, 128}.  bf16 with d = 64 or 128 runs on tensor cores, the
+ * probabilities rounded to bf16 for their product with v (where min(window +
+ * sinks, T) <= 256, to a sum of two bf16 numbers); other shapes run on CUDA
+ * cores in fp32.
+ * Precondition not checked on the device: q, k, v finite, in the rows behind a
+ * shorter sequence too (keys are read by tiles, and a hidden infinity or NaN
+ * in k or v would meet a zero weight).  An output that overlaps an input or
+ * another output is refused.  Errors as for kron_delta_fwd.  Asynchronous on
+ * `stream`.
  */
 KD_API int kron_delta_swa_fwd(const void *q, const void *k, const void *v, void *out, float *lse, int B,
                               int T, int H, int Hk, int d, int window, int sinks, float scale, int dtype,
@@ -568,8 +573,9 @@ KD_API int kron_delta_swa_fwd(const void *q, const void *k, const void *v, void 
  *   dO, dq : [B,T,H,d];  dk, dv : [B,T,Hk,d] (dtype), each summed over the
  *         query heads that read the key head.
  *   workspace : at least kron_delta_swa_workspace_size(KD_SWA_WS_BWD, ...).
- * Every sum runs in a fixed order (bitwise reproducible).  Errors as for
- * kron_delta_bwd.  Asynchronous on `stream`.
+ * Every sum runs in a fixed order (bitwise reproducible).  Preconditions and
+ * overlaps as for the forward, dO included.  Errors as for kron_delta_bwd.
+ * Asynchronous on `stream`.
  */
 KD_API int kron_delta_swa_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse,
                               const void *dO, void *dq, void *dk, void *dv, int B, int T, int H, int Hk,
@@ -589,7 +595,8 @@ KD_API int kron_delta_swa_bwd(const void *q, const void *k, const void *v, const
  *         pos < 0 is idle: its cache is left as it was and its out is zero.
  *   workspace : at least kron_delta_swa_workspace_size(KD_SWA_WS_DECODE, ...)
  *         bytes, 256-byte aligned (NULL where that is 0).
- * Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_WORKSPACE,
+ * An output (the caches too) that overlaps an input or another output is
+ * refused.  Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_WORKSPACE,
  * KD_ERR_CUDA.  Asynchronous on `stream`.
  */
 KD_API int kron_delta_swa_decode(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
@@ -603,8 +610,8 @@ KD_API int kron_delta_swa_decode(const void *q, const void *k, const void *v, vo
  * their slots.  Slots that none of them belongs to are left as they were.
  *   k, v : [B,T,Hk,d] (dtype);  lens : [B] 64-bit integers; a length below 0
  *   counts as 0 and one above T as T.
- * No workspace.  Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_CUDA.
- * Asynchronous on `stream`.
+ * No workspace.  Overlaps are refused.  Errors: KD_ERR_INVALID_ARG,
+ * KD_ERR_UNSUPPORTED, KD_ERR_CUDA.  Asynchronous on `stream`.
  */
 KD_API int kron_delta_swa_fill(const void *k, const void *v, const long long *lens, void *k_cache,
                                void *v_cache, int B, int T, int Hk, int d, int window, int sinks, int dtype,
@@ -628,7 +635,7 @@ KD_API size_t kron_delta_glr_workspace_size(int kind, int B, int T, int D, int d
  *   workspace : with save = 1 at least
  *         kron_delta_glr_workspace_size(KD_GLR_WS_SAVE, ...) bytes, 256-byte
  *         aligned (the fp32 state at each 64th token), else NULL.
- * Errors as for kron_delta_fwd.  Asynchronous on `stream`.
+ * An output that overlaps an input or another output is refused.  Errors as for kron_delta_fwd.  Asynchronous on `stream`.
  */
 KD_API int kron_delta_glr_fwd(const void *x, const void *i_pre, const void *f_pre, const float *a_log,
                               const float *h0, void *out, float *hT, int B, int T, int D, int dtype,
@@ -642,7 +649,7 @@ KD_API int kron_delta_glr_fwd(const void *x, const void *i_pre, const void *f_pr
  *   dx, di_pre, df_pre : [B,T,D] (dtype).  da_log : [D] fp32, summed over the
  *   batch and the tokens in a fixed order.  dh0 : [B,D] fp32 or NULL.
  *   workspace : at least kron_delta_glr_workspace_size(KD_GLR_WS_BWD, ...).
- * Errors as for kron_delta_bwd.  Asynchronous on `stream`.
+ * Overlaps as for the forward.  Errors as for kron_delta_bwd.  Asynchronous on `stream`.
  */
 KD_API int kron_delta_glr_bwd(const void *x, const void *i_pre, const void *f_pre, const float *a_log,
                               const void *dh, const float *dhT, void *dx, void *di_pre, void *df_pre,
@@ -653,7 +660,7 @@ KD_API int kron_delta_glr_bwd(const void *x, const void *i_pre, const void *f_pr
  * One decode step of the gated linear recurrence: one new token per sequence.
  *   x, i_pre, f_pre, out : [B,D] (dtype);  a_log : [D] fp32.
  *   h : [B,D] fp32, read and overwritten with the new state.
- * No workspace.  Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_CUDA.
+ * No workspace.  Overlaps are refused.  Errors: KD_ERR_INVALID_ARG, KD_ERR_UNSUPPORTED, KD_ERR_CUDA.
  * Asynchronous on `stream`.
  */
 KD_API int kron_delta_glr_decode(const void *x, const void *i_pre, const void *f_pre, const float *a_log,

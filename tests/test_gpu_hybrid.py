@@ -557,3 +557,53 @@ def test_a_thread_without_a_context_can_call():
     torch.cuda.synchronize()
     assert rc == [kd.KD_OK, kd.KD_OK]
     assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_captured_training_step_replays_on_new_inputs(dtype):
+    """Forward and backward of all three in one graph, by their functions and
+    by autograd: replayed after the inputs changed, it gives the eager results."""
+    B, T, H, Hk, d, window, sinks = 2, 300, 4, 2, 64, 30, 3
+    rng = np.random.default_rng(5)
+    shapes = [(B, T, H, d), (B, T, Hk, d), (B, T, Hk, d), (B, T, H * d), (B, T, H * d), (B, T, H * d)]
+    new = [draw(rng, s, dtype)[0] for s in shapes]
+    x = [n.clone() for n in new]
+    a_log = torch.rand(H * d, device="cuda")
+    freqs, _ = kd.rotary_freqs(d)
+
+    def calls():
+        q, k, v, zi, zf, g = x
+        qr, kr = kd.rotary_fwd(q, k, freqs)
+        o, lse, ws = kd.swa_fwd(qr, kr, v, window, sinks, save=True)
+        y, _, gw = kd.glr_fwd(o.view(B, T, H * d), zi, zf, a_log, save=True)
+        r = kd.glr_bwd(o.view(B, T, H * d), zi, zf, a_log, None, g, fwd_workspace=gw)
+        s = kd.swa_bwd(qr, kr, v, o, lse, r["dx"].view(B, T, H, d), window, sinks, fwd_workspace=ws)
+        return [y, r["di_pre"], r["df_pre"], r["da_log"], s["dv"], *kd.rotary_bwd(s["dq"], s["dk"], freqs)]
+
+    def graded():
+        leaves = [t.detach().requires_grad_() for t in x[:5]] + [a_log.detach().requires_grad_()]
+        q, k, v, zi, zf, a = leaves
+        qr, kr = kd.RotaryFunction.apply(q, k, freqs)
+        y, _ = kd.GlrFunction.apply(kd.SwaFunction.apply(qr, kr, v, window, sinks).view(B, T, H * d), zi, zf, a)
+        dq, dk, dv, di, df, da = torch.autograd.grad(y, leaves, x[5])
+        return [y.detach(), di, df, da, dv, dq, dk]
+    for fn in (calls, graded):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            fn()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = fn()
+        for _ in range(2):
+            for a, n in zip(x, new):
+                a.copy_(n.roll(1, 1))
+            new = [n.roll(1, 1) for n in new]
+            want = fn()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+        assert kd.device_status() is None

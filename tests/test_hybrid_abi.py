@@ -190,3 +190,28 @@ def test_rotary_freqs_values():
     yarn, s = kd.rotary_freqs(8, scaling="yarn", factor=4.0, trained_len=1000, low=1.0, high=32.0, device="cpu")
     assert yarn[0] == w[0] and torch.allclose(yarn[3], w[3] / 4) and w[1] / 4 < yarn[1] < w[1]
     assert abs(s - 1.1386294361119891) < 1e-12
+
+
+@pytest.mark.parametrize("fn,defaults,outs,ins", [
+    ("rotary", ROT, ["qo", "ko"], ["q", "k"]), ("swa_fwd", FWD, ["out", "lse"], ["q", "k", "v"]),
+    ("swa_bwd", BWD, ["dq", "dk", "dv", "ws"], ["q", "k", "v", "out", "lse", "dO", "fws"]),
+    ("swa_decode", DEC, ["out", "kc", "vc"], ["q", "k", "v", "pos"]), ("swa_fill", FILL, ["kc", "vc"], ["k", "v", "lens"]),
+    ("glr_fwd", GF, ["out", "hT"], ["x", "i", "f", "a", "h0"]),
+    ("glr_bwd", GB, ["dx", "di", "df", "da", "dh0", "ws"], ["x", "i", "f", "a", "dh", "dhT", "fws"]),
+    ("glr_decode", dict(x=P, i=P, f=P, a=P, h=P, out=P, B=1, D=16, dtype=1, stream=None), ["h", "out"], ["x", "i", "f", "a"]),
+])
+def test_outputs_that_overlap_are_refused(L, fn, defaults, outs, ins):
+    a = dict(defaults)
+    for n, name in enumerate(outs + ins):
+        a[name] = ctypes.c_void_p((n + 1) << 24)
+    a["B"] = 4
+    call = getattr(L, "kron_delta_" + fn)
+    for o in outs:
+        for other in outs + ins:
+            if other == o or (fn == "rotary" and (o, other) in (("qo", "q"), ("ko", "k"))):
+                continue
+            for shift in (0, 16):  # the other's last bytes too: every tensor here holds more than 16
+                b = dict(a)
+                b[o] = ctypes.c_void_p(a[other].value + shift) if (o, shift) != ("ws", 16) else a[other]
+                assert call(*b.values()) == INV, (o, other)
+                assert b"overlaps" in L.kron_delta_last_error()
