@@ -366,31 +366,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
         tc::mbar_arrive(&s.s_free[i]);
       }
       const bool grow = n == 0 ? m > top : (m - top) * s2 > 8.f;  // false while a row has seen no key
-      if (n > 0) {  // the product before has read the weights, and the output is complete
-        warp_wait(&s.o_full[i], (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
-        if (__any_sync(0xffffffffu, grow)) {  // each warp its half of the channels
-          tc::tc_after_sync();
-          const float f = grow ? ex2((top - m) * s2) : 1.f;
-          sum *= f;
-#pragma unroll
-          for (int c = 0; c < D / 2; c += 16) {
-            float o[16];
-            tc::tmem_ld16(o_lane + c, o);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= f;
-            tc::tmem_st16(o_lane + c, o);
-          }
-          tc::tmem_st_wait();
-        }
-      }
+      const float f = n > 0 && grow ? ex2((top - m) * s2) : 1.f;
       if (grow) top = m;
       const float ref = top == -INFINITY ? 0.f : top * s2;
+      // the product before has read the weights, and the output is complete
+      const auto before = [&] {
+        if (n == 0) return;
+        warp_wait(&s.o_full[i], (n - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
+        if (!__any_sync(0xffffffffu, grow)) return;
+        tc::tc_after_sync();  // each warp its half of the channels
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 16) {
+          float o[16];
+          tc::tmem_ld16(o_lane + c, o);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= f;
+          tc::tmem_st16(o_lane + c, o);
+        }
+        tc::tmem_st_wait();
+      };
+      if (kFine) before();
       float a0 = 0.f, a1 = 0.f;
+      uint4 w[kFine ? 1 : 8];
 #pragma unroll
       for (int c = 0; c < 64; c += 8) {
-        uint4 w;
-        uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
+        uint4& wc = w[kFine ? 0 : c / 8];
+        uint32_t* wp = reinterpret_cast<uint32_t*>(&wc);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           x[c + e] = ex2(fmaf(x[c + e], s2, -ref));
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
           a0 += x[c + e];
           a1 += x[c + e + 1];
         }
-        *reinterpret_cast<uint4*>(prow + ((c / 8) ^ (r & 7)) * 16) = w;
-        if (kFine) {  // what the rounding left
+        if (kFine) {  // and what the rounding left
+          *reinterpret_cast<uint4*>(prow + ((c / 8) ^ (r & 7)) * 16) = wc;
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             x[c + e] -= __uint_as_float(wp[e / 2] << 16);
@@ -408,14 +410,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
           }
         }
       }
-      sum += a0 + a1;
+      sum = fmaf(sum, f, a0 + a1);
+      if (!kFine) {
+        before();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(prow + (c ^ (r & 7)) * 16) = w[c];
+      }
       if (kFine) {
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
-          float w[16];
+          float l[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) w[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
-          tc::tmem_st16(s_lane + c / 2, w);
+          for (int e = 0; e < 32; e += 2) l[e / 2] = bf16_pair(x[c + e], x[c + e + 1]);
+          tc::tmem_st16(s_lane + c / 2, l);
         }
         tc::tmem_st_wait();
       }
