@@ -7,7 +7,7 @@
 // a part of its columns) for the elementwise work, which bounds these kernels
 // (with half as many warps of twice the columns: dk and dv 685 in place of 530,
 // dq 505 in place of 400, the forward 370 in place of 315), one thread that
-// loads tiles by TMA into a ring, and two that issue MMAs, each the products of
+// loads tiles by TMA into a ring, and two warps that issue MMAs, each the products of
 // one chain (scores, then what is made of them), so that one chain's waits (250
 // cycles each, even for a phase that is complete) lie beside the other's
 // products.  Tiles are 128 x 128: an MMA of 128 x 64 x 16 takes 50 cycles where
@@ -150,10 +150,11 @@ __device__ __forceinline__ void store_tile(const unsigned char* src, const CUten
 template <int D>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t id = tc::idesc(128, 128, 1);
+  const uint64_t da = tc::desc_sw128(a), db = tc::desc_sw128(b);
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
     const uint32_t o = s / 4 * 16384 + s % 4 * 32;
-    tc::mma_bf16_ss(d, tc::desc_sw128(a + o), tc::desc_sw128(b + o), id, s > 0);
+    tc::warp_mma_bf16_ss(d, tc::desc_at(da, o), tc::desc_at(db, o), id, s > 0);
   }
 }
 
@@ -163,9 +164,10 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
 template <int D>
 __device__ __forceinline__ void mma_mix(uint32_t d, uint32_t w, uint32_t x, bool acc) {
   constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+  const uint64_t dx = tc::desc_sw128_mn(x, 16384u);
 #pragma unroll
   for (int s = 0; s < 8; ++s)
-    tc::mma_bf16_ts(d, w + s / 2 * 32 + s % 2 * 8, tc::desc_sw128_mn(x + s * 2048, 16384u), id, acc || s > 0);
+    tc::warp_mma_bf16_ts(d, w + s / 2 * 32 + s % 2 * 8, tc::desc_at(dx, s * 2048), id, acc || s > 0);
 }
 
 // ---- forward -----------------------------------------------------------------
@@ -260,70 +262,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       }
     }
   } else if (warp >= kMmaWarp) {
-    if (lane == 0) {
-      const int i = warp - kMmaWarp;
-      const KeyRange mine(upto(q0 + 128 * i), upto(q0 + 128 * i + 128), W, S, 128);
-      const uint32_t base = tc::smem_u32(sm);
-      const uint32_t q = base + i * Cf::TILE, p = base + Cf::P + i * 32768;
-      const uint32_t sc = tmem + Cf::S_COL + i * 128, o = tmem + Cf::O_COL + i * 128;
-      int s_done = 0, p_done = 0;  // tiles whose scores, whose products are issued
-      const auto landed = [&](int load) {
-        tc::mbar_wait<false>(&s.full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab);
-        return base + Cf::RING + load % Cf::SLOTS * Cf::TILE;
-      };
-      const auto release = [&](int load, bool used) {  // only where the slot is loaded again: every commit is waited for
-        if (load + Cf::SLOTS >= loads) return;
-        if (used)
-          tc::mma_commit(&s.empty[load % Cf::SLOTS]);
-        else
-          tc::mbar_arrive(&s.empty[load % Cf::SLOTS]);
-      };
-      // S = q k^T of tile n, when the group has read the scores before
-      const auto scores = [&](int n) {
-        const bool has = mine.has(all.tile(n));
-        // a tile that this group skips is waited for as well, so that its slot's
-        // barrier counts one arrival of each chain per load
-        const uint32_t k = landed(load_of_k(n));
-        if (has) {
-          const int m = s_done++;
-          if (m > 0) tc::mbar_wait<false>(&s.s_free[i], (m - 1) & 1, a.err, tc::kErrTimeoutMma, ab);
-          tc::tc_after_sync();
-          mma_scores<D>(sc, q, k);
-          tc::mma_commit(&s.s_full[i]);
-        }
-        release(load_of_k(n), has);
-      };
-      // O += P v of tile n
-      const auto mix = [&](int n) {
-        const bool has = mine.has(all.tile(n));
-        const int load = load_of_v(n, all.count);
-        const uint32_t v = landed(load);
-        if (has) {
-          constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
-          const int m = p_done++;
-          tc::mbar_wait<false>(&s.p_full[i], m & 1, a.err, tc::kErrTimeoutMma, ab);
-          tc::tc_after_sync();
+    const int i = warp - kMmaWarp;
+    const KeyRange mine(upto(q0 + 128 * i), upto(q0 + 128 * i + 128), W, S, 128);
+    const uint32_t base = tc::smem_u32(sm);
+    const uint32_t q = base + i * Cf::TILE, p = base + Cf::P + i * 32768;
+    const uint32_t sc = tmem + Cf::S_COL + i * 128, o = tmem + Cf::O_COL + i * 128;
+    // (all lanes run every tile, also when a wait gave up and the later ones
+    // return at once: elect.sync wants the whole warp)
+    const auto wait = [&](uint64_t* bar, uint32_t parity, int code) { tc::mbar_wait<false>(bar, parity, a.err, code, ab); };
+    int s_done = 0, p_done = 0;  // tiles whose scores, whose products are issued
+    const auto landed = [&](int load) {
+      wait(&s.full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, tc::kErrTimeoutLoad);
+      return base + Cf::RING + load % Cf::SLOTS * Cf::TILE;
+    };
+    const auto release = [&](int load, bool used) {  // only where the slot is loaded again: every commit is waited for
+      if (load + Cf::SLOTS >= loads) return;
+      if (used)
+        tc::warp_mma_commit(&s.empty[load % Cf::SLOTS]);
+      else if (lane == 0)
+        tc::mbar_arrive(&s.empty[load % Cf::SLOTS]);
+    };
+    // S = q k^T of tile n, when the group has read the scores before
+    const auto scores = [&](int n) {
+      const bool has = mine.has(all.tile(n));
+      // a tile that this group skips is waited for as well, so that its slot's
+      // barrier counts one arrival of each chain per load
+      const uint32_t k = landed(load_of_k(n));
+      if (has) {
+        const int m = s_done++;
+        if (m > 0) wait(&s.s_free[i], (m - 1) & 1, tc::kErrTimeoutMma);
+        tc::tc_after_sync();
+        mma_scores<D>(sc, q, k);
+        tc::warp_mma_commit(&s.s_full[i]);
+      }
+      release(load_of_k(n), has);
+    };
+    // O += P v of tile n
+    const auto mix = [&](int n) {
+      const bool has = mine.has(all.tile(n));
+      const int load = load_of_v(n, all.count);
+      const uint32_t v = landed(load);
+      if (has) {
+        constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+        const int m = p_done++;
+        wait(&s.p_full[i], m & 1, tc::kErrTimeoutMma);
+        tc::tc_after_sync();
+        const uint64_t dp = tc::desc_sw128(p), dv = tc::desc_sw128_mn(v, 16384u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          tc::warp_mma_bf16_ss(o, tc::desc_at(dp, c / 4 * 16384 + c % 4 * 32), tc::desc_at(dv, c * 2048), id, m > 0 || c > 0);
+        if (kFine) {  // the low parts, over the scores
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            tc::mma_bf16_ss(o, tc::desc_sw128(p + c / 4 * 16384 + c % 4 * 32), tc::desc_sw128_mn(v + c * 2048, 16384u),
-                            id, m > 0 || c > 0);
-          if (kFine) {  // the low parts, over the scores
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              tc::mma_bf16_ts(o, sc + c / 4 * 64 + c % 4 * 8, tc::desc_sw128_mn(v + c * 2048, 16384u), id, 1);
-          }
-          tc::mma_commit(&s.o_full[i]);
+            tc::warp_mma_bf16_ts(o, sc + c / 4 * 64 + c % 4 * 8, tc::desc_at(dv, c * 2048), id, 1);
         }
-        release(load, has);
-      };
-      if (mine.count) tc::mbar_wait<false>(&s.q_full, 0, a.err, tc::kErrTimeoutLoad, ab);
-      scores(0);
-      for (int n = 0; n < all.count && !*ab; ++n) {
-        const bool more = n + 1 < all.count;
-        if (more && !kFine) scores(n + 1);
-        mix(n);
-        if (more && kFine) scores(n + 1);
+        tc::warp_mma_commit(&s.o_full[i]);
       }
+      release(load, has);
+    };
+    if (mine.count) wait(&s.q_full, 0, tc::kErrTimeoutLoad);
+    scores(0);
+    for (int n = 0; n < all.count; ++n) {
+      const bool more = n + 1 < all.count;
+      if (more && !kFine) scores(n + 1);
+      mix(n);
+      if (more && kFine) scores(n + 1);
     }
   } else {
     // query tile i, columns 64 g .. 64 g + 63 of row r
@@ -520,7 +523,9 @@ __device__ __forceinline__ void bwd_finish(uint32_t tmem) {
   if (threadIdx.x < 32) tc::tmem_dealloc(tmem, 512);
 }
 
-// The ring of a backward kernel as its MMA threads see it.
+// The ring of a backward item as its MMA warps see it.  (All lanes run every
+// tile, also when a wait gave up and the later ones return at once: elect.sync
+// wants the whole warp.)
 template <typename Cf>
 struct BwdRing {
   BwdBars& s;
@@ -534,7 +539,7 @@ struct BwdRing {
   }
   __device__ uint32_t at(int load) const { return base + Cf::RING + load % Cf::SLOTS * Cf::TILE; }  // landed before
   __device__ void release(int load) const {  // only where the slot is loaded again
-    if (load + Cf::SLOTS < loads) tc::mma_commit(&s.empty[load % Cf::SLOTS]);
+    if (load + Cf::SLOTS < loads) tc::warp_mma_commit(&s.empty[load % Cf::SLOTS]);
   }
   __device__ void ready(uint64_t* bar, int use) const {
     tc::mbar_wait<false>(bar, use & 1, err, tc::kErrTimeoutMma, &s.abort_flag);
@@ -600,34 +605,30 @@ __device__ __forceinline__ void dq_item(const BwdMaps& m, const SwaArgs& a, cons
       }
     }
   } else if (warp == kMmaWarp) {  // scores and dq
-    if (lane == 0) {
-      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
-      ring.ready(&s.own, 0);
-      mma_scores<D>(tmem, ring.base, ring.landed(0));
-      tc::mma_commit(&s.s_full[0]);
-      for (int n = 0; n < count && !*ab; ++n) {
-        if (n + 1 < count) {  // the next scores, while the groups work on dS
-          mma_scores<D>(tmem + (n + 1) % 2 * 128, ring.base, ring.landed(2 * n + 2));
-          tc::mma_commit(&s.s_full[(n + 1) % 2]);
-        }
-        ring.ready(&s.ds_ready[n % 2], n >> 1);
-        mma_mix<D>(tmem + DQ, tmem + n % 2 * 128, ring.at(2 * n), n > 0);
-        if (kFine) mma_mix<D>(tmem + DQ, tmem + n % 2 * 128 + 16, ring.at(2 * n), true);
-        ring.release(2 * n);
+    const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    ring.ready(&s.own, 0);
+    mma_scores<D>(tmem, ring.base, ring.landed(0));
+    tc::warp_mma_commit(&s.s_full[0]);
+    for (int n = 0; n < count; ++n) {
+      if (n + 1 < count) {  // the next scores, while the groups work on dS
+        mma_scores<D>(tmem + (n + 1) % 2 * 128, ring.base, ring.landed(2 * n + 2));
+        tc::warp_mma_commit(&s.s_full[(n + 1) % 2]);
       }
-      tc::mma_commit(&s.done);
+      ring.ready(&s.ds_ready[n % 2], n >> 1);
+      mma_mix<D>(tmem + DQ, tmem + n % 2 * 128, ring.at(2 * n), n > 0);
+      if (kFine) mma_mix<D>(tmem + DQ, tmem + n % 2 * 128 + 16, ring.at(2 * n), true);
+      ring.release(2 * n);
     }
+    tc::warp_mma_commit(&s.done);
   } else if (warp == kMmaWarp + 1) {  // dP, when the groups have read the one before
-    if (lane == 0) {
-      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
-      ring.ready(&s.own, 0);
-      for (int n = 0; n < count && !*ab; ++n) {
-        const uint32_t v = ring.landed(2 * n + 1);
-        if (n > 0) ring.ready(&s.ds_ready[(n - 1) % 2], (n - 1) >> 1);
-        mma_scores<D>(tmem + DP, ring.base + Cf::TILE, v);
-        tc::mma_commit(&s.dp_full);
-        ring.release(2 * n + 1);
-      }
+    const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    ring.ready(&s.own, 0);
+    for (int n = 0; n < count; ++n) {
+      const uint32_t v = ring.landed(2 * n + 1);
+      if (n > 0) ring.ready(&s.ds_ready[(n - 1) % 2], (n - 1) >> 1);
+      mma_scores<D>(tmem + DP, ring.base + Cf::TILE, v);
+      tc::warp_mma_commit(&s.dp_full);
+      ring.release(2 * n + 1);
     }
   } else {
     const int g = warp >> 2, t = q0 + (tid & 127);  // columns 32 g .. 32 g + 31
@@ -729,49 +730,46 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
       }
     }
   } else if (warp == kMmaWarp) {  // scores and dv
-    if (lane == 0) {
-      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
-      ring.ready(&s.own, 0);
-      const auto scores = [&](int n) {
-        const uint32_t q = ring.landed(2 * n);
-        if (n > 0) ring.ready(&s.s_free, n - 1);
-        mma_scores<D>(tmem, ring.base, q);
-        tc::mma_commit(&s.s_full[0]);
-        ring.release(2 * n);
-      };
-      scores(0);
-      for (int n = 0; n < count && !*ab; ++n) {
-        if (!kFine && n + 1 < count) scores(n + 1);  // while the groups work on p
-        const uint32_t g = ring.landed(2 * n + 1), p = ring.base + Cf::P;
-        ring.ready(&s.p_ready, n);
-        constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+    const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    ring.ready(&s.own, 0);
+    const auto scores = [&](int n) {
+      const uint32_t q = ring.landed(2 * n);
+      if (n > 0) ring.ready(&s.s_free, n - 1);
+      mma_scores<D>(tmem, ring.base, q);
+      tc::warp_mma_commit(&s.s_full[0]);
+      ring.release(2 * n);
+    };
+    scores(0);
+    for (int n = 0; n < count; ++n) {
+      if (!kFine && n + 1 < count) scores(n + 1);  // while the groups work on p
+      const uint32_t g = ring.landed(2 * n + 1), p = ring.base + Cf::P;
+      ring.ready(&s.p_ready, n);
+      constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
+      const uint64_t dp = tc::desc_sw128(p), dg = tc::desc_sw128_mn(g, 16384u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          tc::mma_bf16_ss(tmem + DV, tc::desc_sw128(p + i / 4 * 16384 + i % 4 * 32),
-                          tc::desc_sw128_mn(g + i * 2048, 16384u), id, n > 0 || i > 0);
-        if (kFine) mma_mix<D>(tmem + DV, tmem, g, true);  // p's low parts, over the scores
-        tc::mma_commit(&s.p_read);
-        ring.release(2 * n + 1);
-        if (kFine && n + 1 < count) scores(n + 1);
-      }
-      tc::mma_commit(&s.done);
+      for (int i = 0; i < 8; ++i)
+        tc::warp_mma_bf16_ss(tmem + DV, tc::desc_at(dp, i / 4 * 16384 + i % 4 * 32), tc::desc_at(dg, i * 2048), id,
+                        n > 0 || i > 0);
+      if (kFine) mma_mix<D>(tmem + DV, tmem, g, true);  // p's low parts, over the scores
+      tc::warp_mma_commit(&s.p_read);
+      ring.release(2 * n + 1);
+      if (kFine && n + 1 < count) scores(n + 1);
     }
+    tc::warp_mma_commit(&s.done);
   } else if (warp == kMmaWarp + 1) {  // dP and dk
-    if (lane == 0) {
-      const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
-      ring.ready(&s.own, 0);
-      for (int n = 0; n < count && !*ab; ++n) {
-        mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(2 * n + 1));
-        tc::mma_commit(&s.dp_full);
-        ring.release(2 * n + 1);
-        const uint32_t q = ring.landed(2 * n);
-        ring.ready(&s.ds_ready[0], n);
-        mma_mix<D>(tmem + DK, tmem + DP, q, n > 0);
-        if (kFine) mma_mix<D>(tmem + DK, tmem + DP + 16, q, true);
-        ring.release(2 * n);
-      }
-      tc::mma_commit(&s.done);
+    const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    ring.ready(&s.own, 0);
+    for (int n = 0; n < count; ++n) {
+      mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(2 * n + 1));
+      tc::warp_mma_commit(&s.dp_full);
+      ring.release(2 * n + 1);
+      const uint32_t q = ring.landed(2 * n);
+      ring.ready(&s.ds_ready[0], n);
+      mma_mix<D>(tmem + DK, tmem + DP, q, n > 0);
+      if (kFine) mma_mix<D>(tmem + DK, tmem + DP + 16, q, true);
+      ring.release(2 * n);
     }
+    tc::warp_mma_commit(&s.done);
   } else {
     const int g = warp >> 2, key = k0 + (tid & 127);  // columns 32 g .. 32 g + 31
     const uint32_t buf = tc::tmem_lane_addr(tmem, warp, g * 32);

@@ -59,6 +59,12 @@ __device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lbo) 
   return d;
 }
 
+// The descriptor `bytes` further on in shared memory (its 14 address bits do not
+// overflow), as one 32-bit addition.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+  return (d & 0xffffffff00000000ull) | (static_cast<uint32_t>(d) + (bytes >> 4));
+}
+
 // Instruction descriptor: dense, fp32 accumulator, A and B K-major.
 // fmt: 1 = bf16 (kind::f16), 2 = tf32 (kind::tf32).  OR in kMajorA / kMajorB
 // for an MN-major A / B operand.
@@ -262,18 +268,36 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, 
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] x B[smem desc]^T  (bf16; A holds two K elements per 32-bit column)
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
 // Arrive (once) on an mbarrier when all MMAs issued so far by this thread are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+
+// The same issued by a whole converged warp (one lane, always the same, is
+// elected): its operands then are values of the warp, which costs the issuing
+// loop less than one thread's.
+__device__ __forceinline__ void warp_mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p, e; elect.sync _|e, 0xffffffff; setp.ne.b32 p, %4, 0; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem desc]^T  (bf16; A holds two K elements per 32-bit column)
+__device__ __forceinline__ void warp_mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p, e; elect.sync _|e, 0xffffffff; setp.ne.b32 p, %4, 0; "
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_commit(uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred e; elect.sync _|e, 0xffffffff; "
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // ---- cluster -------------------------------------------------------------------
