@@ -532,14 +532,27 @@ struct BwdRing {
   uint32_t base;
   int loads;
   int* err;
-  __device__ uint32_t landed(int load) const {
-    tc::mbar_wait<false>(&s.full[load % Cf::SLOTS], (load / Cf::SLOTS) & 1, err, tc::kErrTimeoutLoad, &s.abort_flag);
+  struct At {  // every second load
+    int load, slot;
+    uint32_t parity;
+    __device__ explicit At(int first) : load(first), slot(first % Cf::SLOTS), parity(first / Cf::SLOTS & 1) {}
+    __device__ void next() {
+      load += 2;
+      slot += 2;
+      if (slot >= Cf::SLOTS) {
+        slot -= Cf::SLOTS;
+        parity ^= 1;
+      }
+    }
+  };
+  __device__ uint32_t tile(const At& x) const { return base + Cf::RING + x.slot * Cf::TILE; }
+  __device__ uint32_t landed(const At& x) const {
+    tc::mbar_wait<false>(&s.full[x.slot], x.parity, err, tc::kErrTimeoutLoad, &s.abort_flag);
     tc::tc_after_sync();
-    return base + Cf::RING + load % Cf::SLOTS * Cf::TILE;
+    return tile(x);
   }
-  __device__ uint32_t at(int load) const { return base + Cf::RING + load % Cf::SLOTS * Cf::TILE; }  // landed before
-  __device__ void release(int load) const {  // only where the slot is loaded again
-    if (load + Cf::SLOTS < loads) tc::warp_mma_commit(&s.empty[load % Cf::SLOTS]);
+  __device__ void release(const At& x) const {  // only where the slot is loaded again
+    if (x.load + Cf::SLOTS < loads) tc::warp_mma_commit(&s.empty[x.slot]);
   }
   __device__ void ready(uint64_t* bar, int use) const {
     tc::mbar_wait<false>(bar, use & 1, err, tc::kErrTimeoutMma, &s.abort_flag);
@@ -606,29 +619,31 @@ __device__ __forceinline__ void dq_item(const BwdMaps& m, const SwaArgs& a, cons
     }
   } else if (warp == kMmaWarp) {  // scores and dq
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    typename BwdRing<Cf>::At at(0), ahead(2);
     ring.ready(&s.own, 0);
-    mma_scores<D>(tmem, ring.base, ring.landed(0));
+    mma_scores<D>(tmem, ring.base, ring.landed(at));
     tc::warp_mma_commit(&s.s_full[0]);
-    for (int n = 0; n < count; ++n) {
+    for (int n = 0; n < count; ++n, at.next(), ahead.next()) {
       if (n + 1 < count) {  // the next scores, while the groups work on dS
-        mma_scores<D>(tmem + (n + 1) % 2 * 128, ring.base, ring.landed(2 * n + 2));
+        mma_scores<D>(tmem + (n + 1) % 2 * 128, ring.base, ring.landed(ahead));
         tc::warp_mma_commit(&s.s_full[(n + 1) % 2]);
       }
       ring.ready(&s.ds_ready[n % 2], n >> 1);
-      mma_mix<D>(tmem + DQ, tmem + n % 2 * 128, ring.at(2 * n), n > 0);
-      if (kFine) mma_mix<D>(tmem + DQ, tmem + n % 2 * 128 + 16, ring.at(2 * n), true);
-      ring.release(2 * n);
+      mma_mix<D>(tmem + DQ, tmem + n % 2 * 128, ring.tile(at), n > 0);
+      if (kFine) mma_mix<D>(tmem + DQ, tmem + n % 2 * 128 + 16, ring.tile(at), true);
+      ring.release(at);
     }
     tc::warp_mma_commit(&s.done);
   } else if (warp == kMmaWarp + 1) {  // dP, when the groups have read the one before
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    typename BwdRing<Cf>::At at(1);
     ring.ready(&s.own, 0);
-    for (int n = 0; n < count; ++n) {
-      const uint32_t v = ring.landed(2 * n + 1);
+    for (int n = 0; n < count; ++n, at.next()) {
+      const uint32_t v = ring.landed(at);
       if (n > 0) ring.ready(&s.ds_ready[(n - 1) % 2], (n - 1) >> 1);
       mma_scores<D>(tmem + DP, ring.base + Cf::TILE, v);
       tc::warp_mma_commit(&s.dp_full);
-      ring.release(2 * n + 1);
+      ring.release(at);
     }
   } else {
     const int g = warp >> 2, t = q0 + (tid & 127);  // columns 32 g .. 32 g + 31
@@ -731,43 +746,46 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
     }
   } else if (warp == kMmaWarp) {  // scores and dv
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    typename BwdRing<Cf>::At q_at(0), g_at(1);
     ring.ready(&s.own, 0);
     const auto scores = [&](int n) {
-      const uint32_t q = ring.landed(2 * n);
+      const uint32_t q = ring.landed(q_at);
       if (n > 0) ring.ready(&s.s_free, n - 1);
       mma_scores<D>(tmem, ring.base, q);
       tc::warp_mma_commit(&s.s_full[0]);
-      ring.release(2 * n);
+      ring.release(q_at);
+      q_at.next();
     };
     scores(0);
-    for (int n = 0; n < count; ++n) {
+    for (int n = 0; n < count; ++n, g_at.next()) {
       if (!kFine && n + 1 < count) scores(n + 1);  // while the groups work on p
-      const uint32_t g = ring.landed(2 * n + 1), p = ring.base + Cf::P;
+      const uint32_t g = ring.landed(g_at), p = ring.base + Cf::P;
       ring.ready(&s.p_ready, n);
       constexpr uint32_t id = tc::idesc(128, D, 1) | tc::kMajorB;
       const uint64_t dp = tc::desc_sw128(p), dg = tc::desc_sw128_mn(g, 16384u);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         tc::warp_mma_bf16_ss(tmem + DV, tc::desc_at(dp, i / 4 * 16384 + i % 4 * 32), tc::desc_at(dg, i * 2048), id,
-                        n > 0 || i > 0);
+                             n > 0 || i > 0);
       if (kFine) mma_mix<D>(tmem + DV, tmem, g, true);  // p's low parts, over the scores
       tc::warp_mma_commit(&s.p_read);
-      ring.release(2 * n + 1);
+      ring.release(g_at);
       if (kFine && n + 1 < count) scores(n + 1);
     }
     tc::warp_mma_commit(&s.done);
   } else if (warp == kMmaWarp + 1) {  // dP and dk
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
+    typename BwdRing<Cf>::At q_at(0), g_at(1);
     ring.ready(&s.own, 0);
-    for (int n = 0; n < count; ++n) {
-      mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(2 * n + 1));
+    for (int n = 0; n < count; ++n, q_at.next(), g_at.next()) {
+      mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(g_at));
       tc::warp_mma_commit(&s.dp_full);
-      ring.release(2 * n + 1);
-      const uint32_t q = ring.landed(2 * n);
+      ring.release(g_at);
+      const uint32_t q = ring.landed(q_at);
       ring.ready(&s.ds_ready[0], n);
       mma_mix<D>(tmem + DK, tmem + DP, q, n > 0);
       if (kFine) mma_mix<D>(tmem + DK, tmem + DP + 16, q, true);
-      ring.release(2 * n);
+      ring.release(q_at);
     }
     tc::warp_mma_commit(&s.done);
   } else {
@@ -777,12 +795,14 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
     // this key's row of the weights, the group's 32 columns: 16-byte chunk c of a
     // block of 64 at (c ^ (row & 7)) * 16
     unsigned char* prow = sm + Cf::P + g / 2 * 16384 + (tid & 127) * 128;
-    for (int n = 0; n < count; ++n) {
-      const int q0 = (qt0 + n % per) * 128, slot = 2 * n % Cf::SLOTS;
+    typename BwdRing<Cf>::At at(0);
+    for (int n = 0, i = 0; n < count; ++n, at.next()) {
+      const int q0 = (qt0 + i) * 128;  // query tile i of this head
+      if (++i == per) i = 0;
       const float4* rows = reinterpret_cast<const float4*>(sm + Cf::ROWS + n % 2 * 1024) + g * 8;
       // the scores' commit follows the arrival of q and its rows, but only this
       // wait lets this thread read what the copy wrote
-      if (!warp_wait(&s.full[slot], (2 * n / Cf::SLOTS) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+      if (!warp_wait(&s.full[at.slot], at.parity, a.err, tc::kErrTimeoutLoad, ab)) break;
       if (!warp_wait(&s.s_full[0], n & 1, a.err, tc::kErrTimeoutMma, ab)) break;
       tc::tc_after_sync();
       float x[32], dp[32];
