@@ -18,7 +18,10 @@
 // (prod f, h) pairs combine through shared memory and the CTAs' through
 // distributed shared memory, and the thread then adds its start state's part,
 // from registers.  The chain along the sequence is only ceil(T / 64C) cluster
-// exchanges long.
+// exchanges long.  B1 T16384 D2048 bf16, with the states saved: forward 118 us
+// (285 MB, 2.4 TB/s), backward 186 us (487 MB, 2.6 TB/s); one step of 256 x 2048
+// 7.2 us.  What bounds them is the issue of about 40 and 70 instructions per
+// pair of channels, a fifth of them on the special function unit.
 //
 // Accuracy: the state's error builds up over 1 / (1 - f) steps, so f must not
 // carry a bias.  With L = log2 f = n + r, |r| <= 1/2, and q = 2^r - 1 by a

@@ -7,34 +7,41 @@
 // a part of its columns) for the elementwise work, which bounds these kernels
 // (with half as many warps of twice the columns: dk and dv 685 in place of 530,
 // dq 505 in place of 400, the forward 370 in place of 315), one thread that
-// loads tiles by TMA into a ring, and two warps that issue MMAs, each the products of
-// one chain (scores, then what is made of them), so that one chain's waits (250
-// cycles each, even for a phase that is complete) lie beside the other's
-// products.  Tiles are 128 x 128: an MMA of 128 x 64 x 16 takes 50 cycles where
-// one of 128 x 128 x 16 takes 68.  B operands of the second products (v, k, dO,
-// q) are read MN-major from the same shared-memory tile that the score product
-// reads K-major, so no tile is stored twice or transposed.
+// loads tiles by TMA into a ring, and two warps that issue MMAs, each the
+// products of one chain (scores, then what is made of them), so that one chain's
+// waits lie beside the other's products.  A whole warp issues, one lane elected:
+// from a single thread, whose descriptors are no values of the warp, eight MMAs
+// take up to 1,000 cycles to issue (backward 992 in place of 909). Tiles are 128
+// x 128: an MMA of 128 x 64 x 16 takes 50 cycles where one of 128 x 128 x 16
+// takes 68.  B operands of the second products (v, k, dO, q) are read MN-major
+// from the same shared-memory tile that the score product reads K-major, so no
+// tile is stored twice or transposed.
 //
-// Forward: 315, 0.82 PFLOP/s over the visible pairs.  256 queries of one head
+// Forward: 293, 0.88 PFLOP/s over the visible pairs.  256 queries of one head
 // per CTA, a group to each 128.  Scores are read into registers at once and
 // their TMEM columns given back for the next tile's, p goes to shared memory as
 // the next product's A operand; per tile pair 32 MMAs (2,200 cycles) stand
-// against 2,050 cycles of the hardware exponential.  With p over the scores in
-// TMEM, where a group waits for both products between two tiles, it took 410.
-// The output stays in TMEM and is rescaled only when a row's maximum has grown
-// by more than 2^8 over the one its sums refer to (then p <= 2^8, still exact
-// enough in bf16, whose precision does not depend on the size).
+// against 2,050 cycles of the hardware exponential, and 384 KB go through shared
+// memory (3,070 cycles at 128 bytes), which is what bounds the 3,600 cycles that
+// a pair takes.  The weights are made in registers before the wait for the
+// product that still reads the last ones (319 where they follow it).  With p
+// over the scores in TMEM, where a group waits for both products between two
+// tiles, it took 410. The output stays in TMEM and is rescaled only when a row's
+// maximum has grown by more than 2^8 over the one its sums refer to (then p <=
+// 2^8, still exact enough in bf16, whose precision does not depend on the size).
 //
-// Backward: 930, 0.97 PFLOP/s over the visible pairs' seven products.  p
-// is recomputed from the saved lse.  dk, dv: 128 keys per CTA (rows are keys:
-// S^T = k q^T, dP^T = v dO^T), 128 queries at a time; dv += P^T dO, dk += dS^T q.
-// dq: 128 queries per CTA; dq += dS k.  The groups take the columns of each tile
-// in parts; p is formed while dP is still being multiplied.  dS goes over dP
-// (dq: over the scores, of which it has two buffers) in TMEM; dkv's p goes to
-// shared memory, so that the next scores need not wait for dv.  (64-column
-// tiles, two at a time, a group to each: dk and dv 880, dq 750.)  Seven products
-// in place of the five of one joint pass, but no atomics and no fp32 copy of
-// dq: every sum has one order.
+// Backward: 855, 1.05 PFLOP/s over the visible pairs' seven products; bound by
+// each tile's chain of waits, exponential and conversions (2,600 cycles for dq,
+// 3,600 for dk, dv, against 1,750 and 2,500 of shared-memory traffic), and by 5
+// us of start and end of each CTA.  p is recomputed from the saved lse.  dk, dv:
+// 128 keys per CTA (rows are keys: S^T = k q^T, dP^T = v dO^T), 128 queries at a
+// time; dv += P^T dO, dk += dS^T q. dq: 128 queries per CTA; dq += dS k.  The
+// groups take the columns of each tile in parts; p is formed while dP is still
+// being multiplied.  dS goes over dP (dq: over the scores, of which it has two
+// buffers) in TMEM; dkv's p goes to shared memory, so that the next scores need
+// not wait for dv.  (64-column tiles, two at a time, a group to each: dk and dv
+// 880, dq 750.)  Seven products in place of the five of one joint pass, but no
+// atomics and no fp32 copy of dq: every sum has one order.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 #include "kd_tc.cuh"

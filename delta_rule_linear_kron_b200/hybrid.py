@@ -375,7 +375,7 @@ def make_rotary_function():
 
     class RotaryFunction(torch.autograd.Function):
         """autograd wrapper of rotary_fwd / rotary_bwd.  apply(q, k, freqs, pos,
-        interleaved, scale) -> (q, k); q and k are not changed."""
+        interleaved, scale) -> (q, k); q and k are not changed, k may be None."""
 
         @staticmethod
         def forward(ctx, q, k, freqs, pos=None, interleaved=False, scale=1.0):
@@ -387,7 +387,7 @@ def make_rotary_function():
         @once_differentiable
         def backward(ctx, dq, dk):
             freqs, pos = ctx.saved_tensors
-            dq, dk = rotary_bwd(dq.contiguous(), dk.contiguous(), freqs, pos, **ctx.how)
+            dq, dk = rotary_bwd(dq.contiguous(), None if dk is None else dk.contiguous(), freqs, pos, **ctx.how)
             return dq, dk, None, None, None, None
 
     return RotaryFunction

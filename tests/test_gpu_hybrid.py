@@ -112,6 +112,15 @@ def test_rotary_default_positions_and_one_token_form():
     assert torch.equal(one[0], a[0][:, 4]) and torch.equal(one[1], a[1][:, 4])
 
 
+def test_rotary_autograd_of_queries_alone():
+    q = torch.randn(1, 9, 2, 32, device="cuda", requires_grad=True)
+    freqs, _ = kd.rotary_freqs(32)
+    y, none = kd.RotaryFunction.apply(q, None, freqs)
+    g = torch.randn_like(y)
+    assert none is None
+    assert torch.equal(torch.autograd.grad(y, q, g)[0], kd.rotary_bwd(g, None, freqs)[0])
+
+
 def test_rotary_autograd():
     q, k = (torch.randn(1, 6, 2, 32, device="cuda", requires_grad=True) for _ in range(2))
     f, s = kd.rotary_freqs(16, scaling="yarn", factor=4.0, trained_len=64)
