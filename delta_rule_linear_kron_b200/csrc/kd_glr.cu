@@ -485,12 +485,21 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
   }
 }
 
+// 32 channels x 8 shares of the rows; each share in order, then the shares.
 __global__ void __launch_bounds__(256) glr_dalog_kernel(const float* __restrict__ part, int rows, int D,
                                                         float* __restrict__ da_log) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= D) return;
+  __shared__ float share[8][32];
+  const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float t = 0.f;
-  for (int r = 0; r < rows; ++r) t += part[(size_t)r * D + c];
+  if (c < D) {
+#pragma unroll 4
+    for (int r = y; r < rows; r += 8) t += part[(size_t)r * D + c];
+  }
+  share[y][lane] = t;
+  __syncthreads();
+  if (y || c >= D) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) t += share[k][lane];
   da_log[c] = t;
 }
 
@@ -579,7 +588,7 @@ cudaError_t glr_bwd_t(const GlrArgs& a, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   prof_begin(st, "glr_dalog");
-  glr_dalog_kernel<<<(a.D + 255) / 256, 256, 0, st>>>(a.part, a.B * C, a.D, a.da_log);
+  glr_dalog_kernel<<<(a.D + 31) / 32, 256, 0, st>>>(a.part, a.B * C, a.D, a.da_log);
   prof_end(st);
   return cudaGetLastError();
 }
