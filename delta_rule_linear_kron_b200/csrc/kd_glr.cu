@@ -18,10 +18,11 @@
 // (prod f, h) pairs combine through shared memory and the CTAs' through
 // distributed shared memory, and the thread then adds its start state's part,
 // from registers.  The chain along the sequence is only ceil(T / 64C) cluster
-// exchanges long.  B1 T16384 D2048 bf16, with the states saved: forward 118 us
-// (285 MB, 2.4 TB/s), backward 186 us (487 MB, 2.6 TB/s); one step of 256 x 2048
-// 7.2 us.  What bounds them is the issue of about 40 and 70 instructions per
-// pair of channels, a fifth of them on the special function unit.
+// exchanges long.  B1 T16384 D2048 bf16, with the states saved: forward 113 us
+// (285 MB, 2.5 TB/s), backward 186 us (487 MB, 2.6 TB/s); one step of 256 x 2048
+// 7.2 us.  What bounds them is the issue of 115 and 186 instructions per pair of
+// channels and token (54 and 52% of the issue slots, 16 warps per SM; 8 of them
+// on the special function unit, 30 and 18%).
 //
 // Accuracy: the state's error builds up over 1 / (1 - f) steps, so f must not
 // carry a bias.  With L = log2 f = n + r, |r| <= 1/2, and q = 2^r - 1 by a
@@ -265,14 +266,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
   __syncthreads();
   if (C > 1) tc::cluster_sync();  // every CTA of the cluster has started
   const size_t base = (size_t)b * T_ * D + c;
+  // Tokens of this thread in chunk n.  (Asked for again where the outputs are
+  // stored, as their address is: kept over the step it costs 4%.)
+  const auto tokens = [&](int n) {
+    const long long left = T_ - ((long long)n * kChunk + warp * kTok);
+    return !live || left <= 0 ? 0 : left < kTok ? (int)left : kTok;
+  };
   for (int s = 0; s < steps; ++s) {
     const int n = s * C + rank, par = s & 1;
-    const long long t0 = (long long)n * kChunk + warp * kTok, left = T_ - t0;
-    const int k = !live || left <= 0 ? 0 : left < kTok ? (int)left : kTok;  // tokens of this thread
     unsigned char* st = sm + par * Cf::STAGE;
     const int own = warp * kTok * 32 + lane;  // this thread's first word of a tile
     if (n < NC) tc::mbar_wait<false>(&full[par], (s >> 1) & 1, err, tc::kErrTimeoutLoad, &abort_flag);
-    if (k < kTok) neutral_from<T, 3>(k, st, own);
+    if (const int k = tokens(n); k < kTok) neutral_from<T, 3>(k, st, own);
     const V *xs = reinterpret_cast<const V*>(st) + own, *is = reinterpret_cast<const V*>(st + Cf::TILE) + own;
     const V* fs = reinterpret_cast<const V*>(st + 2 * Cf::TILE) + own;
     Run r[kTok], run = {pk(1.f), pk(0.f)};
@@ -295,8 +300,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
     const Run all = then(pre, run);  // in the last warp: the whole chunk
     F2 mine = carry;  // state at the start of this CTA's chunk
     if (C > 1) {
-      // warp w hands the chunk's run to CTA w; the buffer's readers of two steps
-      // ago are through: their CTA's runs of the step before have arrived here
+      // the last warp hands the chunk's run to every CTA; the buffer's readers of
+      // two steps ago are through: their CTA's runs of the step before have arrived here
       if (warp == kWarps - 1)
         for (int q = 0; q < C; ++q) send(&cruns[par][rank][lane], &runs_in[par], q, all);
       tc::mbar_wait<true>(&runs_in[par], (s >> 1) & 1, err, tc::kErrTimeoutCluster, &abort_flag);
@@ -313,7 +318,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
     }
     const F2 h = fma2(pre.f, mine, pre.h);
     if (states && warp == 0 && live && n < NC) *reinterpret_cast<F2*>(states + ((size_t)b * NC + n) * D + c) = mine;
-    T* o = out + base + (size_t)t0 * D;
+    const int k = tokens(s * C + rank);
+    T* o = out + base + ((size_t)(s * C + rank) * kChunk + warp * kTok) * D;
 #pragma unroll
     for (int j = 0; j < kTok; ++j)
       if (j < k) __stcs(reinterpret_cast<V*>(o + (size_t)j * D), P::of(fma2(r[j].f, h, r[j].h)));
