@@ -1111,7 +1111,7 @@ int kron_delta_swa_fwd(const void* q, const void* k, const void* v, void* out, f
   KD_TRY(device_info(&di));
   a.err = di.err; a.sms = di.sms;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return launched(kd::swa_tc_supported(d, dtype) ? kd::launch_swa_fwd_tc(a, st) : kd::launch_swa_fwd_simt(a, st),
+  return launched(kd::swa_tc_supported(dtype) ? kd::launch_swa_fwd_tc(a, st) : kd::launch_swa_fwd_simt(a, st),
                   "swa forward launch");
 }
 
@@ -1148,7 +1148,7 @@ int kron_delta_swa_bwd(const void* q, const void* k, const void* v, const void* 
   KD_TRY(device_info(&di));
   a.err = di.err; a.sms = di.sms;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return launched(kd::swa_tc_supported(d, dtype) ? kd::launch_swa_bwd_tc(a, st) : kd::launch_swa_bwd_simt(a, st),
+  return launched(kd::swa_tc_supported(dtype) ? kd::launch_swa_bwd_tc(a, st) : kd::launch_swa_bwd_simt(a, st),
                   "swa backward launch");
 }
 

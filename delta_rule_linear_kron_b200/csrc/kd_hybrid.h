@@ -53,7 +53,7 @@ struct SwaBwdLayout {
 constexpr int kSwaPiece = 2048;
 SwaBwdLayout swa_bwd_layout(int B, int T, int H, int Hk, int d, int window, int sinks);
 
-bool swa_tc_supported(int d, int dtype);
+bool swa_tc_supported(int dtype);
 cudaError_t launch_swa_fwd_simt(const SwaArgs& a, cudaStream_t st);
 cudaError_t launch_swa_bwd_simt(const SwaArgs& a, cudaStream_t st);
 cudaError_t launch_swa_fwd_tc(const SwaArgs& a, cudaStream_t st);

@@ -1,6 +1,6 @@
 // kd_swa.cu -- sliding-window attention with first tokens kept, on CUDA cores
-// in fp32 (fp32 tensors, and bf16 with d = 32), and the passes around the
-// products that the tensor-core path (kd_swa_tc.cu) shares.
+// for fp32 tensors, and the passes around the products that the tensor-core
+// path for bf16 (kd_swa_tc.cu) shares.
 //
 // Query t sees key j when j <= t and (t - j < W or j < S).
 //   forward   x = scale q k^T over the visible keys, one pass with the running
@@ -10,12 +10,10 @@
 //
 // 64 queries x 64 keys at a time from shared memory, 256 threads with 4 x 4
 // tiles of the products; bound by shared-memory loads and fp32 FMA.  B2 T4096 H8
-// window 512 fp32: forward 0.74, 0.39, 0.24 ms and backward 2.2, 1.08, 0.63 ms
-// for d = 128, 64, 32 (22 and 26 TFLOP/s at d = 128); bf16 with d = 32 the same
-// (the tensor cores want d = 64 at least for their 128-byte rows; there they
-// are 3 to 13 times as fast, at 200 tokens 2).  Tiles with no visible pair are
-// not visited.  The gradient kernels recompute p
-// from lse: one per key tile for dk, dv and one per query tile for dq, so that
+// window 512: forward 0.74, 0.39, 0.24 ms and backward 2.2, 1.08, 0.63 ms for
+// d = 128, 64, 32 (22 and 26 TFLOP/s at d = 128).  Tiles with no visible pair
+// are not visited.  The gradients recompute p from lse, dk and dv by key tile
+// and dq by query tile, so that
 // every sum has a fixed order and needs no atomics.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
@@ -39,15 +37,13 @@ __device__ __forceinline__ bool single_key(int t, int W, int S) { return t == 0 
 
 // Rows t0 .. t0 + 63 of head h of a [B,T,H,D] tensor into [64][D + 4] fp32;
 // rows at or behind T become zero.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int t0, int T_, int H, int h, size_t b) {
-  constexpr int E = 16 / sizeof(T);
-  for (int i = threadIdx.x; i < kB * (D / E); i += kThreads) {
-    const int r = i / (D / E), c = (i % (D / E)) * E, t = t0 + r;
-    Pack<T, E> v;
-    if (t < T_) v = *reinterpret_cast<const Pack<T, E>*>(src + ((b * T_ + t) * (size_t)H + h) * D + c);
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[r * (D + 4) + c + e] = t < T_ ? to_f(v.x[e]) : 0.f;
+template <int D>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int t0, int T_, int H, int h, size_t b) {
+  for (int i = threadIdx.x; i < kB * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4, t = t0 + r;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < T_) v = *reinterpret_cast<const float4*>(src + ((b * T_ + t) * (size_t)H + h) * D + c);
+    *reinterpret_cast<float4*>(dst + r * (D + 4) + c) = v;
   }
 }
 
@@ -110,16 +106,16 @@ __device__ __forceinline__ void mix_tile(const float* Wt, const float* X, int ra
   }
 }
 
-// Row of this thread's columns, rounded to T.
-template <typename T, int D>
-__device__ __forceinline__ void store_cols(T* row, int tx, const float (&v)[D / 16]) {
+// This thread's columns of a row.
+template <int D>
+__device__ __forceinline__ void store_cols(float* row, int tx, const float (&v)[D / 16]) {
   using C = Cols<D>;
 #pragma unroll
   for (int n = 0; n < C::N; n += C::E) {
     float p[C::E];
 #pragma unroll
     for (int e = 0; e < C::E; ++e) p[e] = v[n + e];
-    store_row<T, C::E>(row + C::at(tx, n), p);
+    store_row<float, C::E>(row + C::at(tx, n), p);
   }
 }
 
@@ -143,7 +139,7 @@ struct KeyTiles {
   __device__ int tile(int i) const { return i < first ? i : band + i - first; }
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
   extern __shared__ float sm[];
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *Pt = V + kB * (D + 4);
@@ -151,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
   const int q0 = blockIdx.x * kB, h = blockIdx.y, hk = h / (a.H / a.Hk);
   const size_t b = blockIdx.z;
   const int q1 = q0 + kB < a.T ? q0 + kB : a.T;
-  load_tile<T, D>(Q, static_cast<const T*>(a.q), q0, a.T, a.H, h, b);
+  load_tile<D>(Q, static_cast<const float*>(a.q), q0, a.T, a.H, h, b);
   float o[4][D / 16], top[4], sum[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -165,8 +161,8 @@ __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
   for (int n = 0; n < kt.count; ++n) {
     const int k0 = kt.tile(n) * kB;
     __syncthreads();
-    load_tile<T, D>(K, static_cast<const T*>(a.k), k0, a.T, a.Hk, hk, b);
-    load_tile<T, D>(V, static_cast<const T*>(a.v), k0, a.T, a.Hk, hk, b);
+    load_tile<D>(K, static_cast<const float*>(a.k), k0, a.T, a.Hk, hk, b);
+    load_tile<D>(V, static_cast<const float*>(a.v), k0, a.T, a.Hk, hk, b);
     __syncthreads();
     float x[4][4];
     dot_tile<D>(Q, K, ty, tx, x);
@@ -207,12 +203,7 @@ __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
     const float r = 1.f / l;
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) o[i][n] *= r;
-    store_cols<T, D>(static_cast<T*>(a.out) + row * D, tx, o[i]);
-    if (a.olo) {
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n) o[i][n] -= to_f(from_f<T>(o[i][n]));
-      store_cols<T, D>(static_cast<T*>(a.olo) + row * D, tx, o[i]);
-    }
+    store_cols<D>(static_cast<float*>(a.out) + row * D, tx, o[i]);
     if (tx == 0) a.lse[row] = (top[i] + log2f(l)) * 0.693147180559945f;
   }
 }
@@ -242,7 +233,7 @@ __device__ __forceinline__ void weights(float (&x)[4][4], float (&dp)[4][4], con
 // dk, dv of key tile `tile` from its band's queries, all query heads of key
 // head h0 / group (piece < 0); or of a tile of first tokens from piece `piece`
 // of the queries beyond its band, query head h0.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void dkv_item(const SwaArgs& a, const SwaBwdLayout& L, float* sm, int tile, int piece, int h0,
                                          size_t b, bool has_far) {
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *G = V + kB * (D + 4);
@@ -258,8 +249,8 @@ __device__ __forceinline__ void dkv_item(const SwaArgs& a, const SwaBwdLayout& L
     if (q_lo >= q_hi) return;  // the sum skips it too
   }
   const int hk = h0 / group;
-  load_tile<T, D>(K, static_cast<const T*>(a.k), k0, a.T, a.Hk, hk, b);
-  load_tile<T, D>(V, static_cast<const T*>(a.v), k0, a.T, a.Hk, hk, b);
+  load_tile<D>(K, static_cast<const float*>(a.k), k0, a.T, a.Hk, hk, b);
+  load_tile<D>(V, static_cast<const float*>(a.v), k0, a.T, a.Hk, hk, b);
   float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -270,8 +261,8 @@ __device__ __forceinline__ void dkv_item(const SwaArgs& a, const SwaBwdLayout& L
     const float* gd = floats(a.ws, L.delta) + (b * a.H + h) * L.Tp;
     for (int q0 = q_lo / kB * kB; q0 < q_hi; q0 += kB) {
       __syncthreads();
-      load_tile<T, D>(Q, static_cast<const T*>(a.q), q0, a.T, a.H, h, b);
-      load_tile<T, D>(G, static_cast<const T*>(a.dO), q0, a.T, a.H, h, b);
+      load_tile<D>(Q, static_cast<const float*>(a.q), q0, a.T, a.H, h, b);
+      load_tile<D>(G, static_cast<const float*>(a.dO), q0, a.T, a.H, h, b);
       if (threadIdx.x < kB) {
         // queries outside [q_lo, q_hi) belong to another item: p = 0
         const int t = q0 + threadIdx.x;
@@ -306,25 +297,25 @@ __device__ __forceinline__ void dkv_item(const SwaArgs& a, const SwaBwdLayout& L
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) dk[i][n] *= a.scale;
     if (pk) {
-      store_cols<float, D>(pk, tx, dk[i]);
-      store_cols<float, D>(pv, tx, dv[i]);
+      store_cols<D>(pk, tx, dk[i]);
+      store_cols<D>(pv, tx, dv[i]);
     } else {
-      store_cols<T, D>(static_cast<T*>(a.dk) + row, tx, dk[i]);
-      store_cols<T, D>(static_cast<T*>(a.dv) + row, tx, dv[i]);
+      store_cols<D>(static_cast<float*>(a.dk) + row, tx, dk[i]);
+      store_cols<D>(static_cast<float*>(a.dv) + row, tx, dv[i]);
     }
   }
 }
 
 // dq of query tile `tile`, head h.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void dq_item(const SwaArgs& a, const SwaBwdLayout& L, float* sm, int tile, int h, size_t b) {
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *G = V + kB * (D + 4);
   float *Dt = G + kB * (D + 4), *lse2 = Dt + kB * kPitch, *delta = lse2 + kB;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int q0 = tile * kB, hk = h / (a.H / a.Hk);
   const int q1 = q0 + kB < a.T ? q0 + kB : a.T;
-  load_tile<T, D>(Q, static_cast<const T*>(a.q), q0, a.T, a.H, h, b);
-  load_tile<T, D>(G, static_cast<const T*>(a.dO), q0, a.T, a.H, h, b);
+  load_tile<D>(Q, static_cast<const float*>(a.q), q0, a.T, a.H, h, b);
+  load_tile<D>(G, static_cast<const float*>(a.dO), q0, a.T, a.H, h, b);
   if (threadIdx.x < kB) {
     const size_t at = (b * a.H + h) * L.Tp + q0 + threadIdx.x;
     lse2[threadIdx.x] = floats(a.ws, L.lse2)[at];
@@ -339,8 +330,8 @@ __device__ __forceinline__ void dq_item(const SwaArgs& a, const SwaBwdLayout& L,
   for (int n = 0; n < kt.count; ++n) {
     const int k0 = kt.tile(n) * kB;
     __syncthreads();
-    load_tile<T, D>(K, static_cast<const T*>(a.k), k0, a.T, a.Hk, hk, b);
-    load_tile<T, D>(V, static_cast<const T*>(a.v), k0, a.T, a.Hk, hk, b);
+    load_tile<D>(K, static_cast<const float*>(a.k), k0, a.T, a.Hk, hk, b);
+    load_tile<D>(V, static_cast<const float*>(a.v), k0, a.T, a.Hk, hk, b);
     __syncthreads();
     float x[4][4], dp[4][4];
     dot_tile<D>(Q, K, ty, tx, x);
@@ -356,31 +347,31 @@ __device__ __forceinline__ void dq_item(const SwaArgs& a, const SwaBwdLayout& L,
     const size_t row = ((b * a.T + t) * (size_t)a.H + h) * D;
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) dq[i][n] *= a.scale;
-    store_cols<T, D>(static_cast<T*>(a.dq) + row, tx, dq[i]);
+    store_cols<D>(static_cast<float*>(a.dq) + row, tx, dq[i]);
   }
 }
 
 // One launch for all of them: the key tiles, the first tokens' far pieces (far
 // items of `far_tiles` tiles) and the query tiles.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) swa_bwd_kernel(SwaArgs a, SwaBwdLayout L, int tiles, int far_tiles,
                                                            int key_items, int far_items) {
   extern __shared__ float sm[];
   int i = blockIdx.x;
   if (i < key_items) {
     const int kb = i / tiles;
-    dkv_item<T, D>(a, L, sm, i % tiles, -1, kb % a.Hk * (a.H / a.Hk), kb / a.Hk, far_tiles > 0);
+    dkv_item<D>(a, L, sm, i % tiles, -1, kb % a.Hk * (a.H / a.Hk), kb / a.Hk, far_tiles > 0);
     return;
   }
   i -= key_items;
   if (i < far_items) {
     const int per = L.pieces * far_tiles, hb = i / per;
-    dkv_item<T, D>(a, L, sm, i % far_tiles, i % per / far_tiles, hb % a.H, hb / a.H, true);
+    dkv_item<D>(a, L, sm, i % far_tiles, i % per / far_tiles, hb % a.H, hb / a.H, true);
     return;
   }
   i -= far_items;
   const int hb = i / tiles;
-  dq_item<T, D>(a, L, sm, i % tiles, hb % a.H, hb / a.H);
+  dq_item<D>(a, L, sm, i % tiles, hb % a.H, hb / a.H);
 }
 
 // HBM-bound: 39 us at T16384 H16 d128 bf16 (201 MB, 5.2 TB/s).
@@ -459,22 +450,22 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
   const size_t smem = (3 * kB * (D + 4) + kB * kPitch) * sizeof(float);
-  cudaError_t e = allow_smem(swa_fwd_kernel<T, D>, smem);
+  cudaError_t e = allow_smem(swa_fwd_kernel<D>, smem);
   if (e != cudaSuccess) return e;
   prof_begin(st, "swa_fwd_simt");
-  swa_fwd_kernel<T, D><<<dim3((a.T + kB - 1) / kB, a.H, a.B), kThreads, smem, st>>>(a);
+  swa_fwd_kernel<D><<<dim3((a.T + kB - 1) / kB, a.H, a.B), kThreads, smem, st>>>(a);
   prof_end(st);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   const SwaBwdLayout L = swa_bwd_layout(a.B, a.T, a.H, a.Hk, a.d, a.window, a.sinks);
   const size_t smem = (4 * kB * (D + 4) + 2 * kB * kPitch + 2 * kB) * sizeof(float);
-  cudaError_t e = allow_smem(swa_bwd_kernel<T, D>, smem);
+  cudaError_t e = allow_smem(swa_bwd_kernel<D>, smem);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
   if (e != cudaSuccess) return e;
   const int tiles = (a.T + kB - 1) / kB;
@@ -484,7 +475,7 @@ cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   const long long items = key_items + far_items + (long long)tiles * a.H * a.B;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   prof_begin(st, "swa_bwd_simt");
-  swa_bwd_kernel<T, D><<<(unsigned)items, kThreads, smem, st>>>(a, L, tiles, far_tiles, (int)key_items, (int)far_items);
+  swa_bwd_kernel<D><<<(unsigned)items, kThreads, smem, st>>>(a, L, tiles, far_tiles, (int)key_items, (int)far_items);
   prof_end(st);
   e = cudaGetLastError();
   if (e == cudaSuccess && has_far) e = launch_swa_sink_sum(a, L, kB, st);
@@ -514,13 +505,11 @@ SwaBwdLayout swa_bwd_layout(int B, int T, int H, int Hk, int d, int window, int 
 }
 
 cudaError_t launch_swa_fwd_simt(const SwaArgs& a, cudaStream_t st) {
-  if (a.dtype == 1) return fwd_go<__nv_bfloat16, 32>(a, st);  // wider bf16 heads run on tensor cores
-  return a.d == 32 ? fwd_go<float, 32>(a, st) : a.d == 64 ? fwd_go<float, 64>(a, st) : fwd_go<float, 128>(a, st);
+  return a.d == 32 ? fwd_go<32>(a, st) : a.d == 64 ? fwd_go<64>(a, st) : fwd_go<128>(a, st);
 }
 
 cudaError_t launch_swa_bwd_simt(const SwaArgs& a, cudaStream_t st) {
-  if (a.dtype == 1) return bwd_go<__nv_bfloat16, 32>(a, st);
-  return a.d == 32 ? bwd_go<float, 32>(a, st) : a.d == 64 ? bwd_go<float, 64>(a, st) : bwd_go<float, 128>(a, st);
+  return a.d == 32 ? bwd_go<32>(a, st) : a.d == 64 ? bwd_go<64>(a, st) : bwd_go<128>(a, st);
 }
 
 template <typename T>

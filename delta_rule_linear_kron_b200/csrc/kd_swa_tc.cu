@@ -1,5 +1,8 @@
 // kd_swa_tc.cu -- sliding-window attention with first tokens kept, on tcgen05
-// (bf16, d = 64 and 128).  The formulas are in kd_swa.cu.
+// (bf16).  The formulas are in kd_swa.cu.  Kernels are made for d = 64 and 128;
+// d = 32 is d = 64 whose tiles' second half lies outside the tensors: loaded as
+// zeros, never stored (B2 T4096 H8 window 512: forward 44 and backward 99 us;
+// on CUDA cores, which have no use for the zeros, 228 and 626).
 //
 // Times are at H16 Hk16 T16384 d128 window 2048, in us.
 //
@@ -881,18 +884,19 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
     const int c0 = g % 2 * (D / 2);
     const uint32_t lanes = tc::tmem_lane_addr(tmem, warp, (is_k ? DK : DV) + c0);
     const float f = is_k ? a.scale : 1.f;
-    const bool first = key < S && key < a.T && has_far;  // rows that other items add to: fp32 parts
+    const bool mine = key < a.T && c0 < a.d;
+    const bool first = key < S && mine && has_far;  // rows that other items add to: fp32 parts
     float* part = nullptr;
     if (first && far)
       part = reinterpret_cast<float*>(a.ws + L.part) +
-             (((((size_t)(is_k ? 0 : 1) * L.pieces + piece) * a.B + b) * a.H + h0) * S + key) * D + c0;
+             (((((size_t)(is_k ? 0 : 1) * L.pieces + piece) * a.B + b) * a.H + h0) * S + key) * a.d + c0;
     else if (first)
       part = reinterpret_cast<float*>(a.ws + L.band) +
-             ((((size_t)(is_k ? 0 : 1) * a.B + b) * a.Hk + hk) * S + key) * D + c0;
+             ((((size_t)(is_k ? 0 : 1) * a.B + b) * a.Hk + hk) * S + key) * a.d + c0;
     if (k0 < S && has_far) {  // the tile of the first tokens: row by row
       __nv_bfloat16* dst =
-          static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + (((size_t)b * a.T + key) * a.Hk + hk) * D + c0;
-      const bool plain = !far && !first && key < a.T;
+          static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dv) + (((size_t)b * a.T + key) * a.Hk + hk) * a.d + c0;
+      const bool plain = !far && !first && mine;
 #pragma unroll
       for (int c = 0; c < D / 2; c += 16) {
         float v[16];
@@ -968,11 +972,11 @@ template <int D, bool kFine>
 cudaError_t fwd_go(const SwaArgs& a, cudaStream_t st) {
   using Cf = FwdCfg<D>;
   CUtensorMap tq, tk, tv, to, tl;
-  if (!make_tmap_bthd(&to, a.out, 2, a.B, a.T, a.H, D, 64, true, 128) ||
-      !make_tmap_bthd(&tl, a.olo ? a.olo : a.out, 2, a.B, a.T, a.H, D, 64, true, 128) ||
-      !make_tmap_bthd(&tq, a.q, 2, a.B, a.T, a.H, D, 64, true, 128) ||
-      !make_tmap_bthd(&tk, a.k, 2, a.B, a.T, a.Hk, D, 64, true, 128) ||
-      !make_tmap_bthd(&tv, a.v, 2, a.B, a.T, a.Hk, D, 64, true, 128))
+  if (!make_tmap_bthd(&to, a.out, 2, a.B, a.T, a.H, a.d, 64, true, 128) ||
+      !make_tmap_bthd(&tl, a.olo ? a.olo : a.out, 2, a.B, a.T, a.H, a.d, 64, true, 128) ||
+      !make_tmap_bthd(&tq, a.q, 2, a.B, a.T, a.H, a.d, 64, true, 128) ||
+      !make_tmap_bthd(&tk, a.k, 2, a.B, a.T, a.Hk, a.d, 64, true, 128) ||
+      !make_tmap_bthd(&tv, a.v, 2, a.B, a.T, a.Hk, a.d, 64, true, 128))
     return cudaErrorInvalidValue;
   cudaError_t e = allow_smem(swa_fwd_tc_kernel<D, kFine>, Cf::BYTES);
   if (e != cudaSuccess) return e;
@@ -991,7 +995,7 @@ cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
   CUtensorMap* maps[7] = {&m.q, &m.g, &m.dq, &m.k, &m.v, &m.dk, &m.dv};
   const void* src[7] = {a.q, a.dO, a.dq, a.k, a.v, a.dk, a.dv};
   for (int i = 0; i < 7; ++i)
-    if (!make_tmap_bthd(maps[i], src[i], 2, a.B, a.T, i < 3 ? a.H : a.Hk, D, 64, true, 128)) return cudaErrorInvalidValue;
+    if (!make_tmap_bthd(maps[i], src[i], 2, a.B, a.T, i < 3 ? a.H : a.Hk, a.d, 64, true, 128)) return cudaErrorInvalidValue;
   cudaError_t e = allow_smem(swa_bwd_tc_kernel<D, kFine>, kBytes);
   if (e == cudaSuccess) e = launch_swa_delta(a, L, st);
   if (e != cudaSuccess) return e;
@@ -1010,14 +1014,14 @@ cudaError_t bwd_go(const SwaArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool swa_tc_supported(int d, int dtype) { return dtype == 1 && (d == 64 || d == 128); }
+bool swa_tc_supported(int dtype) { return dtype == 1; }
 cudaError_t launch_swa_fwd_tc(const SwaArgs& a, cudaStream_t st) {
-  if (fine(a)) return a.d == 64 ? fwd_go<64, true>(a, st) : fwd_go<128, true>(a, st);
-  return a.d == 64 ? fwd_go<64, false>(a, st) : fwd_go<128, false>(a, st);
+  if (fine(a)) return a.d <= 64 ? fwd_go<64, true>(a, st) : fwd_go<128, true>(a, st);
+  return a.d <= 64 ? fwd_go<64, false>(a, st) : fwd_go<128, false>(a, st);
 }
 cudaError_t launch_swa_bwd_tc(const SwaArgs& a, cudaStream_t st) {
-  if (fine(a)) return a.d == 64 ? bwd_go<64, true>(a, st) : bwd_go<128, true>(a, st);
-  return a.d == 64 ? bwd_go<64, false>(a, st) : bwd_go<128, false>(a, st);
+  if (fine(a)) return a.d <= 64 ? bwd_go<64, true>(a, st) : bwd_go<128, true>(a, st);
+  return a.d <= 64 ? bwd_go<64, false>(a, st) : bwd_go<128, false>(a, st);
 }
 
 }  // namespace kd

@@ -111,10 +111,12 @@ def _size(n):
     return n
 
 
+@functools.lru_cache(maxsize=1024)  # of its arguments alone; asked on every decode step
 def swa_workspace_size(kind, B, T, H, Hk, d, window, sinks, dtype) -> int:
     return _size(lib().kron_delta_swa_workspace_size(kind, B, T, H, Hk, d, window, sinks, dtype))
 
 
+@functools.lru_cache(maxsize=1024)
 def glr_workspace_size(kind, B, T, D, dtype) -> int:
     return _size(lib().kron_delta_glr_workspace_size(kind, B, T, D, dtype))
 

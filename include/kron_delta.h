@@ -553,10 +553,9 @@ KD_API size_t kron_delta_swa_workspace_size(int kind, int B, int T, int H, int H
  *         kron_delta_swa_workspace_size(KD_SWA_WS_SAVE, ...) bytes, 256-byte
  *         aligned (the rounding of the bf16 output, which the backward adds
  *         back; zero bytes for fp32), else NULL.
- * d in {32, 64, 128}.  bf16 with d = 64 or 128 runs on tensor cores, the
- * probabilities rounded to bf16 for their product with v (where min(window +
- * sinks, T) <= 256, to a sum of two bf16 numbers); other shapes run on CUDA
- * cores in fp32.
+ * d in {32, 64, 128}.  bf16 runs on tensor cores, the probabilities rounded to
+ * bf16 for their product with v (where min(window + sinks, T) <= 256, to a sum
+ * of two bf16 numbers); fp32 runs on CUDA cores in fp32.
  * Precondition not checked on the device: q, k, v finite, in the rows behind a
  * shorter sequence too (keys are read by tiles, and a hidden infinity or NaN
  * in k or v would meet a zero weight).  An output that overlaps an input or

@@ -7,7 +7,7 @@ Tolerances follow from the arithmetic.  A rounding to bf16 is off by at most
           the sine and cosine (sincospi's 2 ulp and the fraction's rounding):
           4 * 2^-22 of |x1| + |x2|, and the output's rounding.
   swa     oracle.hybrid.swa_bounds, where p and dS are rounded to bf16 before
-          their products on the tensor-core path (bf16, d = 64 and 128).
+          their products on the tensor-core path (bf16).
   glr     h is a sum of terms prod f * m i x.  e^{-|z|} carries the rounding of
           its argument (|z| 2^-24, twice with the hardware exponential's own),
           so l = log f is within (6 + 2 |z|) 2^-24 of itself, and f = e^l is
@@ -135,7 +135,7 @@ def test_rotary_autograd():
 
 
 def on_tensor_cores(dtype, d):
-    return dtype == "bf16" and d >= 64
+    return dtype == "bf16"
 
 
 def check_swa(B, T, H, Hk, d, window, sinks, dtype, seed=0, size=1.0, scale=None):
@@ -178,6 +178,14 @@ def test_swa_grouped_heads(dtype, d, B, H, Hk):
 def test_swa_sharp_scores(dtype, d):
     """Large scores: probabilities near one-hot, running maxima that move a lot."""
     check_swa(1, 200, 2, 1, d, 90, 2, dtype, seed=1, size=4.0)
+
+
+@pytest.mark.parametrize("B,T,H,Hk,window,sinks", [(2, 300, 4, 2, 299, 128), (1, 700, 3, 3, 500, 5), (2, 190, 8, 1, 70, 3),
+                                                   (1, 2300, 2, 1, 30, 5), (1, 2300, 2, 2, 400, 70)])
+def test_swa_heads_of_32(B, T, H, Hk, window, sinks):
+    """Half a tile's channels lie outside the tensors: nothing of them is read
+    or written (the neighbours in memory are other heads, checked too)."""
+    check_swa(B, T, H, Hk, 32, window, sinks, "bf16", seed=T + H)
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 32)])
