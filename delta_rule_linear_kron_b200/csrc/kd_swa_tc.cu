@@ -195,7 +195,7 @@ struct FwdCfg {
 };
 
 struct FwdBars {
-  uint64_t q_full, full[6], empty[6], s_full[2], s_free[2], p_full[2], o_full[2];
+  uint64_t q_full[2], full[6], empty[6], s_full[2], s_free[2], p_full[2], o_full[2];
   uint32_t tmem;
   int abort_flag;
 };
@@ -239,8 +239,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     tc::mbar_expect_tx(&s.full[slot], Cf::TILE);
     load_tile<D>(sm + Cf::RING + slot * Cf::TILE, is_k ? &tk : &tv, hk, all.tile(tile) * 128, b, &s.full[slot]);
   };
-  if (warp == kLoadWarp && lane == 0) {  // the first loads fly while the CTA sets up
-    tc::mbar_init(&s.q_full, 1);
+  const auto load_q = [&](int i) {
+    tc::mbar_expect_tx(&s.q_full[i], Cf::TILE);
+    load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &s.q_full[i]);
+  };
+  if (warp == kLoadWarp && lane == 0) {  // what the first scores want flies while the CTA sets up
+    tc::mbar_init(&s.q_full[0], 1);
+    tc::mbar_init(&s.q_full[1], 1);
     for (int i = 0; i < Cf::SLOTS; ++i) {
       tc::mbar_init(&s.full[i], 1);
       tc::mbar_init(&s.empty[i], 2);
@@ -253,10 +258,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
     }
     tc::mbar_init_fence();
     s.abort_flag = 0;
-    const int two = q0 + 128 < a.T ? 2 : 1;
-    tc::mbar_expect_tx(&s.q_full, two * Cf::TILE);
-    for (int i = 0; i < two; ++i) load_tile<D>(sm + i * Cf::TILE, &tq, h, q0 + 128 * i, b, &s.q_full);
-    for (int n = 0; n < Cf::SLOTS && n < loads; ++n) load(n);
+    load_q(0);
+    load(0);
   }
   if (warp == 0) tc::tmem_alloc(&s.tmem, 512);
   tc::tc_before_sync();
@@ -266,8 +269,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
 
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      for (int n = Cf::SLOTS; n < loads; ++n) {
-        if (!tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+      if (q0 + 128 < a.T) load_q(1);
+      for (int n = 1; n < loads; ++n) {
+        if (n >= Cf::SLOTS &&
+            !tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
         load(n);
       }
     }
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) swa_fwd_tc_kernel(
       }
       release(load, has);
     };
-    if (mine.count) wait(&s.q_full, 0, tc::kErrTimeoutLoad);
+    if (mine.count) wait(&s.q_full[i], 0, tc::kErrTimeoutLoad);
     scores(0);
     for (int n = 0; n < all.count; ++n) {
       const bool more = n + 1 < all.count;
@@ -490,7 +495,7 @@ struct BwdCfg {
 };
 
 struct BwdBars {
-  uint64_t own, full[5], empty[5], s_full[2], s_free, dp_full, p_ready, p_read, ds_ready[2], done;
+  uint64_t own[2], full[5], empty[5], s_full[2], s_free, dp_full, p_ready, p_read, ds_ready[2], done;
   uint32_t tmem;
   int abort_flag;
 };
@@ -500,8 +505,9 @@ static_assert(sizeof(BwdBars) <= 256, "barriers fit behind the tiles");
 template <typename F>
 __device__ __forceinline__ bool bwd_setup(unsigned char* sm, BwdBars& s, int chains, int* err, F first_loads) {
   if (!tiles_aligned(sm, err)) return false;
-  if (threadIdx.x == kLoadWarp * 32) {  // the first loads fly while the CTA sets up
-    tc::mbar_init(&s.own, 1);
+  if (threadIdx.x == kLoadWarp * 32) {  // what the first scores want flies while the CTA sets up
+    tc::mbar_init(&s.own[0], 1);
+    tc::mbar_init(&s.own[1], 1);
     for (int i = 0; i < 5; ++i) {
       tc::mbar_init(&s.full[i], 1);
       tc::mbar_init(&s.empty[i], chains);
@@ -611,26 +617,27 @@ __device__ __forceinline__ void dq_item(const BwdMaps& m, const SwaArgs& a, cons
     load_tile<D>(sm + Cf::RING + slot * Cf::TILE, n & 1 ? &m.v : &m.k, hk, keys.tile(n / 2) * 128, b, &s.full[slot]);
   };
   if (!bwd_setup(sm, s, 1, a.err, [&] {
-        tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
-        load_tile<D>(sm, &m.q, h, q0, b, &s.own);
+        tc::mbar_expect_tx(&s.own[0], Cf::TILE);
+        load_tile<D>(sm, &m.q, h, q0, b, &s.own[0]);
         load(0);
-        load_tile<D>(sm + Cf::TILE, &m.g, h, q0, b, &s.own);
-        for (int n = 1; n < Cf::SLOTS && n < 2 * count; ++n) load(n);
       }))
     return;
   const uint32_t tmem = s.tmem;
   volatile int* ab = &s.abort_flag;
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      for (int n = Cf::SLOTS; n < 2 * count; ++n) {
-        if (!tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+      tc::mbar_expect_tx(&s.own[1], Cf::TILE);
+      load_tile<D>(sm + Cf::TILE, &m.g, h, q0, b, &s.own[1]);
+      for (int n = 1; n < 2 * count; ++n) {
+        if (n >= Cf::SLOTS &&
+            !tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
         load(n);
       }
     }
   } else if (warp == kMmaWarp) {  // scores and dq
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
     typename BwdRing<Cf>::At at(0), ahead(2);
-    ring.ready(&s.own, 0);
+    ring.ready(&s.own[0], 0);
     mma_scores<D>(tmem, ring.base, ring.landed(at));
     tc::warp_mma_commit(&s.s_full[0]);
     for (int n = 0; n < count; ++n, at.next(), ahead.next()) {
@@ -647,7 +654,7 @@ __device__ __forceinline__ void dq_item(const BwdMaps& m, const SwaArgs& a, cons
   } else if (warp == kMmaWarp + 1) {  // dP, when the groups have read the one before
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
     typename BwdRing<Cf>::At at(1);
-    ring.ready(&s.own, 0);
+    ring.ready(&s.own[1], 0);
     for (int n = 0; n < count; ++n, at.next()) {
       const uint32_t v = ring.landed(at);
       if (n > 0) ring.ready(&s.ds_ready[(n - 1) % 2], (n - 1) >> 1);
@@ -738,26 +745,27 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
     }
   };
   if (!bwd_setup(sm, s, 2, a.err, [&] {
-        tc::mbar_expect_tx(&s.own, 2 * Cf::TILE);
-        load_tile<D>(sm, &m.k, hk, k0, b, &s.own);
+        tc::mbar_expect_tx(&s.own[0], Cf::TILE);
+        load_tile<D>(sm, &m.k, hk, k0, b, &s.own[0]);
         load(0);
-        load_tile<D>(sm + Cf::TILE, &m.v, hk, k0, b, &s.own);
-        for (int n = 1; n < Cf::SLOTS && n < 2 * count; ++n) load(n);
       }))
     return;
   const uint32_t tmem = s.tmem;
   volatile int* ab = &s.abort_flag;
   if (warp == kLoadWarp) {
     if (lane == 0) {
-      for (int n = Cf::SLOTS; n < 2 * count; ++n) {
-        if (!tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
+      tc::mbar_expect_tx(&s.own[1], Cf::TILE);
+      load_tile<D>(sm + Cf::TILE, &m.v, hk, k0, b, &s.own[1]);
+      for (int n = 1; n < 2 * count; ++n) {
+        if (n >= Cf::SLOTS &&
+            !tc::mbar_wait<false>(&s.empty[n % Cf::SLOTS], (n / Cf::SLOTS - 1) & 1, a.err, tc::kErrTimeoutLoad, ab)) break;
         load(n);
       }
     }
   } else if (warp == kMmaWarp) {  // scores and dv
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
     typename BwdRing<Cf>::At q_at(0), g_at(1);
-    ring.ready(&s.own, 0);
+    ring.ready(&s.own[0], 0);
     const auto scores = [&](int n) {
       const uint32_t q = ring.landed(q_at);
       if (n > 0) ring.ready(&s.s_free, n - 1);
@@ -786,7 +794,7 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
   } else if (warp == kMmaWarp + 1) {  // dP and dk
     const BwdRing<Cf> ring{s, tc::smem_u32(sm), 2 * count, a.err};
     typename BwdRing<Cf>::At q_at(0), g_at(1);
-    ring.ready(&s.own, 0);
+    ring.ready(&s.own[1], 0);
     for (int n = 0; n < count; ++n, q_at.next(), g_at.next()) {
       mma_scores<D>(tmem + DP, ring.base + Cf::TILE, ring.landed(g_at));
       tc::warp_mma_commit(&s.dp_full);
