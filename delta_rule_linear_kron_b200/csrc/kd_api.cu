@@ -1109,7 +1109,7 @@ int kron_delta_swa_fwd(const void* q, const void* k, const void* v, void* out, f
   a.dtype = dtype; a.scale = scale;
   DeviceInfo di;
   KD_TRY(device_info(&di));
-  a.err = di.err; a.sms = di.sms;
+  a.err = di.err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launched(kd::swa_tc_supported(dtype) ? kd::launch_swa_fwd_tc(a, st) : kd::launch_swa_fwd_simt(a, st),
                   "swa forward launch");
@@ -1146,7 +1146,7 @@ int kron_delta_swa_bwd(const void* q, const void* k, const void* v, const void* 
   a.dtype = dtype; a.scale = scale;
   DeviceInfo di;
   KD_TRY(device_info(&di));
-  a.err = di.err; a.sms = di.sms;
+  a.err = di.err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launched(kd::swa_tc_supported(dtype) ? kd::launch_swa_bwd_tc(a, st) : kd::launch_swa_bwd_simt(a, st),
                   "swa backward launch");

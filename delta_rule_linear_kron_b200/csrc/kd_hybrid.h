@@ -36,7 +36,6 @@ struct SwaArgs {
   const void* olo_in;
   char* ws;             // backward scratch (SwaBwdLayout)
   int* err = nullptr;   // the library's device error word
-  int sms = 0;
 };
 
 // Backward scratch.  lse2 and delta are [B][H][Tp] fp32 (Tp = T rounded up to
