@@ -13,8 +13,9 @@
 // serve all heads of a token, so a CTA takes whole tokens: it fills a table of
 // its tokens' rot/2 pairs in shared memory, then moves the heads' rows as
 // vectors, x threads to a row and y rows at a time.  16384 tokens of 16 + 4
-// heads of 128 bf16 (168 MB): 34.9 us, 4.8 TB/s; with two and four rows in
-// flight per thread 53 and 68 us (more registers, fewer CTAs).
+// heads of 128 bf16 (168 MB): 33 to 35 us, 5 TB/s; with two and four rows in
+// flight per thread 53 and 68 us (more registers, fewer CTAs), with a thread's
+// first row loaded ahead of the table 43.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 
