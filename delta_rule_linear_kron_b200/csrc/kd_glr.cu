@@ -57,6 +57,17 @@ __device__ __forceinline__ float rsq(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// fminf and fmaxf return the other operand for a NaN; these return the NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -99,7 +110,9 @@ struct Gates {
   F2 s, j;  // with kBack: sigma(-f~), and sigma(-i~) = 2^k sigma(i~) (1 - i would cancel)
 };
 
-// na2: -a log2 e.
+// na2: -a log2 e.  A NaN in zf or na2 makes f NaN, one in zi i: no bound below
+// may take it for a number, or a run that has diverged would go on as if its
+// gates were shut.
 template <bool kBack>
 __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   Gates g;
@@ -107,8 +120,18 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   const F2 e = pk(ex, ey);
   const F2 d = add2(e, pk(2.f));
   // sigma(i~) = 1 / (1 + 2^k); the bound (2e-37, 0 for every purpose) keeps the
-  // product of reciprocals below in range
-  const F2 k2 = pk(ex2(fminf(-kLog2e * zi.x, 122.f)), ex2(fminf(-kLog2e * zi.y, 122.f)));
+  // product of reciprocals below in range.  That product is f's too, which the
+  // forward may spoil with a NaN of i~ (h_t is NaN with i alone); the backward
+  // may not, since f_t carries the gradients of earlier tokens, so it keeps the
+  // NaN aside (k2n) and gives it to i.
+  F2 k2, k2n;
+  if (kBack) {
+    const float kx = ex2(-kLog2e * zi.x), ky = ex2(-kLog2e * zi.y);
+    k2 = pk(fminf(kx, 0x1p122f), fminf(ky, 0x1p122f));
+    k2n = pk(min_nan(kx, 0x1p122f), min_nan(ky, 0x1p122f));
+  } else {
+    k2 = pk(ex2(min_nan(-kLog2e * zi.x, 122.f)), ex2(min_nan(-kLog2e * zi.y, 122.f)));
+  }
   const F2 c = add2(k2, pk(1.f));
   // the reciprocals of 2 + e, 1 + 2^k (and 1 + e) from one of their product
   F2 dc = mul2(d, c), one = add2(e, pk(1.f));
@@ -118,7 +141,7 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   if (kBack) {
     g.s = mul2(mul2(r, dc), pk(zf.x >= 0.f ? ex : 1.f, zf.y >= 0.f ? ey : 1.f));
     const F2 ro = mul2(r, one);
-    g.i = mul2(ro, d);
+    g.i = fma2(k2n, pk(0.f), mul2(ro, d));
     g.j = mul2(k2, g.i);
     rd = mul2(ro, c);
   } else {
@@ -135,8 +158,8 @@ __device__ __forceinline__ Gates gates(float2 zf, float2 zi, F2 na2) {
   const F2 soft = fma2(p, pk(2.f), pk(fmaxf(-zf.x, 0.f), fmaxf(-zf.y, 0.f)));
   const float2 Lf = un(mul2(soft, na2));
   // the backward's dl L must be 0, not 0 * infinity, where f~ starts a new sequence
-  if (kBack) g.L = pk(fmaxf(Lf.x, -1e30f), fmaxf(Lf.y, -1e30f));
-  const F2 Lc = pk(fmaxf(Lf.x, -127.f), fmaxf(Lf.y, -127.f));
+  if (kBack) g.L = pk(max_nan(Lf.x, -1e30f), max_nan(Lf.y, -1e30f));
+  const F2 Lc = pk(max_nan(Lf.x, -127.f), max_nan(Lf.y, -127.f));
   const float kMagic = 12582912.f;  // 1.5 2^23: rounds to an integer, kept in the low bits
   const F2 t = add2(Lc, pk(kMagic));
   const F2 n = add2(t, pk(-kMagic)), x = fma2(n, pk(-1.f), Lc);

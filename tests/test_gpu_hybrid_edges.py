@@ -1,0 +1,67 @@
+"""Edges of rotary positions, sliding-window attention and the gated linear
+recurrence on the GPU: what is not a number, what overflows, tensors at the
+least alignment that is allowed."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import delta_rule_linear_kron_b200 as kd  # noqa: E402
+from oracle import hybrid as O  # noqa: E402
+from tests.test_gpu_hybrid import glr_inputs, host, run_glr  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    kd.lib()
+
+
+# ---- what is not a number ---------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "i_pre", "f_pre", "a_log", "h0", "dh", "dhT"])
+def test_glr_nan_reaches_what_depends_on_it(name, dtype):
+    """One NaN: the results are NaN where the formulas' are, and everything
+    else is bitwise what it is without it."""
+    t, r = glr_inputs(2, 700, 72, dtype, 11)
+    clean = run_glr(t)
+    at = {1: (37,), 2: (1, 37), 3: (1, 333, 37)}[t[name].dim()]
+    t[name][at] = r[name][at] = float("nan")
+    got, ref = run_glr(t), O.glr(**r)
+    for n, x in got.items():
+        bad = np.isnan(ref[n])
+        assert bad.any() == (n in NAN_IN[name]), n
+        assert np.array_equal(np.isnan(host(x)), bad), n
+        ok = torch.from_numpy(~bad).cuda()
+        assert torch.equal(x[ok], clean[n][ok]), n
+
+
+# what one NaN in an input reaches
+NAN_IN = {"x": {"out", "hT", "di_pre", "df_pre", "da_log"},
+          "i_pre": {"out", "hT", "dx", "di_pre", "df_pre", "da_log"},
+          "f_pre": {"out", "hT", "dx", "di_pre", "df_pre", "da_log", "dh0"},
+          "a_log": {"out", "hT", "dx", "di_pre", "df_pre", "da_log", "dh0"},
+          "h0": {"out", "hT", "df_pre", "da_log"},
+          "dh": {"dx", "di_pre", "df_pre", "da_log", "dh0"}, "dhT": {"dx", "di_pre", "df_pre", "da_log", "dh0"}}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "i_pre", "f_pre", "a_log", "h"])
+def test_glr_decode_nan_reaches_what_depends_on_it(name, dtype):
+    t, _ = glr_inputs(3, 1, 40, dtype, 12)
+    a = {n: t[n][:, 0].contiguous() for n in ("x", "i_pre", "f_pre")}
+    a.update(a_log=t["a_log"], h=t["h0"])
+    clean = {n: x.clone() for n, x in a.items()}
+    want = kd.glr_decode(**clean)
+    at = (slice(None), 7) if name == "a_log" else (1, 7)
+    a[name][at[-1:] if name == "a_log" else at] = float("nan")
+    got = kd.glr_decode(**a)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[at] = True
+    for x, y in ((got, want), (a["h"], clean["h"])):
+        assert torch.equal(torch.isnan(x), bad) and torch.equal(x[~bad], y[~bad])
