@@ -97,7 +97,7 @@ __device__ __forceinline__ void finish(const SwaDecodeArgs& a, size_t b, int h0,
     } else if (!cluster) {
       float* part = a.part + ((b * a.H + h0 + r) * a.splits + blockIdx.x) * (size_t)(D + 2);
       *reinterpret_cast<float2*>(part + 2 + c) = acc;
-      if (c == 0) *reinterpret_cast<float2*>(part) = make_float2(top, sum);
+      if (c == 0) *reinterpret_cast<float2*>(part) = make_float2(top, n ? sum : -1.f);
     } else {
       *reinterpret_cast<float2*>(sh_o + r * D + c) = acc;  // only this thread reads these two of warp 0
     }
@@ -459,6 +459,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecod
 
 // Joins the parts (at most kDecodeParts) of one head: the parts' weights first,
 // in shared memory, then each channel's sum with its loads in flight together.
+// An idle sequence, whose out is zero, is told by its parts' sum of -1: a live
+// one's is not negative, but it may be NaN, which is then the answer.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restrict__ part, int splits,
                                                             T* __restrict__ out) {
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restr
     sum = fmaf(f, w[s], sum);
     acc = fmaf(f, p[(size_t)s * (D + 2) + 2 + threadIdx.x], acc);
   }
-  out[(size_t)blockIdx.x * D + threadIdx.x] = from_f<T>(sum > 0.f ? acc / sum : 0.f);
+  out[(size_t)blockIdx.x * D + threadIdx.x] = from_f<T>(w[0] < 0.f ? 0.f : acc / sum);
 }
 
 int pieces_of(long long slots) { return (int)((slots + 63) / 64 < kDecodeParts ? (slots + 63) / 64 : kDecodeParts); }

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 import delta_rule_linear_kron_b200 as kd  # noqa: E402
 from oracle import hybrid as O  # noqa: E402
-from tests.test_gpu_hybrid import glr_inputs, host, run_glr  # noqa: E402
+from tests.test_gpu_hybrid import draw, glr_inputs, host, run_glr  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -65,3 +65,33 @@ def test_glr_decode_nan_reaches_what_depends_on_it(name, dtype):
     bad[at] = True
     for x, y in ((got, want), (a["h"], clean["h"])):
         assert torch.equal(torch.isnan(x), bad) and torch.equal(x[~bad], y[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [40, 3000, 9000, 40000])
+def test_swa_decode_nan_reaches_what_depends_on_it(window, dtype):
+    """In one CTA, in a cluster's parts and in parts through the workspace: a
+    NaN in a query makes its head NaN, one in a key its group's heads, one in a
+    value its channel of them; an idle sequence's out is zero."""
+    H, Hk, d, sinks = 4, 2, 64, 3
+    rng = np.random.default_rng(window)
+    B = 6
+    q, k, v = (draw(rng, (B, h, d), dtype)[0] for h in (H, Hk, Hk))
+    kc, vc = (draw(rng, (B, window + sinks, Hk, d), dtype)[0] for _ in range(2))
+    pos = torch.tensor([-1, 5, window + sinks + 7, window + sinks, window // 2, 0], device="cuda")
+    want = kd.swa_decode(q, k, v, kc.clone(), vc.clone(), pos, window, sinks)
+    nan = float("nan")
+    q[:3, 1, 9] = nan          # idle, its start, wrapped
+    k[3, 1, 0] = nan           # the new key
+    kc[4, 2, 0, 5] = nan       # a first token's
+    v[5, 0, 11] = nan          # the only value
+    vc[2, 4, 1, 3] = nan
+    got = kd.swa_decode(q, k, v, kc, vc, pos, window, sinks)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[1:3, 1] = True
+    bad[3, 2:] = True
+    bad[4, :2] = True
+    bad[5, :2, 11] = True
+    bad[2, 2:, 3] = True
+    assert torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], want[~bad])
+    assert not got[0].any()
