@@ -49,6 +49,10 @@ constexpr int kDecodeClusterBytes = 2 * (4096 + 128);
 constexpr int kDecodeCtas = 272;
 constexpr int kBatch = 8;  // rows of keys (then of values) in flight per lane
 constexpr float kLog2e = 1.44269504088896f;
+// where running maxima start.  Finite, so that a score of -infinity (a product
+// that overflows, an infinite key) weighs 0 and not NaN also before any other
+// has been seen.
+constexpr float kLowest = -3.402823466e38f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -78,14 +82,14 @@ __device__ __forceinline__ void finish(const SwaDecodeArgs& a, size_t b, int h0,
   // place of warp 0's
   for (int i = tid; i < heads * (D / 2); i += kWarps * 32) {
     const int r = i / (D / 2), c = i % (D / 2) * 2;
-    float top = -INFINITY;
+    float top = kLowest;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w * R + r]);
     float sum = 0.f;
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = sh_m[w * R + r] == -INFINITY ? 0.f : ex2(sh_m[w * R + r] - top);
+      const float f = sh_m[w * R + r] == kLowest ? 0.f : ex2(sh_m[w * R + r] - top);
       const float2 v = *reinterpret_cast<const float2*>(sh_o + (w * R + r) * D + c);
       sum = fmaf(f, sh_l[w * R + r], sum);
       acc = make_float2(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y));
@@ -105,10 +109,10 @@ __device__ __forceinline__ void finish(const SwaDecodeArgs& a, size_t b, int h0,
   if (!cluster) return;
   __syncthreads();  // every thread has read the warps' maxima and sums
   for (int r = tid; r < heads; r += kWarps * 32) {
-    float top = -INFINITY, sum = 0.f;
+    float top = kLowest, sum = 0.f;
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w * R + r]);
     for (int w = 0; w < kWarps; ++w)
-      sum += sh_m[w * R + r] == -INFINITY ? 0.f : ex2(sh_m[w * R + r] - top) * sh_l[w * R + r];
+      sum += sh_m[w * R + r] == kLowest ? 0.f : ex2(sh_m[w * R + r] - top) * sh_l[w * R + r];
     *reinterpret_cast<float2*>(sh_o + R * D + r * 2) = make_float2(top, sum);  // over warp 1's values
   }
   tc::cluster_sync();
@@ -122,7 +126,7 @@ __device__ __forceinline__ void finish(const SwaDecodeArgs& a, size_t b, int h0,
         ms[s] = peer_f2(sh_o + R * D + r * 2, s);
         v[s] = peer_f2(sh_o + r * D + c, s);
       }
-    float top = -INFINITY, sum = 0.f;
+    float top = kLowest, sum = 0.f;
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
@@ -130,7 +134,7 @@ __device__ __forceinline__ void finish(const SwaDecodeArgs& a, size_t b, int h0,
 #pragma unroll
     for (int s = 0; s < 8; ++s)
       if (s < a.splits) {
-        const float f = ms[s].x == -INFINITY ? 0.f : ex2(ms[s].x - top);  // 0 for an empty part
+        const float f = ms[s].x == kLowest ? 0.f : ex2(ms[s].x - top);  // 0 for an empty part
         sum = fmaf(f, ms[s].y, sum);
         acc = make_float2(fmaf(f, v[s].x, acc.x), fmaf(f, v[s].y, acc.y));
       }
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
   float q[GC][E], o[GC][E], m[GC], l[GC];
 #pragma unroll
   for (int g = 0; g < GC; ++g) {
-    m[g] = -INFINITY;
+    m[g] = kLowest;
     l[g] = 0.f;
     P v{};
     if (g0 + g < group) v = *reinterpret_cast<const P*>(static_cast<const T*>(a.q) + (b * a.H + hk * group + g0 + g) * D + c);
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
       }
 #pragma unroll
       for (int w = R::lanes; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      const float f = ex2(m[g] - top);  // top is finite: the warp's first row is in range
+      const float f = ex2(m[g] - top);
       m[g] = top;
       l[g] *= f;
 #pragma unroll
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecod
                                                                (b * a.H + hk * group + g0 + r) * D + c)
                           : 0u;
     }
-  float o[D / 8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  float o[D / 8][4], m0 = kLowest, m1 = kLowest, l0 = 0.f, l1 = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   const float s2 = a.scale * kLog2e;
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecod
       t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
       t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
     }
-    if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {  // both finite: a tile has a key in range
+    if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
       const float f0 = ex2(m0 - t0), f1 = ex2(m1 - t1);
       m0 = t0;
       m1 = t1;
@@ -472,11 +476,11 @@ __global__ void __launch_bounds__(D) swa_decode_join_kernel(const float* __restr
     w[s] = v.y;
   }
   __syncthreads();
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
+  float top = kLowest, sum = 0.f, acc = 0.f;
   for (int s = 0; s < splits; ++s) top = fmaxf(top, m[s]);
 #pragma unroll 8
   for (int s = 0; s < splits; ++s) {
-    const float f = m[s] == -INFINITY ? 0.f : ex2(m[s] - top);  // 0 for an empty part
+    const float f = m[s] == kLowest ? 0.f : ex2(m[s] - top);  // 0 for an empty part
     sum = fmaf(f, w[s], sum);
     acc = fmaf(f, p[(size_t)s * (D + 2) + 2 + threadIdx.x], acc);
   }

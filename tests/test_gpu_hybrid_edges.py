@@ -95,3 +95,42 @@ def test_swa_decode_nan_reaches_what_depends_on_it(window, dtype):
     bad[2, 2:, 3] = True
     assert torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], want[~bad])
     assert not got[0].any()
+
+
+# ---- what overflows -----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [300, 3000, 9000])
+def test_swa_decode_scores_of_minus_infinity_weigh_nothing(window, dtype):
+    """Keys whose scores are -infinity (by an infinite channel, or by overflow)
+    drop out, also where they are all that a warp or a part has seen so far."""
+    H, Hk, d, sinks, B = 4, 2, 64, 2, 2
+    rng = np.random.default_rng(window)
+    n = window + sinks
+    (q, qh), (k, kh), (v, vh) = (draw(rng, (B, h, d), dtype) for h in (H, Hk, Hk))
+    q[..., 0] = qh[..., 0] = 2.0
+    (kc, kch), (vc, vch) = (draw(rng, (B, n, Hk, d), dtype) for _ in range(2))
+    low = torch.finfo(kc.dtype).min
+    gone = np.zeros((B, n), dtype=bool)
+    gone[0, :n - 5] = True                      # all but the last slots
+    gone[1] = rng.random(n) < 0.7
+    pos = torch.tensor([n - 1, n + 3], device="cuda")
+    slots = [O.ring_slot(int(p), window, sinks) for p in pos]
+    for b, s in enumerate(slots):
+        gone[b, s] = False
+        kch[b, s], vch[b, s] = kh[b], vh[b]
+    at = torch.from_numpy(gone).cuda()
+    kc[..., 0][at] = -float("inf")
+    kc[0, : n // 2, :, 0] = low                 # times 2: beyond fp32
+    got = host(kd.swa_decode(q, k, v, kc, vc, pos, window, sinks))
+    for b in range(B):
+        for h in range(H):
+            kk, vv = kch[b, ~gone[b], h // 2], vch[b, ~gone[b], h // 2]
+            x = kk @ qh[b, h] / np.sqrt(d)
+            w = np.exp(x - x.max())
+            w /= w.sum()
+            # scores d + 8 roundings of sum |q||k|, twice; sums of n terms; the output's rounding
+            e = 2 * (d + 8) * 2.0 ** -24 * (np.abs(kk) @ np.abs(qh[b, h])).max() / np.sqrt(d) + (2 * n + 32) * 2.0 ** -24
+            ref, u = w @ vv, 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+            assert (np.abs(got[b, h] - ref) <= e * (w @ np.abs(vv)) + u * np.abs(ref) + 1e-30).all(), (b, h)
