@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
   const size_t b = blockIdx.z;
   const int slots = a.window + a.sinks;
   const long long pos = a.pos[b];
-  const int n = pos < 0 ? 0 : pos + 1 < slots ? (int)pos + 1 : slots;
+  const int n = pos < 0 ? 0 : pos < slots ? (int)pos + 1 : slots;
   const int mine = pos < 0 ? -1 : (int)slot_of(pos, a.window, a.sinks);
   const int per = (n + a.splits - 1) / a.splits;
   const int lo = (int)min((long long)blockIdx.x * per, (long long)n), hi = min((long long)lo + per, (long long)n);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) swa_decode_mma_kernel(SwaDecod
   const size_t b = blockIdx.z;
   const int slots = a.window + a.sinks;
   const long long pos = a.pos[b];
-  const int n = pos < 0 ? 0 : pos + 1 < slots ? (int)pos + 1 : slots;
+  const int n = pos < 0 ? 0 : pos < slots ? (int)pos + 1 : slots;
   const int mine = pos < 0 ? -1 : (int)slot_of(pos, a.window, a.sinks);
   const int per = (n + a.splits - 1) / a.splits;
   const int lo = (int)min((long long)blockIdx.x * per, (long long)n), hi = (int)min((long long)lo + per, (long long)n);

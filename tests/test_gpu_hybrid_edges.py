@@ -134,3 +134,15 @@ def test_swa_decode_scores_of_minus_infinity_weigh_nothing(window, dtype):
             e = 2 * (d + 8) * 2.0 ** -24 * (np.abs(kk) @ np.abs(qh[b, h])).max() / np.sqrt(d) + (2 * n + 32) * 2.0 ** -24
             ref, u = w @ vv, 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
             assert (np.abs(got[b, h] - ref) <= e * (w @ np.abs(vv)) + u * np.abs(ref) + 1e-30).all(), (b, h)
+
+
+def test_swa_decode_last_position_of_64_bits():
+    """The largest position sees a full cache and stores its token."""
+    window, sinks, p = 20, 3, 2 ** 63 - 1
+    q, k, v = torch.randn(1, 2, 32, device="cuda"), torch.randn(1, 1, 32, device="cuda"), torch.randn(1, 1, 32, device="cuda")
+    kc, vc = (torch.randn(1, window + sinks, 1, 32, device="cuda") for _ in range(2))
+    near = sinks + (p - sinks) % window + window * 1000  # a position of the same slot
+    a, b = [kc.clone(), vc.clone()], [kc.clone(), vc.clone()]
+    got = kd.swa_decode(q, k, v, *a, torch.tensor([p], device="cuda"), window, sinks)
+    want = kd.swa_decode(q, k, v, *b, torch.tensor([near], device="cuda"), window, sinks)
+    assert want.any() and torch.equal(got, want) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
