@@ -102,6 +102,12 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   return r;
 }
 
+// -e^{a_log} log2 e of two channels.  Finite where e^{a_log} leaves fp32, so
+// that a gate without a logarithm (1, as for tokens behind the end) stays 1.
+__device__ __forceinline__ F2 exponents(const float* a_log) {
+  return pk(max_nan(-kLog2e * expf(a_log[0]), -3.402823466e38f), max_nan(-kLog2e * expf(a_log[1]), -3.402823466e38f));
+}
+
 struct Gates {
   F2 L;  // log2 f, with kBack
   F2 f;
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(
   }
   F2 na2 = pk(0.f), carry = pk(0.f);
   if (live) {
-    na2 = pk(-kLog2e * expf(a_log[c]), -kLog2e * expf(a_log[c + 1]));
+    na2 = exponents(a_log + c);
     if (h0) carry = *reinterpret_cast<const F2*>(h0 + (size_t)b * D + c);
   }
   __syncthreads();
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 2 : 1) glr_bwd_k
   }
   F2 na2 = pk(0.f), carry = pk(0.f);
   if (live) {
-    na2 = pk(-kLog2e * expf(a_log[c]), -kLog2e * expf(a_log[c + 1]));
+    na2 = exponents(a_log + c);
     if (dhT) carry = *reinterpret_cast<const F2*>(dhT + (size_t)b * D + c);
   }
   const F2 a = mul2(na2, pk(-kLn2));
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const T* __restrict__ x
   const float2 vx = P::f(*reinterpret_cast<const V*>(x + at)), vi = P::f(*reinterpret_cast<const V*>(ip + at));
   const float2 vf = P::f(*reinterpret_cast<const V*>(fp + at));
   const F2 s = *reinterpret_cast<const F2*>(h + at);
-  const Gates g = gates<false>(vf, vi, pk(-kLog2e * expf(a_log[c]), -kLog2e * expf(a_log[c + 1])));
+  const Gates g = gates<false>(vf, vi, exponents(a_log + c));
   const F2 y = fma2(g.f, s, mul2(mul2(mul2(g.w, inv_m(g.w)), g.i), pk(vx.x, vx.y)));
   *reinterpret_cast<F2*>(h + at) = y;
   *reinterpret_cast<V*>(out + at) = P::of(y);

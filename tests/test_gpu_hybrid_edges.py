@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 import delta_rule_linear_kron_b200 as kd  # noqa: E402
 from oracle import hybrid as O  # noqa: E402
-from tests.test_gpu_hybrid import draw, glr_inputs, host, run_glr  # noqa: E402
+from tests.test_gpu_hybrid import check_glr, draw, glr_inputs, host, run_glr  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -146,3 +146,17 @@ def test_swa_decode_last_position_of_64_bits():
     got = kd.swa_decode(q, k, v, *a, torch.tensor([p], device="cuda"), window, sinks)
     want = kd.swa_decode(q, k, v, *b, torch.tensor([near], device="cuda"), window, sinks)
     assert want.any() and torch.equal(got, want) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [70, 128, 1000])
+def test_glr_exponents_beyond_fp32(T, dtype):
+    """e^{a_log} beyond fp32: each gate forgets all, and a sequence that ends
+    inside a chunk of tokens keeps its last state and passes dhT on."""
+    t, r = glr_inputs(2, T, 72, dtype, T)
+    for c, a in ((3, 88.0), (4, 89.0), (40, 120.0), (71, 300.0)):
+        t["a_log"][c] = r["a_log"][c] = a
+    check_glr(t, r, dtype)
+    f = kd.glr_fwd(t["x"], t["i_pre"], t["f_pre"], t["a_log"], t["h0"])[1]
+    t["a_log"][71] = float("inf")
+    assert torch.equal(kd.glr_fwd(t["x"], t["i_pre"], t["f_pre"], t["a_log"], t["h0"])[1], f)
