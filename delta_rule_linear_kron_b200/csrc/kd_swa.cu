@@ -141,7 +141,7 @@ struct KeyTiles {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) swa_fwd_kernel(SwaArgs a) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float *Q = sm, *K = Q + kB * (D + 4), *V = K + kB * (D + 4), *Pt = V + kB * (D + 4);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int q0 = blockIdx.x * kB, h = blockIdx.y, hk = h / (a.H / a.Hk);
@@ -356,7 +356,7 @@ __device__ __forceinline__ void dq_item(const SwaArgs& a, const SwaBwdLayout& L,
 template <int D>
 __global__ void __launch_bounds__(kThreads) swa_bwd_kernel(SwaArgs a, SwaBwdLayout L, int tiles, int far_tiles,
                                                            int key_items, int far_items) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   int i = blockIdx.x;
   if (i < key_items) {
     const int kb = i / tiles;

@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kWarps * 32) swa_decode_kernel(SwaDecodeArgs a
   using R = Row<T, D>;
   constexpr int E = R::E;
   using P = Pack<T, E>;
-  __shared__ float sh_m[kWarps][GC], sh_l[kWarps][GC], sh_o[kWarps][GC][D];
+  __shared__ float sh_m[kWarps][GC], sh_l[kWarps][GC];
+  __shared__ __align__(16) float sh_o[kWarps][GC][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / R::lanes, c = (lane % R::lanes) * E;
   const int group = a.H / a.Hk, chunks = (group + GC - 1) / GC;

@@ -916,7 +916,13 @@ __device__ __forceinline__ void dkv_item(const BwdMaps& m, const SwaArgs& a, con
 #pragma unroll
         for (int e = 0; e < 16; e += 4)
           if (part) *reinterpret_cast<float4*>(part + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        if (plain) store_row<__nv_bfloat16, 16>(dst + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {  // 16 bytes at a time: what dk and dv are aligned to
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = v[e + i];
+          if (plain) store_row<__nv_bfloat16, 8>(dst + c + e, w);
+        }
       }
     } else {  // dk over k, dv over v, which nothing reads any more
       stage_lane<D / 2>(lanes, f, sm + (is_k ? 0 : Cf::TILE), nullptr, tid & 127, c0);

@@ -160,3 +160,103 @@ def test_glr_exponents_beyond_fp32(T, dtype):
     f = kd.glr_fwd(t["x"], t["i_pre"], t["f_pre"], t["a_log"], t["h0"])[1]
     t["a_log"][71] = float("inf")
     assert torch.equal(kd.glr_fwd(t["x"], t["i_pre"], t["f_pre"], t["a_log"], t["h0"])[1], f)
+
+
+# ---- the least alignment ------------------------------------------------------------
+
+
+class Placed:
+    """Tensors 16 bytes behind a 256-byte boundary, the memory around them marked."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def __call__(self, t):
+        n = t.numel() * t.element_size()
+        buf = torch.full((256 + n + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+        at = -buf.data_ptr() % 256 + 16
+        x = buf[at:at + n].view(t.dtype).view(t.shape)
+        x.copy_(t)
+        assert x.data_ptr() % 256 == 16
+        self.bufs.append((buf, at, n))
+        return x
+
+    def untouched(self):
+        return all((b[:a] == 0x5a).all() and (b[a + n:] == 0x5a).all() for b, a, n in self.bufs)
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("f32", 32), ("f32", 128)])
+@pytest.mark.parametrize("window", [40, 300])
+def test_swa_tensors_at_16_bytes(dtype, d, window):
+    """Every tensor of the attention at the least alignment that the C entry
+    points take, first tokens with far queries among them."""
+    B, T, H, Hk, sinks = 2, 700, 4, 2, 70
+    rng = np.random.default_rng(d + window)
+    q, k, v, g = (draw(rng, (B, T, h, d), dtype)[0] for h in (H, Hk, Hk, H))
+    out, lse, ws = kd.swa_fwd(q, k, v, window, sinks, save=True)
+    ref = dict(out=out, lse=lse, **kd.swa_bwd(q, k, v, out, lse, g, window, sinks, fwd_workspace=ws))
+    place, L, s = Placed(), kd.lib(), torch.cuda.current_stream().cuda_stream
+    q, k, v, g = (place(x) for x in (q, k, v, g))
+    got = {n: place(torch.zeros_like(x)) for n, x in ref.items()}
+    dt, nb = (kd.KD_BF16 if dtype == "bf16" else kd.KD_F32), 0 if ws is None else ws.numel()
+    shape = (B, T, H, Hk, d, window, sinks, d ** -0.5, dt)
+    assert L.kron_delta_swa_fwd(ptr(q), ptr(k), ptr(v), ptr(got["out"]), ptr(got["lse"]), *shape, ptr(ws), nb, 1, s) == kd.KD_OK
+    n = kd.swa_workspace_size(kd.KD_SWA_WS_BWD, B, T, H, Hk, d, window, sinks, dt)
+    scratch = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert L.kron_delta_swa_bwd(*(ptr(x) for x in (q, k, v, got["out"], got["lse"], g, got["dq"], got["dk"], got["dv"])),
+                                *shape, ptr(ws), nb, ptr(scratch), n, s) == kd.KD_OK
+    torch.cuda.synchronize()
+    for n, x in ref.items():
+        assert torch.equal(got[n], x), n
+    assert place.untouched()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_other_tensors_at_16_bytes(dtype):
+    """The same of rotary, the one-token step and the fill of its cache, and the
+    recurrence."""
+    rng = np.random.default_rng(1)
+    place = Placed()
+    q, k = (draw(rng, (2, 30, h, 64), dtype)[0] for h in (3, 1))
+    f, _ = kd.rotary_freqs(48)
+    for inter in (False, True):
+        want = kd.rotary_fwd(q, k, f, interleaved=inter)
+        a, b = place(q), place(k)
+        got = kd.rotary_fwd(a, b, place(f), interleaved=inter, out=(a, b))
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    for window in (40, 9000):
+        kc, vc = (draw(rng, (2, window + 2, 1, 64), dtype)[0] for _ in range(2))
+        lens, pos = torch.tensor([30, 11], device="cuda"), torch.tensor([window + 30, 11], device="cuda")
+        ca, cb = place(kc), place(vc)
+        v = draw(rng, (2, 30, 1, 64), dtype)[0]
+        kd.swa_fill(k, v, lens, kc, vc, window, 2)
+        kd.swa_fill(place(k), place(v), place(lens), ca, cb, window, 2)
+        one = [x[:, 7].contiguous() for x in (q, k, v)]
+        want = kd.swa_decode(*one, kc, vc, pos, window, 2)
+        got = kd.swa_decode(*(place(x) for x in one), ca, cb, place(pos), window, 2, out=place(torch.zeros_like(want)))
+        assert torch.equal(got, want) and torch.equal(ca, kc) and torch.equal(cb, vc)
+    t, _ = glr_inputs(2, 150, 72, dtype, 5)
+    want, p = run_glr(t), {n: place(x) for n, x in t.items()}
+    B, T, D, dt = 2, 150, 72, kd.KD_BF16 if dtype == "bf16" else kd.KD_F32
+    L, s = kd.lib(), torch.cuda.current_stream().cuda_stream
+    got = {n: place(torch.zeros_like(x)) for n, x in want.items()}
+    sizes = [kd.glr_workspace_size(kind, B, T, D, dt) for kind in (kd.KD_GLR_WS_SAVE, kd.KD_GLR_WS_BWD)]
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    ins = [ptr(p[n]) for n in ("x", "i_pre", "f_pre", "a_log")]
+    assert L.kron_delta_glr_fwd(*ins, ptr(p["h0"]), ptr(got["out"]), ptr(got["hT"]), B, T, D, dt, ptr(ws[0]), sizes[0], 1,
+                                s) == kd.KD_OK
+    assert L.kron_delta_glr_bwd(*ins, *(ptr(p[n]) for n in ("dh", "dhT")),
+                                *(ptr(got[n]) for n in ("dx", "di_pre", "df_pre", "da_log", "dh0")), B, T, D, dt, ptr(ws[0]),
+                                sizes[0], ptr(ws[1]), sizes[1], s) == kd.KD_OK
+    one = [place(t[n][:, 3].contiguous()) for n in ("x", "i_pre", "f_pre")]
+    h, h2 = place(t["h0"]), t["h0"].clone()
+    assert torch.equal(kd.glr_decode(*one, p["a_log"], h, out=place(torch.zeros_like(one[0]))),
+                       kd.glr_decode(*(x.clone() for x in one), t["a_log"], h2)) and torch.equal(h, h2)
+    torch.cuda.synchronize()
+    for n, x in want.items():
+        assert torch.equal(got[n], x), n
+    assert place.untouched()
