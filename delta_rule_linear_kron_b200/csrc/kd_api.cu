@@ -1066,6 +1066,9 @@ int kron_delta_rotary(const void* q, const void* k, const double* freqs, const l
     KD_TRY(check_apart({{q_out, row * H, "q_out"}}, {{k, row * Hk, "k"}}));
     KD_TRY(check_apart({{k_out, row * Hk, "k_out"}}, {{q, row * H, "q"}, {q_out, row * H, "q_out"}}));
   }
+  // a CTA reads its frequencies and positions while others write rows
+  for (const Span& o : {Span{q_out, row * H, "q_out"}, Span{k_out, row * Hk, "k_out"}})
+    KD_TRY(check_apart({o}, {{freqs, (size_t)rot / 2 * 8, "freqs"}, {pos, (size_t)B * T * 8, "pos"}}));
   KD_TRY(check_stream(stream));
   kd::RotaryArgs a{};
   a.x[0] = q; a.x[1] = k; a.y[0] = q_out; a.y[1] = k_out; a.heads[0] = H; a.heads[1] = Hk;

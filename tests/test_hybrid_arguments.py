@@ -1,0 +1,40 @@
+"""Arguments of the operators beside the delta rules that are refused before
+anything reaches a GPU, or that must be understood (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import delta_rule_linear_kron_b200 as kd
+from delta_rule_linear_kron_b200 import build as kbuild
+
+torch = pytest.importorskip("torch")
+
+
+def at(n):
+    return ctypes.c_void_p(n)   # aligned, never dereferenced: every call here is refused
+
+
+@pytest.fixture(scope="module")
+def L():
+    kbuild.build()
+    return kd.lib()
+
+
+@pytest.mark.parametrize("with_k", [True, False])
+@pytest.mark.parametrize("out", ["qo", "ko"])
+@pytest.mark.parametrize("other", ["freqs", "pos"])
+def test_rotary_outputs_over_frequencies_or_positions_are_refused(L, out, other, with_k):
+    """Also where only the last bytes of either meet the first of the other."""
+    if out == "ko" and not with_k:
+        return
+    a = dict(q=at(1 << 24), k=at(2 << 24), freqs=at(3 << 24), pos=at(4 << 24), qo=at(5 << 24), ko=at(6 << 24), B=2, T=5, H=2,
+             Hk=1, d=64, rot=64, inter=0, inv=0, scale=1.0, dtype=1, stream=None)
+    if not with_k:
+        a.update(k=None, ko=None, Hk=0)
+    size = {"freqs": 32 * 8, "pos": 2 * 5 * 8, "qo": 2 * 5 * 2 * 64 * 2, "ko": 2 * 5 * 64 * 2}
+    base = a[other].value
+    for shift in (0, size[other] - 16, 16 - size[out]):
+        b = dict(a)
+        b[out] = at(base + shift)
+        assert L.kron_delta_rotary(*b.values()) == kd.KD_ERR_INVALID_ARG
+        assert b"overlaps " + other.encode() in L.kron_delta_last_error()
