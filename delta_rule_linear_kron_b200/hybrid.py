@@ -83,8 +83,8 @@ def _streamed(fn):
         if stream is None:
             return fn(*args, **kw)
         import torch
-        first = args[0] if args else next(iter(kw.values()))
-        if first.device != stream.device:
+        first = next((a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
+        if first is not None and first.device != stream.device:
             raise _invalid(f"stream belongs to {stream.device} but the call's tensors are on {first.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)

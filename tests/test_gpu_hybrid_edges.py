@@ -260,3 +260,17 @@ def test_other_tensors_at_16_bytes(dtype):
     for n, x in want.items():
         assert torch.equal(got[n], x), n
     assert place.untouched()
+
+
+# ---- how calls are made ---------------------------------------------------------------
+
+
+def test_arguments_by_name_in_any_order_on_a_stream():
+    q, k = torch.randn(1, 40, 2, 32, device="cuda"), torch.randn(1, 40, 1, 32, device="cuda")
+    f, _ = kd.rotary_freqs(32)
+    want = kd.swa_fwd(q, k, k, 9, 1)[0], kd.rotary_fwd(q, None, f)[0]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = kd.swa_fwd(sinks=1, window=9, v=k, k=k, q=q, stream=s)[0], kd.rotary_fwd(k=None, freqs=f, q=q, stream=s)[0]
+    s.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -38,3 +38,17 @@ def test_rotary_outputs_over_frequencies_or_positions_are_refused(L, out, other,
         b[out] = at(base + shift)
         assert L.kron_delta_rotary(*b.values()) == kd.KD_ERR_INVALID_ARG
         assert b"overlaps " + other.encode() in L.kron_delta_last_error()
+
+
+class StreamOfCuda:
+    device = torch.device("cuda", 0)
+
+
+def test_a_stream_is_held_against_the_first_tensor_wherever_it_stands():
+    """Arguments by name come in any order, numbers before tensors."""
+    x = torch.zeros(1, 4, 2, 32)
+    for call in (lambda **k: kd.swa_fwd(window=3, q=x, k=x, v=x, **k), lambda **k: kd.swa_fwd(x, x, x, 3, **k),
+                 lambda **k: kd.rotary_fwd(interleaved=True, k=None, q=x, freqs=x, **k),
+                 lambda **k: kd.glr_fwd(save=True, h0=None, x=x, i_pre=x, f_pre=x, a_log=x, **k)):
+        with pytest.raises(kd.KronDeltaError, match="stream belongs to cuda:0 but the call's tensors are on cpu"):
+            call(stream=StreamOfCuda())
