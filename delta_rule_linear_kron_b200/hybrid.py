@@ -111,8 +111,20 @@ def _size(n):
     return n
 
 
+def _int32(n, most=2 ** 31 - 1):
+    """n as a C int: ctypes cuts off what is beyond 32 bits, and what is left
+    may be in range."""
+    return max(-2 ** 31, min(n, most))
+
+
+def _window(window):
+    """A window beyond the longest sequence is all of it."""
+    return _int32(window, 2 ** 31 - 1 - KD_SWA_MAX_SINKS)
+
+
 @functools.lru_cache(maxsize=1024)  # of its arguments alone; asked on every decode step
 def swa_workspace_size(kind, B, T, H, Hk, d, window, sinks, dtype) -> int:
+    window, sinks = _int32(window) if kind == KD_SWA_WS_DECODE else _window(window), _int32(sinks)
     return _size(lib().kron_delta_swa_workspace_size(kind, B, T, H, Hk, d, window, sinks, dtype))
 
 
@@ -228,11 +240,13 @@ def _scale(scale, d):
 @_streamed
 def swa_fwd(q, k, v, window, sinks=0, *, scale=None, out=None, save=False, workspace=None, stream=None):
     """Causal attention where query t sees key j when j <= t and (t - j < window
-    or j < sinks).  q [B,T,H,d], k, v [B,T,Hk,d] (bf16 or fp32), H a multiple of
-    Hk; scale defaults to 1/sqrt(d).  Returns (out [B,T,H,d], lse [B,T,H] fp32,
+    or j < sinks); window >= T is plain causal attention.  q [B,T,H,d], k, v
+    [B,T,Hk,d] (bf16 or fp32), H a multiple of Hk, finite in every row, padding
+    included; scale defaults to 1/sqrt(d).  Returns (out [B,T,H,d], lse [B,T,H] fp32,
     workspace or None); pass all three (save=True) to swa_bwd."""
     import torch
     B, T, H, Hk, d, dt, dev, ptrs = _swa_inputs(q, k, v)
+    window, sinks = _window(window), _int32(sinks)
     out, p_out = _out(out, q, dev)
     lse = q.new_empty((B, T, H), dtype=torch.float32)
     if save and workspace is None:
@@ -248,6 +262,7 @@ def swa_bwd(q, k, v, out, lse, dO, window, sinks=0, *, scale=None, fwd_workspace
     Returns dict dq, dk, dv (summed in a fixed order: bitwise reproducible)."""
     import torch
     B, T, H, Hk, d, dt, dev, ptrs = _swa_inputs(q, k, v)
+    window, sinks = _window(window), _int32(sinks)
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
     if workspace is None:
         workspace = _alloc_ws(swa_workspace_size(KD_SWA_WS_BWD, B, T, H, Hk, d, window, sinks, dt), q.device)

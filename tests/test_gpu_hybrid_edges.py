@@ -274,3 +274,14 @@ def test_arguments_by_name_in_any_order_on_a_stream():
     got = kd.swa_fwd(sinks=1, window=9, v=k, k=k, q=q, stream=s)[0], kd.rotary_fwd(k=None, freqs=f, q=q, stream=s)[0]
     s.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_swa_windows_beyond_32_bits():
+    """Plain causal attention, forward and backward, with first tokens as without."""
+    q, k, g = (torch.randn(1, 300, h, 32, device="cuda") for h in (2, 1, 2))
+    want = kd.swa_fwd(q, k, k, 300, save=True)
+    grads = kd.swa_bwd(q, k, k, *want[:2], g, 300, fwd_workspace=want[2])
+    for window in (2 ** 31, 2 ** 32 + 3, 2 ** 63 - 1):
+        got = kd.swa_fwd(q, k, k, window, 1, save=True)
+        r = kd.swa_bwd(q, k, k, *got[:2], g, window, 1, fwd_workspace=got[2])
+        assert torch.equal(got[0], want[0]) and all(torch.equal(r[n], x) for n, x in grads.items())

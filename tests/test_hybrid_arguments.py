@@ -52,3 +52,19 @@ def test_a_stream_is_held_against_the_first_tensor_wherever_it_stands():
                  lambda **k: kd.glr_fwd(save=True, h0=None, x=x, i_pre=x, f_pre=x, a_log=x, **k)):
         with pytest.raises(kd.KronDeltaError, match="stream belongs to cuda:0 but the call's tensors are on cpu"):
             call(stream=StreamOfCuda())
+
+
+def test_a_window_beyond_32_bits_is_all_of_the_sequence():
+    """Not its lowest 32 bits; what a call has to refuse stays refused."""
+    def size(kind, window, sinks=2):
+        return kd.swa_workspace_size(kind, 2, 100, 4, 2, 64, window, sinks, kd.KD_BF16)
+    for kind in (kd.KD_SWA_WS_SAVE, kd.KD_SWA_WS_BWD):
+        for window in (2 ** 31 - 128, 2 ** 31, 2 ** 32 + 8, 2 ** 63 - 1):
+            assert size(kind, window) == size(kind, 100)
+    assert size(kd.KD_SWA_WS_BWD, 8) > size(kd.KD_SWA_WS_BWD, 100)  # a narrow window's first tokens have parts
+    for window, sinks in ((-2 ** 32 + 8, 2), (0, 2), (8, 2 ** 32 + 2), (8, -2 ** 32 + 2), (8, 2 ** 31)):
+        for kind in (kd.KD_SWA_WS_SAVE, kd.KD_SWA_WS_BWD, kd.KD_SWA_WS_DECODE):
+            with pytest.raises(kd.KronDeltaError, match="must be"):
+                size(kind, window, sinks)
+    with pytest.raises(kd.KronDeltaError, match="window < 2"):  # a cache of so many slots
+        size(kd.KD_SWA_WS_DECODE, 2 ** 32 + 8)
