@@ -8,9 +8,9 @@
 //   dx = g m i,  di~ = g m x i (1 - i),  dl = g (f h_{t-1} - i x f^2 / m)
 //   df~ = dl a sigma(-f~),  da_log = sum dl l
 //
-// HBM-bound in bytes (8 per element forward, 14.25 backward with bf16), but
-// close to the rates of instructions and of the special function unit too, so
-// nothing may be computed twice.  One pass: a cluster of C CTAs takes 64
+// By its bytes (8.06 per element forward and 14.06 backward with bf16, the saved
+// states among them) a stream through HBM, but with enough arithmetic per element
+// that nothing may be computed twice.  One pass: a cluster of C CTAs takes 64
 // channels and C consecutive chunks of 64 tokens at a time.  TMA brings the
 // chunks' tiles a step ahead.  A warp holds 8 tokens, a lane 2 channels (one
 // f32x2 register pair, so that most of the arithmetic is two channels an
@@ -18,11 +18,15 @@
 // (prod f, h) pairs combine through shared memory and the CTAs' through
 // distributed shared memory, and the thread then adds its start state's part,
 // from registers.  The chain along the sequence is only ceil(T / 64C) cluster
-// exchanges long.  B1 T16384 D2048 bf16, with the states saved: forward 113 us
-// (285 MB, 2.5 TB/s), backward 186 us (487 MB, 2.6 TB/s); one step of 256 x 2048
-// 7.2 us.  What bounds them is the issue of 115 and 186 instructions per pair of
-// channels and token (54 and 52% of the issue slots, 16 warps per SM; 8 of them
-// on the special function unit, 30 and 18%).
+// exchanges long.  B1 T16384 D2048, with the states saved: bf16 forward 114 us
+// (271 MB, 2.4 TB/s), backward 184 us (472 MB, 2.6 TB/s); fp32 114 us (539 MB,
+// 4.7 TB/s) and 357 us (941 MB, 2.6 TB/s: its tiles leave room for one CTA per
+// SM); one step of 256 x 2048 7.2 us.  No unit is at its rate: 110 and 188
+// instructions per pair of channels and token take 53 and 52% of the issue slots
+// (8 of them on the special function unit, 31 and 18%), HBM is at 26 and 28%.
+// What bounds them is latency: 13 warps per SM (256 CTAs leave 40 of the 148 SMs
+// with one CTA) of which a scheduler finds one ready per cycle, in chains of
+// dependent arithmetic, of waits for tiles, states and the exchange.
 //
 // Accuracy: the state's error builds up over 1 / (1 - f) steps, so f must not
 // carry a bias.  With L = log2 f = n + r, |r| <= 1/2, and q = 2^r - 1 by a
@@ -559,9 +563,9 @@ __global__ void __launch_bounds__(128) glr_decode_kernel(const T* __restrict__ x
 
 // CTAs of a cluster (chunks taken at a time): enough CTAs for all of 148 SMs,
 // as far as the sequence has chunks, and at most the portable 8.  Forward and
-// backward in us, clusters of 8 and of 1: 113 and 433, 186 and 786 (B1 T16384
+// backward in us, clusters of 8 and of 1: 114 and 426, 184 and 826 (B1 T16384
 // D2048: 256 CTAs and 32); where D and B make 256 CTAs by themselves, clusters
-// of 1 and of 2: 179 and 189, 317 and 328 (B8 T4096 D2048).
+// of 1 and of 2: 175 and 187, 323 and 337 (B8 T4096 D2048).
 int cluster_size(const GlrArgs& a, int NC) {
   const long long lanes = (long long)((a.D + kChans - 1) / kChans) * a.B;
   int C = 1;

@@ -9,13 +9,15 @@
 // (at position 2^20 an fp32 product is off by 0.06 rad), and only the fraction
 // goes to fp32's sincospi.
 //
-// HBM-bound: every element is read and written once.  One sine and cosine
-// serve all heads of a token, so a CTA takes whole tokens: it fills a table of
-// its tokens' rot/2 pairs in shared memory, then moves the heads' rows as
-// vectors, x threads to a row and y rows at a time.  16384 tokens of 16 + 4
-// heads of 128 bf16 (168 MB): 33 to 35 us, 5 TB/s; with two and four rows in
-// flight per thread 53 and 68 us (more registers, fewer CTAs), with a thread's
-// first row loaded ahead of the table 43.
+// Every element is read and written once.  One sine and cosine serve all heads
+// of a token, so a CTA takes whole tokens: it fills a table of its tokens' rot/2
+// pairs in shared memory, then moves the heads' rows as vectors, x threads to a
+// row and y rows at a time.  16384 tokens of 16 + 4 heads of 128 bf16 (168 MB):
+// 33 to 35 us, 5 TB/s.  What bounds it is the table's reads: the shared-memory
+// pipe is at 73% of its rate, three quarters of that the vectors of a row's
+// threads meeting in the same banks.  With two and four rows in flight per
+// thread 53 and 68 us (more registers, fewer CTAs), with a thread's first row
+// loaded ahead of the table 43.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 

@@ -9,9 +9,11 @@
 //             dq = scale dS k,  dk = scale dS^T q,  dv = p^T dO
 //
 // 64 queries x 64 keys at a time from shared memory, 256 threads with 4 x 4
-// tiles of the products; bound by shared-memory loads and fp32 FMA.  B2 T4096 H8
-// window 512: forward 0.74, 0.39, 0.24 ms and backward 2.2, 1.08, 0.63 ms for
-// d = 128, 64, 32 (22 and 26 TFLOP/s at d = 128).  Tiles with no visible pair
+// tiles of the products; bound by shared-memory loads and fp32 FMA (at d = 128
+// 65 and 69% of the L1's rate, 56 and 57% of the issue slots, with one CTA per SM
+// that does not load while it computes).  B2 T4096 H8 window 512, in ms: forward
+// 0.65, 0.35, 0.22 and backward 2.0, 0.98, 0.58 for d = 128, 64, 32 (25 and 29
+// TFLOP/s at d = 128).  Tiles with no visible pair
 // are not visited.  The gradients recompute p from lse, dk and dv by key tile
 // and dq by query tile, so that
 // every sum has a fixed order and needs no atomics.

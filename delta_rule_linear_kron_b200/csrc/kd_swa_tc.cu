@@ -4,7 +4,10 @@
 // zeros, never stored (B2 T4096 H8 window 512: forward 44 and backward 99 us;
 // on CUDA cores, which have no use for the zeros, 228 and 626).
 //
-// Times are at H16 Hk16 T16384 d128 window 2048, in us.
+// Times are at H16 Hk16 T16384 d128 window 2048, in us, of single calls at the
+// full 1.965 GHz.  Calls back to back reach the power limit (1.67 GHz), where a
+// training step with 4 first tokens takes 1,450 in place of 1,309: forward 363
+// (317), delta 42 (39), backward 1,026 (899), first tokens' sums 9, and gaps.
 //
 // Every kernel has 19 warps: four groups of four (thread = TMEM lane = tile row,
 // a part of its columns) for the elementwise work, which bounds these kernels
@@ -20,7 +23,7 @@
 // from the same shared-memory tile that the score product reads K-major, so no
 // tile is stored twice or transposed.
 //
-// Forward: 293, 0.88 PFLOP/s over the visible pairs.  256 queries of one head
+// Forward: 295, 0.87 PFLOP/s over the visible pairs.  256 queries of one head
 // per CTA, a group to each 128.  Scores are read into registers at once and
 // their TMEM columns given back for the next tile's, p goes to shared memory as
 // the next product's A operand; per tile pair 32 MMAs (2,200 cycles) stand
@@ -33,7 +36,7 @@
 // maximum has grown by more than 2^8 over the one its sums refer to (then p <=
 // 2^8, still exact enough in bf16, whose precision does not depend on the size).
 //
-// Backward: 855, 1.05 PFLOP/s over the visible pairs' seven products; bound by
+// Backward: 852, 1.06 PFLOP/s over the visible pairs' seven products; bound by
 // each tile's chain of waits, exponential and conversions (2,600 cycles for dq,
 // 3,600 for dk, dv, against 1,750 and 2,500 of shared-memory traffic), and by 5
 // us of start and end of each CTA.  p is recomputed from the saved lse.  dk, dv:

@@ -548,7 +548,8 @@ KD_API size_t kron_delta_swa_workspace_size(int kind, int B, int T, int H, int H
  *   q, out : [B,T,H,d] (dtype).  k, v : [B,T,Hk,d] (dtype); H a multiple of
  *         Hk, query head h reads key head h / (H / Hk).
  *   lse : [B,T,H] fp32, natural logarithm.
- *   window >= 1;  0 <= sinks <= KD_SWA_MAX_SINKS;  scale finite, > 0.
+ *   1 <= window < 2^31 - KD_SWA_MAX_SINKS;  0 <= sinks <= KD_SWA_MAX_SINKS;
+ *         scale finite, > 0.
  *   workspace : with save = 1 at least
  *         kron_delta_swa_workspace_size(KD_SWA_WS_SAVE, ...) bytes, 256-byte
  *         aligned (the rounding of the bf16 output, which the backward adds
@@ -592,6 +593,7 @@ KD_API int kron_delta_swa_bwd(const void *q, const void *k, const void *v, const
  *   [B,sinks+window,Hk,d] (dtype).
  *   pos : the new token's position [B], 64-bit integers.  A sequence with
  *         pos < 0 is idle: its cache is left as it was and its out is zero.
+ *         (Only then: a NaN that a live sequence sees is in its out.)
  *   workspace : at least kron_delta_swa_workspace_size(KD_SWA_WS_DECODE, ...)
  *         bytes, 256-byte aligned (NULL where that is 0).
  * An output (the caches too) that overlaps an input or another output is
@@ -627,7 +629,8 @@ KD_API size_t kron_delta_glr_workspace_size(int kind, int B, int T, int D, int d
  *     f_t = sigma(f_pre_t)^a,   h_t = f_t h_{t-1} + sqrt(1 - f_t^2) sigma(i_pre_t) x_t
  * The write is scaled by sqrt(1 - f^2), which keeps the state's variance at
  * the input's.  f_pre = -infinity (or the type's lowest value) gives f = 0 and
- * so starts a new sequence at that token.
+ * so starts a new sequence at that token.  A NaN in an input reaches every
+ * result that depends on it; e^{a_log} beyond fp32 counts as its largest value.
  *   x, i_pre, f_pre, out : [B,T,D] (dtype); out is h_t.
  *   a_log : [D] fp32.  h0 : [B,D] fp32 or NULL (zero).  hT : [B,D] fp32 or NULL.
  *   D a multiple of 8.  The state, and every sum, is fp32.
