@@ -978,8 +978,8 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 // forward's rounding of p reaches it through delta), 1.52 at 9, 1.45 at 129,
 // and by chance up to 1.84 where a batch has only some ten rows; from some
 // hundred keys on 1.43, which is what rounding dS alone costs.  With the finer
-// ones 1.00 throughout.  They cost 144 -> 175 us forward and 376 -> 469
-// backward at T16384 H16 Hk4 d128 window 252, 10 -> 11.5 and 11 -> 13 at T200.
+// ones 1.00 throughout.  They cost 112 -> 137 us forward and 271 -> 346 backward
+// at T16384 H16 Hk4 d128 window 252, 11 -> 13 and 13 -> 15 at T200 Hk16.
 constexpr int kFineKeys = 256;
 bool fine(const SwaArgs& a) {
   return (a.window + a.sinks < a.T ? a.window + a.sinks : a.T) <= kFineKeys;  // window, sinks <= T
