@@ -128,3 +128,89 @@ def test_swa_decode_long_caches(B, H, Hk, window, sinks, d, dtype):
         if dtype == "bf16":
             e = e + 2.0 ** -16
         assert bool(((got[b].view(Hk, G, d) - ref).abs() <= e * mag + ROUND[dtype] * ref.abs() + 1e-30).all()), b
+
+
+# ---- offsets that pass 32 bits ------------------------------------------------------------
+
+
+@pytest.fixture
+def memory():
+    yield
+    torch.cuda.empty_cache()
+
+
+FAR = 2 ** 20  # 2^20 tokens of 16 heads of 128: 2^31 elements
+
+
+def randn(*shape, dtype=torch.bfloat16, seed=0):
+    return torch.randn(*shape, device="cuda", dtype=dtype, generator=torch.Generator("cuda").manual_seed(seed))
+
+
+@pytest.mark.parametrize("dtype,Hk", [("bf16", 16), ("f32", 2)])
+def test_swa_offsets_beyond_32_bits(memory, dtype, Hk):
+    """The rows behind 2^31 elements are bitwise those of a sequence that starts
+    256 tokens before them (a window of 64, the same tiles)."""
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v, g = (randn(1, FAR + 300, h, 128, dtype=t, seed=i) for i, h in enumerate((16, Hk, Hk, 16)))
+
+    def both(q, k, v, g):
+        out, lse, ws = kd.swa_fwd(q, k, v, 64, save=True)
+        return dict(out=out, lse=lse, **kd.swa_bwd(q, k, v, out, lse, g, 64, fwd_workspace=ws))
+    want = both(*(x[:, FAR - 256:].contiguous() for x in (q, k, v, g)))
+    got = both(q, k, v, g)
+    for n, x in want.items():
+        assert torch.isfinite(x[:, 256:]).all() and torch.equal(got[n][:, FAR:], x[:, 256:]), n
+    kd.device_status()
+
+
+def test_rotary_and_glr_offsets_beyond_32_bits(memory):
+    q = randn(1, FAR + 300, 16, 128)
+    f, _ = kd.rotary_freqs(128)
+    pos = torch.arange(FAR, FAR + 300, device="cuda")[None]
+    got = kd.rotary_fwd(q, None, f, out=(q, None))[0][:, FAR:].clone()
+    q = randn(1, FAR + 300, 16, 128)[:, FAR:].contiguous()
+    assert torch.equal(got, kd.rotary_fwd(q, None, f, pos)[0])
+    del q
+    x, i, z = (randn(1, FAR + 300, 2048, seed=s) for s in (1, 2, 3))
+    z[:, FAR - 512] = -float("inf")  # a new sequence, at the start of a step of its cluster
+    a, g = torch.zeros(2048, device="cuda"), randn(1, FAR + 300, 2048, seed=4)
+
+    def both(x, i, z, g):
+        out, hT, ws = kd.glr_fwd(x, i, z, a, save=True)
+        r = kd.glr_bwd(x, i, z, a, None, g, fwd_workspace=ws)
+        return dict(out=out, hT=hT[:, None].expand(1, 812, 2048), dx=r["dx"], di_pre=r["di_pre"], df_pre=r["df_pre"])
+    want = both(*(y[:, FAR - 512:].contiguous() for y in (x, i, z, g)))
+    got = both(x, i, z, g)
+    for n, y in want.items():
+        assert torch.isfinite(y).all() and torch.equal(got[n][:, -300:], y[:, -300:]), n
+    kd.device_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_swa_decode_offsets_beyond_32_bits(memory, dtype):
+    """Caches on both sides of 2^31 elements: their fill, and full ones whose
+    first and last slots alone have weight."""
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    B, Hk, d, window = 3, 8, 128, 2 ** 20 + 7  # 2^30 elements and some to a sequence
+    kc, vc = (torch.zeros(B, window, Hk, d, dtype=t, device="cuda") for _ in range(2))
+    k, v = randn(B, 40, Hk, d, dtype=t, seed=1), randn(B, 40, Hk, d, dtype=t, seed=2)
+    q1, k1, v1 = (randn(B, Hk, d, dtype=t, seed=s) for s in (3, 4, 5))
+    small = [torch.zeros(B, 64, Hk, d, dtype=t, device="cuda") for _ in range(2)]
+    lens = torch.full((B,), 40, device="cuda")
+    kd.swa_fill(k, v, lens, kc, vc, window)
+    kd.swa_fill(k, v, lens, *small, 64)
+    assert torch.equal(kc[:, :64], small[0]) and torch.equal(vc[:, :64], small[1]) and not kc[:, 64:].any()
+    # full caches: 40 keys at the front, 41 at the end, the last one the new token; all the others weigh nothing
+    kc[:, 40:, :, 0] = -float("inf")
+    kc[:, -41:-1], vc[:, -41:-1] = k, v
+    q1[..., 0] = 1.0
+    pos = torch.full((B,), window - 1, device="cuda")
+    got = kd.swa_decode(q1, k1, v1, kc, vc, pos, window).double()
+    assert torch.equal(kc[:, -1], k1) and torch.equal(vc[:, -1], v1)
+    kk, vv = (torch.cat((x, x, y[:, None]), 1).double().transpose(1, 2) for x, y in ((k, k1), (v, v1)))  # [B, Hk, 81, d]
+    p = torch.softmax((kk @ q1.double()[..., None])[..., 0] * d ** -0.5, -1)
+    ref, mag = (p[..., None, :] @ vv)[..., 0, :], (p[..., None, :] @ vv.abs())[..., 0, :]
+    # scores of d + 8 roundings of their magnitudes, twice; 81 keys; weights in two bf16 parts; all but those taken twice
+    worst = (kk.abs() @ q1.double().abs()[..., None])[..., 0].amax(-1)[..., None] * d ** -0.5
+    e = 2 * (2 * (d + 8) * 2.0 ** -24 * worst + (2 * 81 + 32) * 2.0 ** -24) + 2.0 ** -16
+    assert bool(((got - ref).abs() <= e * mag + ROUND[dtype] * ref.abs()).all())
