@@ -14,10 +14,10 @@
 // pairs in shared memory, then moves the heads' rows as vectors, x threads to a
 // row and y rows at a time.  16384 tokens of 16 + 4 heads of 128 bf16 (168 MB):
 // 33 to 35 us, 5 TB/s.  What bounds it is the table's reads: the shared-memory
-// pipe is at 73% of its rate, three quarters of that the vectors of a row's
-// threads meeting in the same banks.  With two and four rows in flight per
-// thread 53 and 68 us (more registers, fewer CTAs), with a thread's first row
-// loaded ahead of the table 43.
+// pipe is at 73% of its rate, three quarters of that for the table, whose vectors
+// for a row's threads lie in the same banks and are read one after another.  With
+// two and four rows in flight per thread 53 and 68 us (more registers, fewer
+// CTAs), with a thread's first row loaded ahead of the table 43.
 #include "kd_hybrid.h"
 #include "kd_rows.cuh"
 
